@@ -102,6 +102,11 @@ def lib() -> ctypes.CDLL:
         L.gdn_qkv_conv_update.argtypes = [vp, fp, fp, vp, ip, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                           vp, vp, vp, ctypes.POINTER(GdnParams), vp]
         L.gdn_qkv_conv_update.restype = ctypes.c_int
+        L.gdn_chunk_bwd.argtypes = [vp, vp, vp, fp, fp, fp, fp, fp, vp, fp, ip, ctypes.c_int32, ctypes.c_int64,
+                                    vp, vp, vp, vp, vp, fp, vp, ctypes.c_int64, ctypes.POINTER(GdnParams), vp]
+        L.gdn_chunk_bwd.restype = ctypes.c_int
+        L.gdn_chunk_bwd_workspace.argtypes = [ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(GdnParams)]
+        L.gdn_chunk_bwd_workspace.restype = ctypes.c_int64
         L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_int64, vp]
         L.gdn_selftest_wait_timeout.restype = ctypes.c_int
         L.gdn_device_status.argtypes = [vp]
@@ -405,3 +410,52 @@ def qkv_conv_update(mixed_qkv, weight, conv_state, nqk, nv, dk, dv, bias=None, s
     if check and rc != GDN_OK:
         raise GdnError(rc, "gdn_qkv_conv_update")
     return q, k, v
+
+
+def chunk_bwd_workspace(q, v, cu_seqlens=None, num_seqs=None) -> int:
+    """Bytes of workspace that ``chunk_bwd`` needs for these tensors (``gdn_chunk_bwd_workspace``)."""
+    import torch
+    n = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
+    p = make_params(q.shape[1], v.shape[1], q.shape[2], v.shape[2], q.dtype == torch.bfloat16)
+    need = lib().gdn_chunk_bwd_workspace(int(n), int(q.shape[0]), ctypes.byref(p))
+    if need < 0:
+        raise GdnError(need, "gdn_chunk_bwd_workspace")
+    return need
+
+
+def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu_seqlens=None, num_seqs=None,
+              A_log=None, dt_bias=None, dq=None, dk=None, dv=None, dg=None, dbeta=None, d_initial_state=None,
+              output_d_initial_state=None, qk_l2norm=True, scale=0.0, workspace=None, stream=None, check=True):
+    """Gradients of ``chunk_fwd`` (``gdn_chunk_bwd``); the inputs are those of the forward call.
+
+    dout [T, Nv, Dv] (dtype of v), d_final_state [N, Nv, Dk, Dv] fp32 or None (zeros).
+    With A_log, dt_bias the g, beta arguments are the raw projections a, b, and dg,
+    dbeta are the gradients of the gate formed from them (then ``gate_bwd``).
+    ``workspace``: a CUDA tensor of at least ``chunk_bwd_workspace`` bytes, allocated
+    when not given.  Returns ``(dq, dk, dv, dg, dbeta, d_initial_state)``, the token
+    gradients in the dtype of q; d_initial_state is None unless an initial state was
+    given or it was asked for.
+    """
+    import torch
+    T, nqk, dk_ = q.shape
+    nv, dv_ = v.shape[1], v.shape[2]
+    n = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    dg = torch.empty((T, nv), dtype=q.dtype, device=q.device) if dg is None else dg
+    dbeta = torch.empty((T, nv), dtype=q.dtype, device=q.device) if dbeta is None else dbeta
+    if d_initial_state is None and (initial_state is not None if output_d_initial_state is None
+                                    else output_d_initial_state):
+        d_initial_state = torch.empty((n, nv, dk_, dv_), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(chunk_bwd_workspace(q, v, cu_seqlens, num_seqs), dtype=torch.uint8, device=q.device)
+    p = make_params(nqk, nv, dk_, dv_, q.dtype == torch.bfloat16, qk_l2norm, scale)
+    rc = lib().gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(A_log), _ptr(dt_bias),
+                             _ptr(initial_state), _ptr(dout), _ptr(d_final_state), _ptr(cu_seqlens), int(n), int(T),
+                             _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(d_initial_state),
+                             _ptr(workspace), int(workspace.numel() * workspace.element_size()), ctypes.byref(p),
+                             _stream(stream))
+    if check and rc != GDN_OK:
+        raise GdnError(rc, "gdn_chunk_bwd")
+    return dq, dk, dv, dg, dbeta, d_initial_state

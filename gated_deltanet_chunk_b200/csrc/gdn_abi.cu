@@ -485,6 +485,69 @@ GDN_API int gdn_qkv_conv_update(const void* mixed_qkv, const float* weight, cons
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+GDN_API int64_t gdn_chunk_bwd_workspace(int32_t num_seqs, int64_t total_tokens, const gdn_params_t* p) {
+  const int rc = check_params(p);
+  if (rc) return rc;
+  if (num_seqs < 1 || num_seqs > 65535) return GDN_ERR_SHAPE;
+  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31)) return GDN_ERR_SHAPE;
+  return gdn::chunk_bwd_workspace(total_tokens, num_seqs, p->num_v_heads, p->head_k_dim, p->head_v_dim);
+}
+
+GDN_API int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                          const float* A_log, const float* dt_bias, const float* initial_state, const void* dout,
+                          const float* d_final_state, const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                          void* dq, void* dk_, void* dv_, void* dg, void* dbeta, float* d_initial_state, void* workspace,
+                          int64_t workspace_bytes, const gdn_params_t* p, void* cuda_stream) {
+  const int64_t need = gdn_chunk_bwd_workspace(num_seqs, total_tokens, p);
+  if (need < 0) return (int)need;
+  if (p->kernel == GDN_KERNEL_TC) return GDN_ERR_SHAPE;  // there is no choice of kernel here
+  if ((A_log == nullptr) != (dt_bias == nullptr)) return GDN_ERR_NULL;
+  if (total_tokens != 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk_ || !dv_ || !dg || !dbeta || !workspace))
+    return GDN_ERR_NULL;
+  if (workspace_bytes < need) return GDN_ERR_SHAPE;
+  if (!cu_seqlens && total_tokens % num_seqs != 0) return GDN_ERR_SHAPE;
+  const void* ptrs[] = {q, k, v, g, beta, initial_state, dout, d_final_state, cu_seqlens,
+                        dq, dk_, dv_, dg, dbeta, d_initial_state, workspace};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return GDN_ERR_ALIGN;
+  if ((A_log && !aligned4(A_log)) || (dt_bias && !aligned4(dt_bias))) return GDN_ERR_ALIGN;
+  const size_t T = (size_t)total_tokens, N = (size_t)num_seqs, esz = p->io_dtype == GDN_DTYPE_BF16 ? 2 : 4;
+  const size_t dk = p->head_k_dim, dv = p->head_v_dim, nqk = p->num_qk_heads, nv = p->num_v_heads;
+  const size_t state = N * nv * dk * dv * 4;
+  auto opt = [](const void* ptr, size_t bytes) { return ptr ? range_of(ptr, bytes) : Range{0, 0}; };
+  const Range in[] = {range_of(q, T * nqk * dk * esz), range_of(k, T * nqk * dk * esz), range_of(v, T * nv * dv * esz),
+                      range_of(g, T * nv * 4), range_of(beta, T * nv * 4), opt(A_log, nv * 4), opt(dt_bias, nv * 4),
+                      opt(initial_state, state), range_of(dout, T * nv * dv * esz), opt(d_final_state, state),
+                      opt(cu_seqlens, (N + 1) * 4)};
+  const Range out[] = {range_of(dq, T * nqk * dk * esz), range_of(dk_, T * nqk * dk * esz), range_of(dv_, T * nv * dv * esz),
+                       range_of(dg, T * nv * esz), range_of(dbeta, T * nv * esz), opt(d_initial_state, state),
+                       range_of(workspace, (size_t)need)};
+  const int nout = (int)(sizeof(out) / sizeof(out[0]));
+  for (int i = 0; i < nout; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return GDN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return GDN_ERR_ALIAS;
+  }
+  const int rc = check_device();
+  if (rc) return rc;
+  gdn::BwdArgs a{};
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.A_log = A_log; a.dt_bias = dt_bias; a.dout = dout;
+  a.s0 = initial_state; a.ds_final = d_final_state; a.cu = cu_seqlens;
+  a.dq = dq; a.dk = dk_; a.dv_out = dv_; a.dg = dg; a.dbeta = dbeta; a.ds0 = d_initial_state;
+  a.ws = static_cast<float*>(workspace);
+  a.uniform_len = cu_seqlens ? 0 : (int32_t)(total_tokens / num_seqs);
+  a.num_seqs = num_seqs; a.total_tokens = total_tokens;
+  a.status = status_word();
+  if (!a.status) return GDN_ERR_CUDA;
+  a.nqk = p->num_qk_heads; a.nv = p->num_v_heads;
+  a.qk_l2norm = p->qk_l2norm ? 1 : 0;
+  a.scale = resolve_scale(p);
+  const cudaError_t e = gdn::launch_chunk_bwd(a, p->head_k_dim, p->head_v_dim, p->io_dtype == GDN_DTYPE_BF16,
+                                              static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 GDN_API int gdn_selftest_wait_timeout(int64_t limit_us, void* cuda_stream) {
   if (limit_us < 1 || limit_us > 2000000) return GDN_ERR_SHAPE;
   const int rc = check_device();

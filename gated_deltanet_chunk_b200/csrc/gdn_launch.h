@@ -29,4 +29,8 @@ cudaError_t launch_gated_rmsnorm(const void* o, const void* z, const float* w, f
 cudaError_t launch_conv_fwd(const ConvArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_conv_update(const ConvArgs& a, int io_bf16, cudaStream_t s);
 
+// Gradients of the chunked forward; dk, dv in {64,128}.  Workspace bytes and launch.
+int64_t chunk_bwd_workspace(int64_t total_tokens, int num_seqs, int nv, int dk, int dv);
+cudaError_t launch_chunk_bwd(const BwdArgs& a, int dk, int dv, int io_bf16, cudaStream_t s);
+
 }  // namespace gdn

@@ -368,6 +368,51 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
                         const gdn_params_t *p, void *cuda_stream);
 
 /*
+ * gdn_chunk_bwd -- gradients of gdn_chunk_fwd: given dout and, optionally, the
+ * gradient of the final states, the gradients of q, k, v, g, beta and of the
+ * initial states.  The forward quantities that it needs are formed again from the
+ * inputs, so nothing has to be kept from the forward call but those.
+ *
+ *   q, k, v, g, beta, initial_state, cu_seqlens, num_seqs, total_tokens
+ *                    as gdn_chunk_fwd had them.  g is any finite value, as for
+ *                    GDN_KERNEL_SIMT.
+ *   A_log, dt_bias   [Nv] fp32, or both NULL.  Given, g and beta hold the raw
+ *                    projections a and b, as in gdn_chunk_fwd_gated; dg and dbeta
+ *                    are still the gradients of the gate itself, which
+ *                    gdn_gate_bwd carries on to a, b, A_log and dt_bias.
+ *   dout             [T, Nv, Dv] io_dtype
+ *   d_final_state    [N, Nv, Dk, Dv] fp32, or NULL for zeros
+ *   dq, dk           [T, Nqk, Dk] io_dtype (summed over the v-heads of a qk-head)
+ *   dv               [T, Nv, Dv] io_dtype
+ *   dg, dbeta        [T, Nv] io_dtype: as the gradients of every token tensor, they
+ *                    are computed in fp32 and rounded once to the type of the
+ *                    activations they flow into
+ *   d_initial_state  [N, Nv, Dk, Dv] fp32, or NULL if it is not wanted
+ *   workspace        device memory of at least gdn_chunk_bwd_workspace bytes, 16-byte
+ *                    aligned; its contents are undefined before and after.  Calls
+ *                    (and captured graphs) that may run at the same time need
+ *                    workspaces of their own.
+ *   p                as gdn_chunk_fwd; kernel must not be GDN_KERNEL_TC
+ *
+ * No output may overlap an input, another output or the workspace.  Tokens that
+ * cu_seqlens leaves outside every sequence are not written.  Zero-length
+ * sequences pass d_final_state on to d_initial_state, and with total_tokens = 0
+ * the token tensors and the workspace may be NULL.  The result does not depend on
+ * the order in which blocks run: no atomics are used.
+ */
+int gdn_chunk_bwd(const void *q, const void *k, const void *v,
+                  const float *g, const float *beta,
+                  const float *A_log, const float *dt_bias,
+                  const float *initial_state, const void *dout, const float *d_final_state,
+                  const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                  void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                  float *d_initial_state, void *workspace, int64_t workspace_bytes,
+                  const gdn_params_t *p, void *cuda_stream);
+
+/* Bytes of workspace that gdn_chunk_bwd needs, or a negative gdn_status_t.  Host only. */
+int64_t gdn_chunk_bwd_workspace(int32_t num_seqs, int64_t total_tokens, const gdn_params_t *p);
+
+/*
  * gdn_device_status -- read and clear, in one atomic step ordered on
  * `cuda_stream`, the library's device-side status word for the current
  * device, then synchronise the stream.  Every kernel of the library reports
