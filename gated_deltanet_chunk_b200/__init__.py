@@ -412,11 +412,11 @@ def qkv_conv_update(mixed_qkv, weight, conv_state, nqk, nv, dk, dv, bias=None, s
     return q, k, v
 
 
-def chunk_bwd_workspace(q, v, cu_seqlens=None, num_seqs=None) -> int:
-    """Bytes of workspace that ``chunk_bwd`` needs for these tensors (``gdn_chunk_bwd_workspace``)."""
+def chunk_bwd_workspace(q, v, cu_seqlens=None, num_seqs=None, qk_l2norm=True, kernel="auto") -> int:
+    """Bytes of workspace that ``chunk_bwd`` needs for these arguments (``gdn_chunk_bwd_workspace``)."""
     import torch
     n = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
-    p = make_params(q.shape[1], v.shape[1], q.shape[2], v.shape[2], q.dtype == torch.bfloat16)
+    p = make_params(q.shape[1], v.shape[1], q.shape[2], v.shape[2], q.dtype == torch.bfloat16, qk_l2norm, kernel=kernel)
     need = lib().gdn_chunk_bwd_workspace(int(n), int(q.shape[0]), ctypes.byref(p))
     if need < 0:
         raise GdnError(need, "gdn_chunk_bwd_workspace")
@@ -425,7 +425,8 @@ def chunk_bwd_workspace(q, v, cu_seqlens=None, num_seqs=None) -> int:
 
 def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu_seqlens=None, num_seqs=None,
               A_log=None, dt_bias=None, dq=None, dk=None, dv=None, dg=None, dbeta=None, d_initial_state=None,
-              output_d_initial_state=None, qk_l2norm=True, scale=0.0, workspace=None, stream=None, check=True):
+              output_d_initial_state=None, qk_l2norm=True, scale=0.0, kernel="auto", workspace=None, stream=None,
+              check=True):
     """Gradients of ``chunk_fwd`` (``gdn_chunk_bwd``); the inputs are those of the forward call.
 
     dout [T, Nv, Dv] (dtype of v), d_final_state [N, Nv, Dk, Dv] fp32 or None (zeros).
@@ -449,8 +450,9 @@ def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu
                                     else output_d_initial_state):
         d_initial_state = torch.empty((n, nv, dk_, dv_), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(chunk_bwd_workspace(q, v, cu_seqlens, num_seqs), dtype=torch.uint8, device=q.device)
-    p = make_params(nqk, nv, dk_, dv_, q.dtype == torch.bfloat16, qk_l2norm, scale)
+        need = chunk_bwd_workspace(q, v, cu_seqlens, num_seqs, qk_l2norm, kernel)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    p = make_params(nqk, nv, dk_, dv_, q.dtype == torch.bfloat16, qk_l2norm, scale, kernel)
     rc = lib().gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(A_log), _ptr(dt_bias),
                              _ptr(initial_state), _ptr(dout), _ptr(d_final_state), _ptr(cu_seqlens), int(n), int(T),
                              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(d_initial_state),

@@ -1,0 +1,146 @@
+// chunk_bwd.cuh -- what the two kernel families of gdn_chunk_bwd share: chunk
+// slots, the split-TF32 warp product, the in-chunk cumsum and the inverse.
+#pragma once
+
+#include "gdn_common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace gdn {
+namespace bwd {
+
+constexpr int C = 64;           // tokens per chunk
+constexpr int TP = C + 4;       // pitch of fp32 [C][C] tiles
+
+// Chunks are numbered by slots: chunk c of sequence n has slot cu[n] / C + n + c.
+// Slots of different sequences never meet (cu[n] / C + ceil(len / C) <= cu[n + 1] / C + 1),
+// and there are at most T / C + N of them.
+template <class Args>
+__device__ __forceinline__ int64_t first_slot(const Args& a, int n) {
+  int64_t s, e;
+  seq_bounds_quiet(a, n, s, e);
+  return s / C + n;
+}
+
+// The chunk at a slot: its sequence's end and its first token; false where the slot is empty.
+template <class Args>
+__device__ __forceinline__ bool chunk_at(const Args& a, int64_t slot, int64_t& c0, int64_t& end) {
+  int lo = 0, hi = a.num_seqs - 1;
+  while (lo < hi) {  // the last sequence whose first slot is not beyond `slot`
+    const int mid = (lo + hi + 1) >> 1;
+    if (first_slot(a, mid) <= slot) lo = mid; else hi = mid - 1;
+  }
+  int64_t start;
+  seq_bounds_quiet(a, lo, start, end);
+  c0 = start + (slot - (start / C + lo)) * C;
+  return c0 >= start && c0 < end;
+}
+
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = ptx::to_tf32(x);
+  lo = ptx::to_tf32(x - __uint_as_float(hi));
+}
+
+// acc += a b with both operands' hi and lo parts; an operand known to be exact in TF32 has no lo part.
+template <bool XA, bool XB>
+__device__ __forceinline__ void mma3(float* acc, const uint32_t* ah, const uint32_t* al, const uint32_t* bh,
+                                     const uint32_t* bl) {
+  if constexpr (!XA) ptx::mma_tf32_16x8x8(acc, al, bh);
+  if constexpr (!XB) ptx::mma_tf32_16x8x8(acc, ah, bl);
+  ptx::mma_tf32_16x8x8(acc, ah, bh);
+}
+
+// acc[NT] (16 x 8 tiles: a 16 x 8 NT block) += A[16 x K] B[K x 8 NT] over k in [k0, k1), one warp;
+// a(m, k) and b(k, n) read the operands' elements.  kPairs = false: operands rounded to TF32 once, one MMA.
+template <int NT, bool kPairs = true, typename FA, typename FB>
+__device__ __forceinline__ void warp_gemm(float (&acc)[NT][4], int k0, int k1, FA a, FB b, int g, int t) {
+#pragma unroll 2
+  for (int kk = k0; kk < k1; kk += 8) {
+    uint32_t ah[4], al[4];
+    split_tf32(a(g, kk + t), ah[0], al[0]);
+    split_tf32(a(g + 8, kk + t), ah[1], al[1]);
+    split_tf32(a(g, kk + t + 4), ah[2], al[2]);
+    split_tf32(a(g + 8, kk + t + 4), ah[3], al[3]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint32_t bh[2], bl[2];
+      split_tf32(b(kk + t, 8 * j + g), bh[0], bl[0]);
+      split_tf32(b(kk + t + 4, 8 * j + g), bh[1], bl[1]);
+      mma3<!kPairs, !kPairs>(acc[j], ah, al, bh, bl);
+    }
+  }
+}
+
+// In-chunk inclusive cumsum of x[0..C) by one warp.
+__device__ __forceinline__ void cumsum_chunk(float* x, int lane) {
+  const float x0 = x[2 * lane], x1 = x[2 * lane + 1];
+  float incl = x0 + x1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  float excl = __shfl_up_sync(0xffffffffu, incl, 1);
+  if (lane == 0) excl = 0.f;
+  x[2 * lane] = excl + x0;
+  x[2 * lane + 1] = excl + x0 + x1;
+}
+
+// T = (I - A)^-1 over A (strictly lower, pitch TP), as in chunk_simt.cu: 16 x 16
+// diagonal blocks by forward substitution in fp32 (a warp per block, a column
+// per lane), then T10 = T11 A10 T00 for blocks of 16 and of 32.  Y: [C / 2][TP]
+// scratch.  Zeros above the diagonal are written; the unit diagonal is stored.
+template <bool kPairs>
+__device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int lane) {
+  if (warp < C / 16 && lane < 16) {
+    float* blk = A + (16 * warp) * TP + 16 * warp;
+    const int jc = lane;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float acc = (jc < i) ? blk[i * TP + jc] : 0.f;
+#pragma unroll
+      for (int m = 0; m < i; ++m)
+        if (m > jc) acc = fmaf(blk[i * TP + m], x[m], acc);
+      x[i] = acc;
+    }
+    __syncwarp(0x0000ffffu);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) blk[i * TP + jc] = jc < i ? x[i] : (jc == i ? 1.f : 0.f);
+  }
+  __syncthreads();
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int s = 16; s < C; s *= 2) {
+    const int nb = s / 16, nunit = (C / (2 * s)) * nb * nb;  // 16 x 16 blocks of all T10 of this size
+    const int p = warp / (nb * nb), rb = (warp / nb) % nb, cb = warp % nb, base = 2 * s * p;
+    if (warp < nunit) {  // Y = A10 T00
+      const float* a10 = A + (base + s + 16 * rb) * TP + base;
+      const float* t00 = A + base * TP + base + 16 * cb;
+      float acc[2][4] = {};
+      warp_gemm<2, kPairs>(acc, 16 * cb, s, [&](int m, int k) { return a10[m * TP + k]; },
+                   [&](int k, int n) { return t00[k * TP + n]; }, g, t);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          Y[(p * s + 16 * rb + g + 8 * (e >> 1)) * TP + 16 * cb + 8 * j + 2 * t + (e & 1)] = acc[j][e];
+    }
+    __syncthreads();
+    if (warp < nunit) {  // T10 = T11 Y
+      const float* t11 = A + (base + s + 16 * rb) * TP + base + s;
+      const float* yp = Y + p * s * TP + 16 * cb;
+      float acc[2][4] = {};
+      warp_gemm<2, kPairs>(acc, 0, 16 * rb + 16, [&](int m, int k) { return t11[m * TP + k]; },
+                   [&](int k, int n) { return yp[k * TP + n]; }, g, t);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          A[(base + s + 16 * rb + g + 8 * (e >> 1)) * TP + base + 16 * cb + 8 * j + 2 * t + (e & 1)] = acc[j][e];
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace bwd
+}  // namespace gdn

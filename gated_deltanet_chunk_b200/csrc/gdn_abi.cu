@@ -485,12 +485,19 @@ GDN_API int gdn_qkv_conv_update(const void* mixed_qkv, const float* weight, cons
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// Whether the gradients run with fp16 operands: bf16 tensors whose q, k are normalised in the call.
+static bool bwd_half(const gdn_params_t* p) {
+  return p->io_dtype == GDN_DTYPE_BF16 && p->qk_l2norm && p->kernel != GDN_KERNEL_SIMT;
+}
+
 GDN_API int64_t gdn_chunk_bwd_workspace(int32_t num_seqs, int64_t total_tokens, const gdn_params_t* p) {
   const int rc = check_params(p);
   if (rc) return rc;
   if (num_seqs < 1 || num_seqs > 65535) return GDN_ERR_SHAPE;
   if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31)) return GDN_ERR_SHAPE;
-  return gdn::chunk_bwd_workspace(total_tokens, num_seqs, p->num_v_heads, p->head_k_dim, p->head_v_dim);
+  return bwd_half(p) ? gdn::chunk_bwd_half_workspace(total_tokens, num_seqs, p->num_qk_heads, p->num_v_heads,
+                                                     p->head_k_dim, p->head_v_dim)
+                     : gdn::chunk_bwd_workspace(total_tokens, num_seqs, p->num_v_heads, p->head_k_dim, p->head_v_dim);
 }
 
 GDN_API int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -500,7 +507,7 @@ GDN_API int gdn_chunk_bwd(const void* q, const void* k, const void* v, const flo
                           int64_t workspace_bytes, const gdn_params_t* p, void* cuda_stream) {
   const int64_t need = gdn_chunk_bwd_workspace(num_seqs, total_tokens, p);
   if (need < 0) return (int)need;
-  if (p->kernel == GDN_KERNEL_TC) return GDN_ERR_SHAPE;  // there is no choice of kernel here
+  if (p->kernel == GDN_KERNEL_TC && !bwd_half(p)) return GDN_ERR_SHAPE;
   if ((A_log == nullptr) != (dt_bias == nullptr)) return GDN_ERR_NULL;
   if (total_tokens != 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk_ || !dv_ || !dg || !dbeta || !workspace))
     return GDN_ERR_NULL;
@@ -543,8 +550,10 @@ GDN_API int gdn_chunk_bwd(const void* q, const void* k, const void* v, const flo
   a.nqk = p->num_qk_heads; a.nv = p->num_v_heads;
   a.qk_l2norm = p->qk_l2norm ? 1 : 0;
   a.scale = resolve_scale(p);
-  const cudaError_t e = gdn::launch_chunk_bwd(a, p->head_k_dim, p->head_v_dim, p->io_dtype == GDN_DTYPE_BF16,
-                                              static_cast<cudaStream_t>(cuda_stream));
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  const cudaError_t e = bwd_half(p)
+                            ? gdn::launch_chunk_bwd_half(a, p->head_k_dim, p->head_v_dim, stream)
+                            : gdn::launch_chunk_bwd(a, p->head_k_dim, p->head_v_dim, p->io_dtype == GDN_DTYPE_BF16, stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

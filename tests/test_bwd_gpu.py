@@ -37,8 +37,8 @@ def run(gdn, x, lens, use_cu=True, **kw):
                          cu_seqlens=cu, num_seqs=None if use_cu else len(lens), output_d_initial_state=True, **kw)
 
 
-def check(gdn, x, lens, io, use_cu=True, **kw):
-    got = run(gdn, x, lens, use_cu, **kw)
+def check(gdn, x, lens, io, use_cu=True, kernel="auto", **kw):
+    got = run(gdn, x, lens, use_cu, kernel=kernel, **kw)
     want = G.rule_grads(x["q"], x["k"], x["v"], x["g"], x["beta"], x["s0"], x["dout"], x["ds"], lens, **kw)
     for name, a, b in zip(NAMES, got, want):
         G.assert_close(a, b, io, name)
@@ -46,11 +46,11 @@ def check(gdn, x, lens, io, use_cu=True, **kw):
     return got
 
 
-@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("io,kernel", [(torch.float32, "auto"), (torch.bfloat16, "auto"), (torch.bfloat16, "simt")])
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
 @pytest.mark.parametrize("lens,nqk,nv,s0", [((130,), 1, 1, False), ((64, 1, 63, 65), 2, 4, True), ((17, 0, 100, 2), 1, 3, True)])
-def test_gradients(gdn, io, dk, dv, lens, nqk, nv, s0):
-    check(gdn, make(lens, nqk, nv, dk, dv, io, s0=s0, ds=s0), lens, io)
+def test_gradients(gdn, io, kernel, dk, dv, lens, nqk, nv, s0):
+    check(gdn, make(lens, nqk, nv, dk, dv, io, s0=s0, ds=s0), lens, io, kernel=kernel)
 
 
 @pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
