@@ -16,6 +16,14 @@ chunk_fwd_ex / recurrent_step_ex                               any of those fusi
                                                                gated RMSNorm epilogue (gdn_ext_t)
 gated_rmsnorm(o, z, weight, eps)       -> y                    the epilogue alone, gdn_gated_rmsnorm
 qkv_conv_fwd / qkv_conv_update         -> (q, k, v[, state])  causal conv1d + SiLU producing q, k, v
+
+Training:
+chunk_bwd(q, k, v, g, beta, dout, ...) -> (dq, dk, dv, dg, dbeta, d_initial_state)   gradients of chunk_fwd
+gate_bwd(dg, dbeta, a, b, A_log, dt_bias) -> (da, db, dA_log, ddt_bias)              of the gate
+gated_rmsnorm_bwd(dy, o, z, weight)    -> (do, dz, dweight)                           of the epilogue
+qkv_conv_bwd(dq, dk, dv, x, weight, ...) -> (dx, dweight, dbias, d_conv_state)        of the conv
+act_quantize(x) / act_dequantize       -> (codes, scales) / x   activations kept in 8 bits; the two
+                                                               gradients above read them as they are
 """
 from __future__ import annotations
 
@@ -107,6 +115,25 @@ def lib() -> ctypes.CDLL:
         L.gdn_chunk_bwd.restype = ctypes.c_int
         L.gdn_chunk_bwd_workspace.argtypes = [ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(GdnParams)]
         L.gdn_chunk_bwd_workspace.restype = ctypes.c_int64
+        L.gdn_act_quantize.argtypes = [vp, vp, vp, ctypes.c_int64, ctypes.c_int32, vp]
+        L.gdn_act_quantize.restype = ctypes.c_int
+        L.gdn_act_dequantize.argtypes = [vp, vp, vp, ctypes.c_int64, ctypes.c_int32, vp]
+        L.gdn_act_dequantize.restype = ctypes.c_int
+        L.gdn_gated_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, vp, fp, ctypes.c_float, vp, vp, fp, ctypes.c_int64,
+                                            ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int64, vp]
+        L.gdn_gated_rmsnorm_bwd.restype = ctypes.c_int
+        L.gdn_gated_rmsnorm_bwd_workspace.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
+        L.gdn_gated_rmsnorm_bwd_workspace.restype = ctypes.c_int64
+        L.gdn_qkv_conv_bwd.argtypes = [vp, vp, vp, vp, vp, fp, fp, vp, vp, ip, ctypes.c_int32, ctypes.c_int64,
+                                       ctypes.c_int32, vp, fp, fp, vp, vp, ctypes.c_int64, ctypes.POINTER(GdnParams), vp]
+        L.gdn_qkv_conv_bwd.restype = ctypes.c_int
+        L.gdn_qkv_conv_bwd_workspace.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(GdnParams)]
+        L.gdn_qkv_conv_bwd_workspace.restype = ctypes.c_int64
+        L.gdn_gate_bwd.argtypes = [vp, vp, fp, fp, fp, fp, vp, vp, fp, fp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                   vp, ctypes.c_int64, vp]
+        L.gdn_gate_bwd.restype = ctypes.c_int
+        L.gdn_gate_bwd_workspace.argtypes = [ctypes.c_int64, ctypes.c_int32]
+        L.gdn_gate_bwd_workspace.restype = ctypes.c_int64
         L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_int64, vp]
         L.gdn_selftest_wait_timeout.restype = ctypes.c_int
         L.gdn_device_status.argtypes = [vp]
@@ -461,3 +488,138 @@ def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu
     if check and rc != GDN_OK:
         raise GdnError(rc, "gdn_chunk_bwd")
     return dq, dk, dv, dg, dbeta, d_initial_state
+
+
+def _kept(x):
+    """(tensor, scales) of a saved activation: a tensor, or the pair that ``act_quantize`` returned."""
+    return x if isinstance(x, tuple) else (x, None)
+
+
+def _workspace(need, what, device):
+    import torch
+    if need < 0:
+        raise GdnError(need, what)
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def act_quantize(x, codes=None, scales=None, stream=None, check=True):
+    """Keep an activation in 8 bits (``gdn_act_quantize``): ``(codes, scales)``.
+
+    x [..., D] (bf16 or fp32, CUDA, contiguous), D a multiple of 32.  codes [..., D]
+    float8_e4m3fn; scales [..., D / 32] uint8, one byte e + 127 per 32 values, which
+    stand for code * 2^e; 2^e is the least power of two with max |x| <= 448 * 2^e.
+    Values that are not finite read back as NaN and do not touch their group's scale.
+    """
+    import torch
+    if x.shape[-1] % 32 != 0:
+        raise GdnError(-2, "gdn_act_quantize")
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty((*x.shape[:-1], x.shape[-1] // 32), dtype=torch.uint8, device=x.device)
+    rc = lib().gdn_act_quantize(_ptr(x), _ptr(codes), _ptr(scales), int(x.numel()),
+                                DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32, _stream(stream))
+    if check and rc != GDN_OK:
+        raise GdnError(rc, "gdn_act_quantize")
+    return codes, scales
+
+
+def act_dequantize(codes, scales, dtype, out=None, stream=None, check=True):
+    """The values that ``act_quantize``'s codes and scales stand for, in ``dtype`` (``gdn_act_dequantize``)."""
+    import torch
+    if out is None:
+        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    rc = lib().gdn_act_dequantize(_ptr(codes), _ptr(scales), _ptr(out), int(codes.numel()),
+                                  DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32, _stream(stream))
+    if check and rc != GDN_OK:
+        raise GdnError(rc, "gdn_act_dequantize")
+    return out
+
+
+def gated_rmsnorm_bwd(dy, o, z, weight, eps=1e-6, d_o=None, d_z=None, d_weight=None, workspace=None, stream=None,
+                      check=True):
+    """Gradients of ``gated_rmsnorm`` (``gdn_gated_rmsnorm_bwd``): ``(do, dz, dweight)``.
+
+    dy [..., D] (bf16 or fp32; D in {64, 128}).  o and z are the forward call's inputs
+    in the dtype of dy, or, each for itself, the pair that ``act_quantize`` returned for
+    it.  do, dz have dy's dtype; dweight [D] is fp32.
+    """
+    import torch
+    (o, os_), (z, zs) = _kept(o), _kept(z)
+    dim, bf16 = dy.shape[-1], dy.dtype == torch.bfloat16
+    rows, io = int(dy.numel() // dim), DTYPE_BF16 if bf16 else DTYPE_F32
+    d_o = torch.empty_like(dy) if d_o is None else d_o
+    d_z = torch.empty_like(dy) if d_z is None else d_z
+    d_weight = torch.empty(dim, dtype=torch.float32, device=dy.device) if d_weight is None else d_weight
+    if workspace is None:
+        workspace = _workspace(lib().gdn_gated_rmsnorm_bwd_workspace(rows, int(dim), io), "gdn_gated_rmsnorm_bwd", dy.device)
+    rc = lib().gdn_gated_rmsnorm_bwd(_ptr(dy), _ptr(o), _ptr(os_), _ptr(z), _ptr(zs), _ptr(weight), float(eps), _ptr(d_o),
+                                     _ptr(d_z), _ptr(d_weight), rows, int(dim), io, _ptr(workspace),
+                                     int(workspace.numel() * workspace.element_size()), _stream(stream))
+    if check and rc != GDN_OK:
+        raise GdnError(rc, "gdn_gated_rmsnorm_bwd")
+    return d_o, d_z, d_weight
+
+
+def qkv_conv_bwd(dq, dk, dv, mixed_qkv, weight, bias=None, conv_state=None, cu_seqlens=None, num_seqs=None,
+                 d_state_out=None, output_d_state=None, dx=None, d_weight=None, d_bias=None, d_state=None,
+                 workspace=None, stream=None, check=True):
+    """Gradients of ``qkv_conv_fwd`` (``gdn_qkv_conv_bwd``): ``(dx, dweight, dbias, d_conv_state)``.
+
+    dq, dk [T, Nqk, Dk], dv [T, Nv, Dv] (bf16 or fp32): the gradients of the call's q, k, v.
+    mixed_qkv, weight, bias, conv_state, cu_seqlens: the call's inputs, mixed_qkv also as
+    the pair that ``act_quantize`` returned for it.  d_state_out [N, C, K]: the gradient of
+    the new conv_state, if there is one.  dx [T, C] and d_conv_state [N, C, K] have dq's
+    dtype, dweight [C, K] and dbias [C] are fp32; dbias is None without a bias, and
+    d_conv_state unless a conv_state was given or it was asked for.
+    """
+    import torch
+    x, xs = _kept(mixed_qkv)
+    T, C = x.shape
+    K = weight.shape[1]
+    nqk, dkk, nv, dvv = dq.shape[1], dq.shape[2], dv.shape[1], dv.shape[2]
+    n = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
+    if C != 2 * nqk * dkk + nv * dvv:
+        raise GdnError(-2, "gdn_qkv_conv_bwd")
+    dev = dq.device
+    dx = torch.empty((T, C), dtype=dq.dtype, device=dev) if dx is None else dx
+    d_weight = torch.empty((C, K), dtype=torch.float32, device=dev) if d_weight is None else d_weight
+    if d_bias is None and bias is not None:
+        d_bias = torch.empty(C, dtype=torch.float32, device=dev)
+    if d_state is None and (conv_state is not None if output_d_state is None else output_d_state):
+        d_state = torch.empty((n, C, K), dtype=dq.dtype, device=dev)
+    p = make_params(nqk, nv, dkk, dvv, dq.dtype == torch.bfloat16)
+    if workspace is None:
+        workspace = _workspace(lib().gdn_qkv_conv_bwd_workspace(int(T), int(K), ctypes.byref(p)), "gdn_qkv_conv_bwd", dev)
+    rc = lib().gdn_qkv_conv_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(x), _ptr(xs), _ptr(weight), _ptr(bias),
+                                _ptr(conv_state), _ptr(d_state_out), _ptr(cu_seqlens), int(n), int(T), int(K), _ptr(dx),
+                                _ptr(d_weight), _ptr(d_bias), _ptr(d_state), _ptr(workspace),
+                                int(workspace.numel() * workspace.element_size()), ctypes.byref(p), _stream(stream))
+    if check and rc != GDN_OK:
+        raise GdnError(rc, "gdn_qkv_conv_bwd")
+    return dx, d_weight, d_bias, d_state
+
+
+def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt_bias=None, workspace=None, stream=None,
+             check=True):
+    """Gradients of the layer's gate (``gdn_gate_bwd``): ``(da, db, dA_log, ddt_bias)``.
+
+    dg, dbeta [T, Nv] (bf16 or fp32, as ``chunk_bwd`` returns them); a, b [T, Nv] and
+    A_log, dt_bias [Nv] fp32, as ``chunk_fwd_gated`` takes them.  da, db have dg's dtype,
+    dA_log and ddt_bias [Nv] are fp32.
+    """
+    import torch
+    T, nv = a.shape
+    da = torch.empty_like(dg) if da is None else da
+    db = torch.empty_like(dg) if db is None else db
+    dA_log = torch.empty(nv, dtype=torch.float32, device=dg.device) if dA_log is None else dA_log
+    ddt_bias = torch.empty(nv, dtype=torch.float32, device=dg.device) if ddt_bias is None else ddt_bias
+    if workspace is None:
+        workspace = _workspace(lib().gdn_gate_bwd_workspace(int(T), int(nv)), "gdn_gate_bwd", dg.device)
+    rc = lib().gdn_gate_bwd(_ptr(dg), _ptr(dbeta), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(da), _ptr(db),
+                            _ptr(dA_log), _ptr(ddt_bias), int(T), int(nv),
+                            DTYPE_BF16 if dg.dtype == torch.bfloat16 else DTYPE_F32, _ptr(workspace),
+                            int(workspace.numel() * workspace.element_size()), _stream(stream))
+    if check and rc != GDN_OK:
+        raise GdnError(rc, "gdn_gate_bwd")
+    return da, db, dA_log, ddt_bias

@@ -86,7 +86,7 @@ float resolve_scale(const gdn_params_t* p) {
 
 }  // namespace
 
-GDN_API int gdn_version(void) { return (1 << 16) | 6; }
+GDN_API int gdn_version(void) { return (1 << 16) | 7; }
 
 GDN_API const char* gdn_status_string(int status) {
   switch (status) {
@@ -100,7 +100,8 @@ GDN_API const char* gdn_status_string(int status) {
     case GDN_ERR_DEVICE_TIMEOUT: return "GDN_ERR_DEVICE_TIMEOUT: a bounded in-kernel wait expired";
     case GDN_ERR_SEQLENS:
       return "GDN_ERR_SEQLENS: cu_seqlens was not non-decreasing from 0 to total_tokens (rows outside were skipped)";
-    case GDN_ERR_GATE: return "GDN_ERR_GATE: a gate g > 0 or NaN reached the tensor-core kernel, which needs g <= 0";
+    case GDN_ERR_GATE:
+      return "GDN_ERR_GATE: a gate g > 0 or NaN reached the tensor-core kernel, which needs g <= 0 (its gradients also 0 <= beta <= 2)";
     default: return "GDN: unknown status";
   }
 }
@@ -554,6 +555,169 @@ GDN_API int gdn_chunk_bwd(const void* q, const void* k, const void* v, const flo
   const cudaError_t e = bwd_half(p)
                             ? gdn::launch_chunk_bwd_half(a, p->head_k_dim, p->head_v_dim, stream)
                             : gdn::launch_chunk_bwd(a, p->head_k_dim, p->head_v_dim, p->io_dtype == GDN_DTYPE_BF16, stream);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// ---- activations in 8 bits, and the gradients around the core ----
+
+// Shared by the calls below: an output may overlap no input and no other output.
+static bool any_overlap(const Range* in, int nin, const Range* out, int nout) {
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (overlap(out[i], in[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+  }
+  return false;
+}
+static Range opt_range(const void* p, size_t bytes) { return p ? range_of(p, bytes) : Range{0, 0}; }
+
+static int act_check(const void* x, const void* codes, const void* scales, int64_t n, int32_t io_dtype) {
+  if (io_dtype != GDN_DTYPE_F32 && io_dtype != GDN_DTYPE_BF16) return GDN_ERR_SHAPE;
+  if (n < 0 || n % 32 != 0 || n >= (int64_t(1) << 42)) return GDN_ERR_SHAPE;
+  if (n == 0) return GDN_OK;
+  if (!x || !codes || !scales) return GDN_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes)) return GDN_ERR_ALIGN;
+  const size_t esz = io_dtype == GDN_DTYPE_BF16 ? 2 : 4;
+  const Range r[] = {range_of(x, (size_t)n * esz), range_of(codes, (size_t)n), range_of(scales, (size_t)n / 32)};
+  if (any_overlap(r, 0, r, 3)) return GDN_ERR_ALIAS;
+  return check_device();
+}
+
+GDN_API int gdn_act_quantize(const void* x, void* codes, void* scales, int64_t n, int32_t io_dtype, void* cuda_stream) {
+  const int rc = act_check(x, codes, scales, n, io_dtype);
+  if (rc || n == 0) return rc;
+  const cudaError_t e = gdn::launch_act_quantize(x, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), n,
+                                                 io_dtype == GDN_DTYPE_BF16, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+GDN_API int gdn_act_dequantize(const void* codes, const void* scales, void* x, int64_t n, int32_t io_dtype,
+                               void* cuda_stream) {
+  const int rc = act_check(x, codes, scales, n, io_dtype);
+  if (rc || n == 0) return rc;
+  const cudaError_t e = gdn::launch_act_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), x,
+                                                   n, io_dtype == GDN_DTYPE_BF16, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+GDN_API int64_t gdn_gated_rmsnorm_bwd_workspace(int64_t rows, int32_t dim, int32_t io_dtype) {
+  if (rows < 0 || rows >= (int64_t(1) << 31) || (dim != 64 && dim != 128)) return GDN_ERR_SHAPE;
+  if (io_dtype != GDN_DTYPE_F32 && io_dtype != GDN_DTYPE_BF16) return GDN_ERR_SHAPE;
+  return gdn::gated_rmsnorm_bwd_workspace(rows, dim, io_dtype == GDN_DTYPE_BF16);
+}
+
+GDN_API int gdn_gated_rmsnorm_bwd(const void* dy, const void* o, const void* o_scales, const void* z, const void* z_scales,
+                                  const float* weight, float eps, void* d_o, void* d_z, float* d_weight, int64_t rows,
+                                  int32_t dim, int32_t io_dtype, void* workspace, int64_t workspace_bytes,
+                                  void* cuda_stream) {
+  const int64_t need = gdn_gated_rmsnorm_bwd_workspace(rows, dim, io_dtype);
+  if (need < 0) return (int)need;
+  if (!std::isfinite(eps) || eps < 0.f) return GDN_ERR_SHAPE;
+  if (!d_weight || (rows != 0 && (!dy || !o || !z || !weight || !d_o || !d_z || !workspace))) return GDN_ERR_NULL;
+  if (workspace_bytes < need) return GDN_ERR_SHAPE;
+  for (const void* ptr : {dy, o, z, (const void*)weight, (const void*)d_o, (const void*)d_z, (const void*)workspace})
+    if (ptr && !aligned16(ptr)) return GDN_ERR_ALIGN;
+  if (!aligned4(d_weight)) return GDN_ERR_ALIGN;
+  const size_t n = (size_t)rows * dim, esz = io_dtype == GDN_DTYPE_BF16 ? 2 : 4;
+  const Range in[] = {range_of(dy, n * esz), range_of(o, n * (o_scales ? 1 : esz)), opt_range(o_scales, n / 32),
+                      range_of(z, n * (z_scales ? 1 : esz)), opt_range(z_scales, n / 32), range_of(weight, (size_t)dim * 4)};
+  const Range out[] = {range_of(d_o, n * esz), range_of(d_z, n * esz), range_of(d_weight, (size_t)dim * 4),
+                       range_of(workspace, (size_t)need)};
+  if (any_overlap(in, 6, out, 4)) return GDN_ERR_ALIAS;
+  const int rc = check_device();
+  if (rc) return rc;
+  gdn::NormBwdArgs a{};
+  a.dy = dy; a.o = o; a.o_scales = static_cast<const uint8_t*>(o_scales);
+  a.z = z; a.z_scales = static_cast<const uint8_t*>(z_scales);
+  a.w = weight; a.eps = eps; a.d_o = d_o; a.d_z = d_z; a.dw = d_weight; a.rows = rows;
+  const cudaError_t e = gdn::launch_gated_rmsnorm_bwd(a, dim, io_dtype == GDN_DTYPE_BF16, static_cast<float*>(workspace),
+                                                      static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+GDN_API int64_t gdn_qkv_conv_bwd_workspace(int64_t total_tokens, int32_t kernel_size, const gdn_params_t* p) {
+  const int rc = check_params(p);
+  if (rc) return rc;
+  if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || kernel_size < 1 || kernel_size > 4) return GDN_ERR_SHAPE;
+  return gdn::conv_bwd_workspace(total_tokens, 2 * p->num_qk_heads * p->head_k_dim + p->num_v_heads * p->head_v_dim, kernel_size);
+}
+
+GDN_API int gdn_qkv_conv_bwd(const void* dq, const void* dk, const void* dv, const void* mixed_qkv, const void* x_scales,
+                             const float* weight, const float* bias, const void* conv_state_in, const void* d_conv_state_out,
+                             const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t kernel_size,
+                             void* d_mixed_qkv, float* d_weight, float* d_bias, void* d_conv_state_in, void* workspace,
+                             int64_t workspace_bytes, const gdn_params_t* p, void* cuda_stream) {
+  const int64_t need = gdn_qkv_conv_bwd_workspace(total_tokens, kernel_size, p);
+  if (need < 0) return (int)need;
+  if (num_seqs < 1 || num_seqs > 65535) return GDN_ERR_SHAPE;
+  if (!weight || !d_weight || (total_tokens != 0 && (!dq || !dk || !dv || !mixed_qkv || !d_mixed_qkv || !workspace)))
+    return GDN_ERR_NULL;
+  if (workspace_bytes < need) return GDN_ERR_SHAPE;
+  if (!cu_seqlens && total_tokens % num_seqs != 0) return GDN_ERR_SHAPE;
+  const void* ptrs[] = {dq, dk, dv, mixed_qkv, weight, conv_state_in, d_conv_state_out, cu_seqlens, d_mixed_qkv,
+                        d_conv_state_in, workspace};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return GDN_ERR_ALIGN;
+  if ((bias && !aligned4(bias)) || !aligned4(d_weight) || (d_bias && !aligned4(d_bias))) return GDN_ERR_ALIGN;
+  gdn::ConvBwdArgs a{};
+  a.nqk = p->num_qk_heads; a.nv = p->num_v_heads; a.dk = p->head_k_dim; a.dv = p->head_v_dim;
+  a.channels = 2 * a.nqk * a.dk + a.nv * a.dv;
+  const size_t T = (size_t)total_tokens, N = (size_t)num_seqs, C = (size_t)a.channels, K = (size_t)kernel_size;
+  const size_t esz = p->io_dtype == GDN_DTYPE_BF16 ? 2 : 4, state = N * C * K * esz;
+  const size_t qkb = T * a.nqk * a.dk * esz, vb = T * a.nv * a.dv * esz;
+  const Range in[] = {range_of(dq, qkb), range_of(dk, qkb), range_of(dv, vb), range_of(mixed_qkv, T * C * (x_scales ? 1 : esz)),
+                      opt_range(x_scales, T * C / 32), range_of(weight, C * K * 4), opt_range(bias, C * 4),
+                      opt_range(conv_state_in, state), opt_range(d_conv_state_out, state), opt_range(cu_seqlens, (N + 1) * 4)};
+  const Range out[] = {range_of(d_mixed_qkv, T * C * esz), range_of(d_weight, C * K * 4), opt_range(d_bias, C * 4),
+                       opt_range(d_conv_state_in, state), range_of(workspace, (size_t)need)};
+  if (any_overlap(in, 10, out, 5)) return GDN_ERR_ALIAS;
+  const int rc = check_device();
+  if (rc) return rc;
+  a.status = status_word();
+  if (!a.status) return GDN_ERR_CUDA;
+  a.dq = dq; a.dk_ = dk; a.dv_ = dv; a.x = mixed_qkv; a.x_scales = static_cast<const uint8_t*>(x_scales);
+  a.weight = weight; a.bias = bias; a.state_in = conv_state_in; a.dstate_out = d_conv_state_out; a.cu = cu_seqlens;
+  a.dx = d_mixed_qkv; a.dw = d_weight; a.db = d_bias; a.dstate_in = d_conv_state_in;
+  a.uniform_len = cu_seqlens ? 0 : (int32_t)(total_tokens / num_seqs);
+  a.num_seqs = num_seqs; a.total_tokens = total_tokens; a.ksize = kernel_size;
+  const cudaError_t e = gdn::launch_conv_bwd(a, p->io_dtype == GDN_DTYPE_BF16, static_cast<float*>(workspace),
+                                             static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+GDN_API int64_t gdn_gate_bwd_workspace(int64_t tokens, int32_t num_v_heads) {
+  if (tokens < 0 || tokens >= (int64_t(1) << 31) || num_v_heads < 1 || num_v_heads > 65535) return GDN_ERR_SHAPE;
+  return gdn::gate_bwd_workspace(tokens, num_v_heads);
+}
+
+GDN_API int gdn_gate_bwd(const void* dg, const void* dbeta, const float* a, const float* b, const float* A_log,
+                         const float* dt_bias, void* da, void* db, float* dA_log, float* ddt_bias, int64_t tokens,
+                         int32_t num_v_heads, int32_t io_dtype, void* workspace, int64_t workspace_bytes, void* cuda_stream) {
+  const int64_t need = gdn_gate_bwd_workspace(tokens, num_v_heads);
+  if (need < 0) return (int)need;
+  if (io_dtype != GDN_DTYPE_F32 && io_dtype != GDN_DTYPE_BF16) return GDN_ERR_SHAPE;
+  if (!A_log || !dt_bias || !dA_log || !ddt_bias || (tokens != 0 && (!dg || !dbeta || !a || !b || !da || !db)) ||
+      (need != 0 && !workspace))
+    return GDN_ERR_NULL;
+  if (workspace_bytes < need) return GDN_ERR_SHAPE;
+  for (const void* ptr : {dg, dbeta, (const void*)a, (const void*)b, (const void*)da, (const void*)db, (const void*)workspace})
+    if (ptr && !aligned16(ptr)) return GDN_ERR_ALIGN;
+  for (const void* ptr : {(const void*)A_log, (const void*)dt_bias, (const void*)dA_log, (const void*)ddt_bias})
+    if (!aligned4(ptr)) return GDN_ERR_ALIGN;
+  const size_t n = (size_t)tokens * num_v_heads, esz = io_dtype == GDN_DTYPE_BF16 ? 2 : 4, head = (size_t)num_v_heads * 4;
+  const Range in[] = {range_of(dg, n * esz), range_of(dbeta, n * esz), range_of(a, n * 4), range_of(b, n * 4),
+                      range_of(A_log, head), range_of(dt_bias, head)};
+  const Range out[] = {range_of(da, n * esz), range_of(db, n * esz), range_of(dA_log, head), range_of(ddt_bias, head),
+                       range_of(workspace, (size_t)need)};
+  if (any_overlap(in, 6, out, 5)) return GDN_ERR_ALIAS;
+  const int rc = check_device();
+  if (rc) return rc;
+  gdn::GateBwdArgs x{};
+  x.dg = dg; x.dbeta = dbeta; x.a = a; x.b = b; x.A_log = A_log; x.dt_bias = dt_bias;
+  x.da = da; x.db = db; x.dA_log = dA_log; x.ddt_bias = ddt_bias; x.tokens = tokens; x.nv = num_v_heads;
+  const cudaError_t e = gdn::launch_gate_bwd(x, io_dtype == GDN_DTYPE_BF16, static_cast<float*>(workspace),
+                                             static_cast<cudaStream_t>(cuda_stream));
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

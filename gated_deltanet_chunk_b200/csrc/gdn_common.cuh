@@ -123,6 +123,61 @@ struct BwdArgs {
   float scale;
 };
 
+// Arguments of the gradients of the gated RMSNorm (gdn_gated_rmsnorm_bwd).
+struct NormBwdArgs {
+  const void* dy;            // [rows, dim] io dtype
+  const void* o;             // [rows, dim] io dtype, or e4m3 codes
+  const uint8_t* o_scales;   // [rows, dim / 32] when o holds codes, or nullptr
+  const void* z;             // as o
+  const uint8_t* z_scales;
+  const float* w;            // [dim]
+  float eps;
+  void* d_o;                 // [rows, dim] io dtype
+  void* d_z;
+  float* dw;                 // [dim]
+  int64_t rows;
+};
+
+// Arguments of the gradients of the gate (gdn_gate_bwd).
+struct GateBwdArgs {
+  const void* dg;            // [tokens, nv] io dtype
+  const void* dbeta;
+  const float* a;            // [tokens, nv]
+  const float* b;
+  const float* A_log;        // [nv]
+  const float* dt_bias;
+  void* da;                  // [tokens, nv] io dtype
+  void* db;
+  float* dA_log;             // [nv]
+  float* ddt_bias;
+  int64_t tokens;
+  int32_t nv;
+};
+
+// Arguments of the gradients of the causal conv1d + SiLU (gdn_qkv_conv_bwd).
+struct ConvBwdArgs {
+  const void* dq;            // [T, nqk, dk] io dtype
+  const void* dk_;
+  const void* dv_;           // [T, nv, dv]
+  const void* x;             // [T, channels] io dtype, or e4m3 codes
+  const uint8_t* x_scales;   // [T, channels / 32] when x holds codes, or nullptr
+  const float* weight;       // [channels, ksize]
+  const float* bias;         // [channels] or nullptr
+  const void* state_in;      // [N, channels, ksize] io dtype or nullptr (zeros)
+  const void* dstate_out;    // [N, channels, ksize] io dtype or nullptr
+  const int32_t* cu;         // [N + 1] or nullptr (equal lengths)
+  void* dx;                  // [T, channels] io dtype
+  float* dw;                 // [channels, ksize]
+  float* db;                 // [channels] or nullptr
+  void* dstate_in;           // [N, channels, ksize] io dtype or nullptr
+  int32_t uniform_len;       // sequence length when cu == nullptr
+  int32_t num_seqs;
+  int64_t total_tokens;
+  int32_t channels, ksize;   // channels = 2 nqk dk + nv dv
+  int32_t nqk, nv, dk, dv;
+  unsigned int* status;      // device status word (kStatus* bits)
+};
+
 template <typename T> __device__ __forceinline__ float to_f32(T x);
 template <> __device__ __forceinline__ float to_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) {

@@ -36,4 +36,16 @@ cudaError_t launch_chunk_bwd(const BwdArgs& a, int dk, int dv, int io_bf16, cuda
 int64_t chunk_bwd_half_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv);
 cudaError_t launch_chunk_bwd_half(const BwdArgs& a, int dk, int dv, cudaStream_t s);
 
+// Activations in 8 bits: n values (a multiple of 32), codes [n], scale bytes [n / 32].
+cudaError_t launch_act_quantize(const void* x, uint8_t* codes, uint8_t* scales, int64_t n, int io_bf16, cudaStream_t s);
+cudaError_t launch_act_dequantize(const uint8_t* codes, const uint8_t* scales, void* y, int64_t n, int io_bf16, cudaStream_t s);
+
+// Gradients of the gated RMSNorm, of the conv and of the gate; `part`: workspace of the bytes that go before.
+int64_t gated_rmsnorm_bwd_workspace(int64_t rows, int dim, int io_bf16);
+cudaError_t launch_gated_rmsnorm_bwd(const NormBwdArgs& p, int dim, int io_bf16, float* part, cudaStream_t s);
+int64_t conv_bwd_workspace(int64_t tokens, int channels, int ksize);
+cudaError_t launch_conv_bwd(const ConvBwdArgs& a, int io_bf16, float* part, cudaStream_t s);
+int64_t gate_bwd_workspace(int64_t tokens, int nv);
+cudaError_t launch_gate_bwd(const GateBwdArgs& p, int io_bf16, float* part, cudaStream_t s);
+
 }  // namespace gdn

@@ -374,8 +374,7 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
  * inputs, so nothing has to be kept from the forward call but those.
  *
  *   q, k, v, g, beta, initial_state, cu_seqlens, num_seqs, total_tokens
- *                    as gdn_chunk_fwd had them.  g is any finite value, as for
- *                    GDN_KERNEL_SIMT.
+ *                    as gdn_chunk_fwd had them.  See "kernels" below for g and beta.
  *   A_log, dt_bias   [Nv] fp32, or both NULL.  Given, g and beta hold the raw
  *                    projections a and b, as in gdn_chunk_fwd_gated; dg and dbeta
  *                    are still the gradients of the gate itself, which
@@ -392,7 +391,15 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
  *                    aligned; its contents are undefined before and after.  Calls
  *                    (and captured graphs) that may run at the same time need
  *                    workspaces of their own.
- *   p                as gdn_chunk_fwd; kernel must not be GDN_KERNEL_TC
+ *   p                as gdn_chunk_fwd
+ *
+ * Kernels: with bf16 io and qk_l2norm, GDN_KERNEL_AUTO and GDN_KERNEL_TC use fp16
+ * operands (each rounded by at most 2^-12 of its value, under powers of two shared by
+ * tiles) with fp32 sums and states, and need g <= 0 and 0 <= beta <= 2: a gate outside
+ * leaves the results undefined and is reported as GDN_ERR_GATE.  GDN_KERNEL_SIMT, fp32
+ * io and calls without qk_l2norm use operands of about fp32's accuracy (pairs of TF32)
+ * and take any finite g and beta; GDN_KERNEL_TC is rejected for the latter two.  The
+ * workspace size depends on that choice.
  *
  * No output may overlap an input, another output or the workspace.  Tokens that
  * cu_seqlens leaves outside every sequence are not written.  Zero-length
@@ -411,6 +418,95 @@ int gdn_chunk_bwd(const void *q, const void *k, const void *v,
 
 /* Bytes of workspace that gdn_chunk_bwd needs, or a negative gdn_status_t.  Host only. */
 int64_t gdn_chunk_bwd_workspace(int32_t num_seqs, int64_t total_tokens, const gdn_params_t *p);
+
+/*
+ * gdn_act_quantize / gdn_act_dequantize -- keep an activation in 8 bits between the
+ * forward and the backward pass, and read it back.
+ *
+ *   x       [n] io_dtype (gdn_dtype_t), n a multiple of 32, 16-byte aligned
+ *   codes   [n] e4m3 bytes (4 exponent bits, bias 7; 3 mantissa bits; no infinity),
+ *           16-byte aligned
+ *   scales  [n / 32] bytes, one for every 32 consecutive values: e + 127 in [1, 247]
+ *
+ * code * 2^e is the value: 2^e is the least power of two, e >= -126, with
+ * max |x| <= 448 * 2^e over the group's finite values, and the code is x / 2^e rounded to
+ * nearest even (in a group whose largest magnitude is above 1.75 * 2^127, at most 240).
+ * Everything else is exact, and bf16 holds what is read back (unless it is below
+ * 2^-133).  NaN and infinities read back as NaN.  codes and scales are what
+ * gdn_gated_rmsnorm_bwd and gdn_qkv_conv_bwd take in the place of an activation whose
+ * rows are a multiple of 32 long.  No two of the tensors may overlap; n = 0 does nothing.
+ */
+int gdn_act_quantize(const void *x, void *codes, void *scales, int64_t n, int32_t io_dtype, void *cuda_stream);
+int gdn_act_dequantize(const void *codes, const void *scales, void *x, int64_t n, int32_t io_dtype,
+                       void *cuda_stream);
+
+/*
+ * gdn_gated_rmsnorm_bwd -- gradients of gdn_gated_rmsnorm.  With n = o / sqrt(mean(o^2)
+ * + eps) and y = n * weight * silu(z), from dy:
+ *
+ *   dy             [rows, dim] io_dtype
+ *   o, z           [rows, dim] io_dtype, as the forward call had them; or e4m3 codes,
+ *                  where o_scales / z_scales (each NULL or [rows, dim / 32] bytes) says
+ *                  so, as gdn_act_quantize wrote them
+ *   d_o, d_z       [rows, dim] io_dtype
+ *   d_weight       [dim] fp32, summed over the rows in fp32, in a fixed order
+ *   workspace      at least gdn_gated_rmsnorm_bwd_workspace bytes, 16-byte aligned;
+ *                  one for each call that may run at the same time
+ * rows, dim, eps as gdn_gated_rmsnorm; with rows = 0 d_weight is set to zero and every
+ * other pointer may be NULL.  No output may overlap an input or another output.  All
+ * arithmetic is fp32.
+ */
+int gdn_gated_rmsnorm_bwd(const void *dy, const void *o, const void *o_scales, const void *z, const void *z_scales,
+                          const float *weight, float eps, void *d_o, void *d_z, float *d_weight,
+                          int64_t rows, int32_t dim, int32_t io_dtype,
+                          void *workspace, int64_t workspace_bytes, void *cuda_stream);
+int64_t gdn_gated_rmsnorm_bwd_workspace(int64_t rows, int32_t dim, int32_t io_dtype);
+
+/*
+ * gdn_qkv_conv_bwd -- gradients of gdn_qkv_conv_fwd, whose arguments' names, shapes and
+ * rules it shares:
+ *
+ *   dq, dk, dv           gradients of q, k, v, io_dtype
+ *   mixed_qkv            [T, C] io_dtype, or e4m3 codes with x_scales [T, C / 32]
+ *                        (gdn_act_quantize); x_scales is NULL otherwise
+ *   conv_state_in        [N, C, K] io_dtype or NULL, the window the call started from
+ *   d_conv_state_out     [N, C, K] io_dtype or NULL: the gradient of the conv_state that
+ *                        the call returned
+ *   d_mixed_qkv          [T, C] io_dtype
+ *   d_weight             [C, K] fp32;  d_bias [C] fp32 or NULL; summed over the tokens in
+ *                        fp32, in a fixed order
+ *   d_conv_state_in      [N, C, K] io_dtype or NULL: the gradient of conv_state_in
+ *   workspace            at least gdn_qkv_conv_bwd_workspace bytes, 16-byte aligned; one
+ *                        for each call that may run at the same time
+ * With T = 0 the sums are zero and d_conv_state_in is d_conv_state_out (or zero).  No
+ * output may overlap an input or another output.  Tokens of no sequence are not written.
+ * All arithmetic is fp32.
+ */
+int gdn_qkv_conv_bwd(const void *dq, const void *dk, const void *dv, const void *mixed_qkv, const void *x_scales,
+                     const float *weight, const float *bias, const void *conv_state_in,
+                     const void *d_conv_state_out, const int32_t *cu_seqlens, int32_t num_seqs,
+                     int64_t total_tokens, int32_t kernel_size,
+                     void *d_mixed_qkv, float *d_weight, float *d_bias, void *d_conv_state_in,
+                     void *workspace, int64_t workspace_bytes, const gdn_params_t *p, void *cuda_stream);
+int64_t gdn_qkv_conv_bwd_workspace(int64_t total_tokens, int32_t kernel_size, const gdn_params_t *p);
+
+/*
+ * gdn_gate_bwd -- gradients of the gate that the _gated calls form: beta = sigmoid(b),
+ * g = -exp(A_log) softplus(a + dt_bias).
+ *
+ *   dg, dbeta       [tokens, Nv] io_dtype, as gdn_chunk_bwd writes them
+ *   a, b            [tokens, Nv] fp32;  A_log, dt_bias [Nv] fp32
+ *   da, db          [tokens, Nv] io_dtype
+ *   dA_log, ddt_bias  [Nv] fp32, summed over the tokens in fp32, in a fixed order
+ *   workspace       at least gdn_gate_bwd_workspace bytes, 16-byte aligned (NULL where
+ *                   that is 0); one for each call that may run at the same time
+ * tokens >= 0 (< 2^31), 1 <= Nv <= 65535; with tokens = 0 the sums are zero.  No output
+ * may overlap an input or another output.
+ */
+int gdn_gate_bwd(const void *dg, const void *dbeta, const float *a, const float *b, const float *A_log,
+                 const float *dt_bias, void *da, void *db, float *dA_log, float *ddt_bias, int64_t tokens,
+                 int32_t num_v_heads, int32_t io_dtype, void *workspace, int64_t workspace_bytes, void *cuda_stream);
+int64_t gdn_gate_bwd_workspace(int64_t tokens, int32_t num_v_heads);
 
 /*
  * gdn_device_status -- read and clear, in one atomic step ordered on
