@@ -12,34 +12,43 @@
 // pre is formed again from x (in io_dtype, or in 8 bits, act8.cuh), so x is all
 // that the forward pass has to keep.
 //
-// Bound by HBM: x and dy are read once, dx written once.  A thread owns 4 channels
-// over a run of tokens, which may cross sequences.  Its rows come through a ring
-// of cp.async copies that only it reads.  In registers it keeps the K - 1 inputs
-// before the token, the K - 1 gradients that later tokens still add to (so a run
-// also looks at the K - 1 tokens behind it), and its part of dw and dbias, which
-// go to the workspace once per run and are added up by a second kernel in a fixed
-// order.
+// Bound by HBM: x and dy are read once, dx written once.  A thread owns 16 bytes
+// of channels (8 bf16 or 4 fp32) over a run of tokens, which may cross sequences.
+// Its rows come through a ring of cp.async copies that only it reads.  In
+// registers it keeps the K - 1 inputs before the token, the K - 1 gradients that
+// later tokens still add to (so a run also looks at the K - 1 tokens behind it),
+// and its part of dw and dbias, which go to the workspace once per run and are
+// added up by a second kernel in a fixed order.  The arithmetic is about 13
+// multiply-adds and two MUFU operations a value, as much issue time as the traffic
+// takes, so channels go in pairs through fma.rn.f32x2.
 #include "act8.cuh"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
+#include "sm100_ptx.cuh"
 
 namespace gdn {
 namespace convbwd {
 
-constexpr int kThreads = 128;
-constexpr int E = 4;                       // channels of a thread
-constexpr int kMinRun = 32;                // tokens of a run at least
-constexpr int kMaxBlocks = 148 * 6;
+constexpr int kThreads = 64;
+constexpr int kStateThreads = 128;
+constexpr int kMinRun = 32;    // tokens of a run at least
+
+template <typename IO> struct Io;
+template <> struct Io<float> { static constexpr int E = 4, kPerSm = 8; };          // channels of a thread, blocks per SM
+template <> struct Io<__nv_bfloat16> { static constexpr int E = 8, kPerSm = 6; };
 
 struct Shape {
   int tiles;    // channel blocks
   int run;      // tokens of a run
   int blocks;   // runs
 };
-static Shape shape_of(int64_t tokens, int channels) {
+// Runs as long as one wave of resident blocks allows.
+static Shape shape_of(int64_t tokens, int channels, int io_bf16) {
   Shape s;
-  s.tiles = (channels + kThreads * E - 1) / (kThreads * E);
-  const int64_t most = kMaxBlocks / s.tiles > 0 ? kMaxBlocks / s.tiles : 1;
+  const int per = kThreads * (io_bf16 ? Io<__nv_bfloat16>::E : Io<float>::E);
+  const int wave = 148 * (io_bf16 ? Io<__nv_bfloat16>::kPerSm : Io<float>::kPerSm);
+  s.tiles = (channels + per - 1) / per;
+  const int64_t most = wave / s.tiles > 0 ? wave / s.tiles : 1;
   int64_t run = (tokens + most - 1) / most;
   if (run < kMinRun) run = kMinRun;
   s.run = (int)run;
@@ -51,30 +60,73 @@ template <int B> __device__ __forceinline__ void cp_async(uint32_t dst, const vo
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(B) : "memory");
 }
 
-template <typename IO> __device__ __forceinline__ void unpack4(const void* p, float* x);
-template <> __device__ __forceinline__ void unpack4<float>(const void* p, float* x) {
-  const float4 v = *static_cast<const float4*>(p);
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+// Two fp32 values in one register pair, and the packed operations on them.
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ float x() const { return __uint_as_float((uint32_t)v); }
+  __device__ __forceinline__ float y() const { return __uint_as_float((uint32_t)(v >> 32)); }
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
 }
-template <> __device__ __forceinline__ void unpack4<__nv_bfloat16>(const void* p, float* x) {
-  const uint2 v = *static_cast<const uint2*>(p);
-  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
-template <typename IO> __device__ __forceinline__ void store4(IO* p, const float* x);
-template <> __device__ __forceinline__ void store4<float>(float* p, const float* x) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
-template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-  __stcs(reinterpret_cast<uint2*>(p), make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b)));
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 
-// sigma(x) (1 + x (1 - sigma(x))); the exponent is clamped so that the divisor stays below the limit of __fdividef
-__device__ __forceinline__ float silu_slope(float x) {
-  const float s = __fdividef(1.f, 1.f + __expf(fminf(-x, 80.f)));
-  return s * fmaf(x, 1.f - s, 1.f);
+// 16 bytes of IO as pairs, and back
+template <typename IO> __device__ __forceinline__ void unpack(const void* p, F2* x);
+template <> __device__ __forceinline__ void unpack<float>(const void* p, F2* x) {
+  const float4 v = *static_cast<const float4*>(p);
+  x[0] = f2(v.x, v.y);
+  x[1] = f2(v.z, v.w);
 }
+template <> __device__ __forceinline__ void unpack<__nv_bfloat16>(const void* p, F2* x) {
+  const uint4 v = *static_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <typename IO> __device__ __forceinline__ void store(IO* p, const F2* x);
+template <> __device__ __forceinline__ void store<float>(float* p, const F2* x) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0].x(), x[0].y(), x[1].x(), x[1].y()));
+}
+template <> __device__ __forceinline__ void store<__nv_bfloat16>(__nv_bfloat16* p, const F2* x) {
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(ptx::pack_bf16x2(x[0].x(), x[0].y()), ptx::pack_bf16x2(x[1].x(), x[1].y()),
+                                                 ptx::pack_bf16x2(x[2].x(), x[2].y()), ptx::pack_bf16x2(x[3].x(), x[3].y())));
+}
+// E codes as pairs
+template <int E> __device__ __forceinline__ void decode(const uint8_t* p, float f, F2* x) {
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    float v[4];
+    act8::decode4(reinterpret_cast<const uint32_t*>(p)[i], f, v);
+    x[2 * i] = f2(v[0], v[1]);
+    x[2 * i + 1] = f2(v[2], v[3]);
+  }
+}
+
+// 1 / (1 + exp(-x)); exp may overflow, and then gives 0
+__device__ __forceinline__ float sigma(float x) { return __fdividef(1.f, 1.f + ptx::ex2_approx(-1.44269504f * x)); }
+// sigma(x) (1 + x (1 - sigma(x)))
+__device__ __forceinline__ F2 silu_slope(F2 x) {
+  const F2 s = f2(sigma(x.x()), sigma(x.y())), one = f2(1.f, 1.f);
+  return mul2(s, fma2(x, fma2(s, f2(-1.f, -1.f), one), one));
+}
+__device__ __forceinline__ float silu_slope(float x) { return silu_slope(f2(x, x)).x(); }
 
 // Where the gradient of channel c0's output is: dq, dk or dv, and the elements between its rows.
 template <typename IO>
@@ -114,161 +166,189 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, int64_t t
 }
 
 template <typename IO, int K, bool k8>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, Shape sh, float* part) {
-  constexpr int kX = k8 ? E : E * (int)sizeof(IO), kY = E * (int)sizeof(IO);  // bytes of a row
-  constexpr int kDepth = sizeof(IO) == 2 ? 16 : 8;
+__global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(ConvBwdArgs a, Shape sh, float* part) {
+  constexpr int E = Io<IO>::E, P = E / 2;
+  constexpr int kX = k8 ? E : 16;          // bytes of a row of x
+  constexpr int kDepth = 8;
   constexpr int H = K - 1;                 // inputs before the token
-  __shared__ __align__(16) uint8_t ring_y[kDepth][kThreads * kY];
+  constexpr int HA = H > 0 ? H : 1;
+  __shared__ __align__(16) uint8_t ring_y[kDepth][kThreads * 16];
   __shared__ __align__(16) uint8_t ring_x[kDepth][kThreads * kX];
   const int c0 = (blockIdx.x * kThreads + threadIdx.x) * E;
   if (c0 >= a.channels) return;
+  // tokens are counted from the run's first one, t0; dx of [0, own) needs dpre of [0, rows)
   const int64_t T = a.total_tokens, t0 = (int64_t)blockIdx.y * sh.run;
-  const int64_t t1 = min(T, t0 + sh.run), te = min(T, t1 + H);  // dx of [t0, t1) needs dpre of [t0, te)
+  const int own = (int)min((int64_t)sh.run, T - t0), rows = (int)min((int64_t)own + H, T - t0);
   size_t pitch;
   const IO* dy = dy_of<IO>(a, c0, pitch);
-  const uint8_t* x = static_cast<const uint8_t*>(a.x) + (size_t)c0 * (kX / E);
-  const size_t xpitch = (size_t)a.channels * (kX / E);
-  const uint8_t* xs = k8 ? a.x_scales + c0 / act8::kGroup : nullptr;
+  const uint8_t* py = reinterpret_cast<const uint8_t*>(dy + (size_t)t0 * pitch);
+  const size_t ypitch = pitch * sizeof(IO), xpitch = (size_t)a.channels * (kX / E);
+  const uint8_t* px = static_cast<const uint8_t*>(a.x) + (size_t)t0 * xpitch + (size_t)c0 * (kX / E);
   const size_t spitch = (size_t)a.channels / act8::kGroup;
-  const uint32_t by = (uint32_t)__cvta_generic_to_shared(&ring_y[0][threadIdx.x * kY]);
+  const uint8_t* ps = k8 ? a.x_scales + (size_t)t0 * spitch + c0 / act8::kGroup : nullptr;
+  IO* pdx = static_cast<IO*>(a.dx) + (size_t)t0 * a.channels + c0;
+  const uint32_t by = (uint32_t)__cvta_generic_to_shared(&ring_y[0][threadIdx.x * 16]);
   const uint32_t bx = (uint32_t)__cvta_generic_to_shared(&ring_x[0][threadIdx.x * kX]);
-  auto fetch = [&](int64_t t, int slot) {
-    if (t < te) {
-      cp_async<kY>(by + slot * (kThreads * kY), dy + (size_t)t * pitch);
-      cp_async<kX>(bx + slot * (kThreads * kX), x + (size_t)t * xpitch);
+  int fetched = 0;
+  auto fetch = [&](int slot) {
+    if (fetched < rows) {
+      cp_async<16>(by + slot * (kThreads * 16), py);
+      cp_async<kX>(bx + slot * (kThreads * kX), px);
+      py += ypitch;
+      px += xpitch;
     }
+    ++fetched;
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
 #pragma unroll
-  for (int u = 0; u + 1 < kDepth; ++u) fetch(t0 + u, u);
+  for (int u = 0; u + 1 < kDepth; ++u) fetch(u);
 
-  float w[K][E], b[E], dw[K][E], db[E], win[H > 0 ? H : 1][E], pend[H > 0 ? H : 1][E];
+  F2 w[K][P], b[P], dw[K][P], db[P], win[HA][P], pend[HA][P];
+  const F2 zero = f2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    b[e] = a.bias ? a.bias[c0 + e] : 0.f;
-    db[e] = 0.f;
+  for (int e = 0; e < P; ++e) {
+    const int c = c0 + 2 * e;
+    b[e] = a.bias ? f2(a.bias[c], a.bias[c + 1]) : zero;
+    db[e] = zero;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      w[i][e] = a.weight[(size_t)(c0 + e) * K + i];
-      dw[i][e] = 0.f;
+      w[i][e] = f2(a.weight[(size_t)c * K + i], a.weight[(size_t)(c + 1) * K + i]);
+      dw[i][e] = zero;
     }
   }
   int n = a.cu ? seq_of(a.cu, a.num_seqs, t0) : (int)(t0 / a.uniform_len);
   int64_t s0, s1;
   seq_bounds(a, n, s0, s1);
-  // win[j]: input at t - H + j; pend[j]: what is known of the gradient of the input at t - H + j
+  // win[j]: input at the token - H + j; pend[j]: what is known of the gradient of the input at the token - H + j
 #pragma unroll
   for (int j = 0; j < H; ++j) {
     const int64_t p = t0 - H + j;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      win[j][e] = p >= s0 ? x_at<IO, k8>(a, p, c0 + e) : window_at<IO>(a, n, c0 + e, (int)(K + (p - s0)));
-      pend[j][e] = 0.f;
+    for (int e = 0; e < P; ++e) {
+      float v[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        v[m] = p >= s0 ? x_at<IO, k8>(a, p, c0 + 2 * e + m) : window_at<IO>(a, n, c0 + 2 * e + m, (int)(K + (p - s0)));
+      win[j][e] = f2(v[0], v[1]);
+      pend[j][e] = zero;
     }
   }
-  // dx of token t, which no later token adds to, if it is this run's and this sequence's
-  auto emit = [&](int64_t t, float* g) {
-    if (t < t0 || t >= t1 || t < s0 || t >= s1) return;
-    if (a.dstate_out && t >= s1 - K) {
-      const IO* d = static_cast<const IO*>(a.dstate_out) + ((size_t)n * a.channels + c0) * K + (t - (s1 - K));
+  // of the sequence: its tokens [lo, hi) in this run, where it ends, and from where d_conv_state_out adds to dx
+  int lo, hi, stop, add;
+  auto enter = [&]() {
+    lo = (int)max((int64_t)0, s0 - t0);
+    stop = (int)min((int64_t)rows, s1 - t0);
+    hi = min(own, stop);
+    add = a.dstate_out ? (int)min((int64_t)rows, s1 - K - t0) : rows;
+  };
+  enter();
+  // dx of token i, which no later token adds to, if it is this run's and this sequence's
+  auto emit = [&](int i, F2* g) {
+    if (i < lo || i >= hi) return;
+    if (i >= add) {
+      const IO* d = static_cast<const IO*>(a.dstate_out) + ((size_t)n * a.channels + c0) * K + (t0 + i - (s1 - K));
 #pragma unroll
-      for (int e = 0; e < E; ++e) g[e] += to_f32(d[e * K]);
+      for (int e = 0; e < P; ++e) g[e] = add2(g[e], f2(to_f32(d[2 * e * K]), to_f32(d[(2 * e + 1) * K])));
     }
-    store4<IO>(static_cast<IO*>(a.dx) + (size_t)t * a.channels + c0, g);
+    store<IO>(pdx + (size_t)i * a.channels, g);
   };
-  // the gradients still pending when the tokens of a sequence end before token t
-  auto flush = [&](int64_t t) {
-#pragma unroll
-    for (int j = 0; j < H; ++j) emit(t - H + j, pend[j]);
-  };
-  uint32_t sc[4] = {0u, 0u, 0u, 0u};  // scale bytes of four rows, read four rows ahead
-  auto scales = [&](int64_t t) {
+  uint32_t sc[4] = {127u, 127u, 127u, 127u};  // scale bytes of four rows, read four rows ahead
+  auto scales = [&](int i) {
     if constexpr (k8) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sc[u] = t + u < te ? xs[(size_t)(t + u) * spitch] : 127u;
+      for (int u = 0; u < 4; ++u) sc[u] = i + u < rows ? ps[(size_t)(i + u) * spitch] : 127u;
     }
   };
-  scales(t0);
-  const int rows = (int)(te - t0);
-  bool open = true;  // the run's last sequence still adds to it
-  for (int i0 = 0; i0 < rows && open; i0 += 4) {
+  scales(0);
+  int i = 0;
+  while (i < rows) {
     uint32_t cur[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) cur[u] = sc[u];
-    scales(t0 + i0 + 4);
+    scales(i + 4);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u;
+    for (int u = 0; u < 4; ++u, ++i) {
       if (i >= rows) break;
-      const int64_t t = t0 + i;
-      fetch(t + kDepth - 1, (i + kDepth - 1) % kDepth);
+      fetch((i + kDepth - 1) % kDepth);
       asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
-      if (t >= s1) {  // the next sequence that has tokens begins
-        flush(t);
-        if (t >= t1) {  // it is all behind the run
-          open = false;
+      if (i >= stop) {  // the next sequence that has tokens begins
+#pragma unroll
+        for (int j = 0; j < H; ++j) emit(i - H + j, pend[j]);
+        if (i >= own) {  // it is all behind the run
+          i = rows;
           break;
         }
-        while (t >= s1 && n + 1 < a.num_seqs) {
+        while (t0 + i >= s1 && n + 1 < a.num_seqs) {
           ++n;
           seq_bounds(a, n, s0, s1);
         }
+        enter();
+        if (stop <= i) stop = rows;  // tokens of no sequence (inconsistent cu_seqlens, already reported): to the end
 #pragma unroll
         for (int j = 0; j < H; ++j)
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            win[j][e] = window_at<IO>(a, n, c0 + e, j + 1);
-            pend[j][e] = 0.f;
+          for (int e = 0; e < P; ++e) {
+            win[j][e] = f2(window_at<IO>(a, n, c0 + 2 * e, j + 1), window_at<IO>(a, n, c0 + 2 * e + 1, j + 1));
+            pend[j][e] = zero;
           }
       }
-      const bool outside = t < s0 || t >= s1;  // only with inconsistent cu_seqlens, already reported
-      float g[E], v[E], cur_g[E];
-      unpack4<IO>(&ring_y[i % kDepth][threadIdx.x * kY], g);
+      const bool outside = t0 + i < s0 || t0 + i >= s1;
+      F2 g[P], v[P], last[P];
+      unpack<IO>(&ring_y[i % kDepth][threadIdx.x * 16], g);
       if constexpr (k8)
-        act8::decode4(*reinterpret_cast<const uint32_t*>(&ring_x[i % kDepth][threadIdx.x * kX]), act8::factor(cur[u]), v);
+        decode<E>(&ring_x[i % kDepth][threadIdx.x * kX], act8::factor(cur[u]), v);
       else
-        unpack4<IO>(&ring_x[i % kDepth][threadIdx.x * kX], v);
+        unpack<IO>(&ring_x[i % kDepth][threadIdx.x * kX], v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float pre = b[e];
+      for (int e = 0; e < P; ++e) {
+        F2 pre = b[e];
 #pragma unroll
-        for (int j = 0; j < H; ++j) pre = fmaf(w[j][e], win[j][e], pre);
-        pre = fmaf(w[K - 1][e], v[e], pre);
-        const float d = outside ? 0.f : g[e] * silu_slope(pre);
-        if (t < t1) {
-          db[e] += d;
+        for (int j = 0; j < H; ++j) pre = fma2(w[j][e], win[j][e], pre);
+        pre = fma2(w[K - 1][e], v[e], pre);
+        g[e] = outside ? zero : mul2(g[e], silu_slope(pre));
 #pragma unroll
-          for (int j = 0; j < H; ++j) dw[j][e] = fmaf(d, win[j][e], dw[j][e]);
-          dw[K - 1][e] = fmaf(d, v[e], dw[K - 1][e]);
+        for (int j = 0; j < H; ++j) pend[j][e] = fma2(w[j][e], g[e], pend[j][e]);
+        last[e] = mul2(w[K - 1][e], g[e]);
+      }
+      if (i < own) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          db[e] = add2(db[e], g[e]);
+#pragma unroll
+          for (int j = 0; j < H; ++j) dw[j][e] = fma2(g[e], win[j][e], dw[j][e]);
+          dw[K - 1][e] = fma2(g[e], v[e], dw[K - 1][e]);
         }
-#pragma unroll
-        for (int j = 0; j < H; ++j) pend[j][e] = fmaf(w[j][e], d, pend[j][e]);
-        cur_g[e] = w[K - 1][e] * d;
       }
       if constexpr (H > 0) {
-        emit(t - H, pend[0]);
+        emit(i - H, pend[0]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+        for (int e = 0; e < P; ++e) {
 #pragma unroll
           for (int j = 0; j + 1 < H; ++j) {
             win[j][e] = win[j + 1][e];
             pend[j][e] = pend[j + 1][e];
           }
-          win[H - 1][e] = v[e];
-          pend[H - 1][e] = cur_g[e];
+          win[HA - 1][e] = v[e];
+          pend[HA - 1][e] = last[e];
         }
       } else {
-        emit(t, cur_g);
+        emit(i, last);
+      }
+      if (i + 1 == rows) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) emit(rows - H + j, pend[j]);
       }
     }
   }
-  if (open) flush(te);
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");  // no copy outlives the block
   float* p = part + (size_t)blockIdx.y * (K + 1) * a.channels + c0;
 #pragma unroll
-  for (int i = 0; i < K; ++i)
-    *reinterpret_cast<float4*>(p + (size_t)i * a.channels) = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-  *reinterpret_cast<float4*>(p + (size_t)K * a.channels) = make_float4(db[0], db[1], db[2], db[3]);
+  for (int j = 0; j <= K; ++j)
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const F2 s = j < K ? dw[j < K ? j : 0][e] : db[e];
+      *reinterpret_cast<float2*>(p + (size_t)j * a.channels + 2 * e) = make_float2(s.x(), s.y());
+    }
 }
 
 // dw[c, i] and dbias[c] from the runs' parts [run][K + 1][channels]: 32 columns by 8 shares of the runs
@@ -292,8 +372,8 @@ __global__ void __launch_bounds__(256) conv_weight_kernel(const float* __restric
 // position p = j - K: the taps i < j of the first tokens meet it, and the new conv_state still holds it where the
 // sequence is shorter than K.
 template <typename IO, int K, bool k8>
-__global__ void __launch_bounds__(kThreads) conv_state_bwd_kernel(ConvBwdArgs a) {
-  const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kStateThreads) conv_state_bwd_kernel(ConvBwdArgs a) {
+  const int64_t idx = (int64_t)blockIdx.x * kStateThreads + threadIdx.x;
   if (idx >= (int64_t)a.num_seqs * a.channels) return;
   const int n = (int)(idx / a.channels), c = (int)(idx % a.channels);
   int64_t s0, s1;
@@ -328,7 +408,7 @@ __global__ void __launch_bounds__(kThreads) conv_state_bwd_kernel(ConvBwdArgs a)
 
 template <typename IO, int K, bool k8>
 static cudaError_t launch_k(const ConvBwdArgs& a, float* part, cudaStream_t s) {
-  const Shape sh = shape_of(a.total_tokens, a.channels);
+  const Shape sh = shape_of(a.total_tokens, a.channels, sizeof(IO) == 2);
   cudaError_t e;
   if (sh.blocks > 0) {
     conv_bwd_kernel<IO, K, k8><<<dim3(sh.tiles, sh.blocks), kThreads, 0, s>>>(a, sh, part);
@@ -337,7 +417,7 @@ static cudaError_t launch_k(const ConvBwdArgs& a, float* part, cudaStream_t s) {
   conv_weight_kernel<<<dim3((a.channels + 31) / 32, K + 1), 256, 0, s>>>(part, sh.blocks, a.channels, K, a.dw, a.db);
   if ((e = cudaGetLastError()) != cudaSuccess || !a.dstate_in) return e;
   const int64_t threads = (int64_t)a.num_seqs * a.channels;
-  conv_state_bwd_kernel<IO, K, k8><<<(unsigned int)((threads + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+  conv_state_bwd_kernel<IO, K, k8><<<(unsigned int)((threads + kStateThreads - 1) / kStateThreads), kStateThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <typename IO, int K>
@@ -351,8 +431,8 @@ static cudaError_t launch_any(const ConvBwdArgs& a, int io_bf16, float* part, cu
 
 }  // namespace convbwd
 
-int64_t conv_bwd_workspace(int64_t tokens, int channels, int ksize) {
-  return (int64_t)convbwd::shape_of(tokens, channels).blocks * (ksize + 1) * channels * (int64_t)sizeof(float);
+int64_t conv_bwd_workspace(int64_t tokens, int channels, int ksize, int io_bf16) {
+  return (int64_t)convbwd::shape_of(tokens, channels, io_bf16).blocks * (ksize + 1) * channels * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_conv_bwd(const ConvBwdArgs& a, int io_bf16, float* part, cudaStream_t s) {

@@ -84,7 +84,7 @@ struct Kept {
 };
 
 template <typename IO, int DIM, bool kO8, bool kZ8>
-__global__ void __launch_bounds__(kThreads) gated_rmsnorm_bwd_kernel(NormBwdArgs p, float* part) {
+__global__ void __launch_bounds__(kThreads, 4) gated_rmsnorm_bwd_kernel(NormBwdArgs p, float* part) {
   constexpr int E = Vec<IO>::N, L = DIM / E, G = kThreads / L;
   __shared__ float sum[G][DIM];
   const int lr = threadIdx.x % L, grp = threadIdx.x / L;

@@ -640,7 +640,8 @@ GDN_API int64_t gdn_qkv_conv_bwd_workspace(int64_t total_tokens, int32_t kernel_
   const int rc = check_params(p);
   if (rc) return rc;
   if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31) || kernel_size < 1 || kernel_size > 4) return GDN_ERR_SHAPE;
-  return gdn::conv_bwd_workspace(total_tokens, 2 * p->num_qk_heads * p->head_k_dim + p->num_v_heads * p->head_v_dim, kernel_size);
+  return gdn::conv_bwd_workspace(total_tokens, 2 * p->num_qk_heads * p->head_k_dim + p->num_v_heads * p->head_v_dim, kernel_size,
+                                 p->io_dtype == GDN_DTYPE_BF16);
 }
 
 GDN_API int gdn_qkv_conv_bwd(const void* dq, const void* dk, const void* dv, const void* mixed_qkv, const void* x_scales,

@@ -43,7 +43,7 @@ cudaError_t launch_act_dequantize(const uint8_t* codes, const uint8_t* scales, v
 // Gradients of the gated RMSNorm, of the conv and of the gate; `part`: workspace of the bytes that go before.
 int64_t gated_rmsnorm_bwd_workspace(int64_t rows, int dim, int io_bf16);
 cudaError_t launch_gated_rmsnorm_bwd(const NormBwdArgs& p, int dim, int io_bf16, float* part, cudaStream_t s);
-int64_t conv_bwd_workspace(int64_t tokens, int channels, int ksize);
+int64_t conv_bwd_workspace(int64_t tokens, int channels, int ksize, int io_bf16);
 cudaError_t launch_conv_bwd(const ConvBwdArgs& a, int io_bf16, float* part, cudaStream_t s);
 int64_t gate_bwd_workspace(int64_t tokens, int nv);
 cudaError_t launch_gate_bwd(const GateBwdArgs& p, int io_bf16, float* part, cudaStream_t s);
