@@ -21,7 +21,10 @@
 // added up by a second kernel in a fixed order.  The arithmetic is about 13
 // multiply-adds and two MUFU operations a value, as much issue time as the traffic
 // takes, so channels go in pairs through fma.rn.f32x2.
+#include <type_traits>
+
 #include "act8.cuh"
+#include "f32x2.cuh"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
 #include "sm100_ptx.cuh"
@@ -60,33 +63,6 @@ template <int B> __device__ __forceinline__ void cp_async(uint32_t dst, const vo
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(B) : "memory");
 }
 
-// Two fp32 values in one register pair, and the packed operations on them.
-struct F2 {
-  uint64_t v;
-  __device__ __forceinline__ float x() const { return __uint_as_float((uint32_t)v); }
-  __device__ __forceinline__ float y() const { return __uint_as_float((uint32_t)(v >> 32)); }
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-
 // 16 bytes of IO as pairs, and back
 template <typename IO> __device__ __forceinline__ void unpack(const void* p, F2* x);
 template <> __device__ __forceinline__ void unpack<float>(const void* p, F2* x) {
@@ -118,15 +94,6 @@ template <int E> __device__ __forceinline__ void decode(const uint8_t* p, float 
     x[2 * i + 1] = f2(v[2], v[3]);
   }
 }
-
-// 1 / (1 + exp(-x)); exp may overflow, and then gives 0
-__device__ __forceinline__ float sigma(float x) { return __fdividef(1.f, 1.f + ptx::ex2_approx(-1.44269504f * x)); }
-// sigma(x) (1 + x (1 - sigma(x)))
-__device__ __forceinline__ F2 silu_slope(F2 x) {
-  const F2 s = f2(sigma(x.x()), sigma(x.y())), one = f2(1.f, 1.f);
-  return mul2(s, fma2(x, fma2(s, f2(-1.f, -1.f), one), one));
-}
-__device__ __forceinline__ float silu_slope(float x) { return silu_slope(f2(x, x)).x(); }
 
 // Where the gradient of channel c0's output is: dq, dk or dv, and the elements between its rows.
 template <typename IO>
@@ -236,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
   // of the sequence: its tokens [lo, hi) in this run, where it ends, and from where d_conv_state_out adds to dx
   int lo, hi, stop, add;
   auto enter = [&]() {
-    lo = (int)max((int64_t)0, s0 - t0);
+    lo = (int)min((int64_t)rows, max((int64_t)0, s0 - t0));
     stop = (int)min((int64_t)rows, s1 - t0);
     hi = min(own, stop);
     add = a.dstate_out ? (int)min((int64_t)rows, s1 - K - t0) : rows;
@@ -259,6 +226,60 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
       for (int u = 0; u < 4; ++u) sc[u] = i + u < rows ? ps[(size_t)(i + u) * spitch] : 127u;
     }
   };
+  // Token i: its share of dw and dbias, of the pending gradients, and dx of token i - H.  kInside: the token is
+  // this run's and its sequence's, and so is token i - H, which d_conv_state_out does not add to.
+  auto row = [&](int i, uint32_t scale, auto inside) {
+    constexpr bool kInside = decltype(inside)::value;
+    fetch((i + kDepth - 1) % kDepth);
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
+    F2 g[P], v[P], last[P];
+    unpack<IO>(&ring_y[i % kDepth][threadIdx.x * 16], g);
+    if constexpr (k8)
+      decode<E>(&ring_x[i % kDepth][threadIdx.x * kX], act8::factor(scale), v);
+    else
+      unpack<IO>(&ring_x[i % kDepth][threadIdx.x * kX], v);
+    if (!kInside && (i < lo || i >= stop)) {  // of no sequence (inconsistent cu_seqlens, already reported)
+#pragma unroll
+      for (int e = 0; e < P; ++e) g[e] = zero;
+    }
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      F2 pre = b[e];
+#pragma unroll
+      for (int j = 0; j < H; ++j) pre = fma2(w[j][e], win[j][e], pre);
+      pre = fma2(w[K - 1][e], v[e], pre);
+      g[e] = mul2(g[e], silu_slope(pre));
+#pragma unroll
+      for (int j = 0; j < H; ++j) pend[j][e] = fma2(w[j][e], g[e], pend[j][e]);
+      last[e] = mul2(w[K - 1][e], g[e]);
+    }
+    if (kInside || i < own) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        db[e] = add2(db[e], g[e]);
+#pragma unroll
+        for (int j = 0; j < H; ++j) dw[j][e] = fma2(g[e], win[j][e], dw[j][e]);
+        dw[K - 1][e] = fma2(g[e], v[e], dw[K - 1][e]);
+      }
+    }
+    F2* out = H > 0 ? pend[0] : last;
+    if constexpr (kInside)
+      store<IO>(pdx + (size_t)(i - H) * a.channels, out);
+    else
+      emit(i - H, out);
+    if constexpr (H > 0) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+#pragma unroll
+        for (int j = 0; j + 1 < H; ++j) {
+          win[j][e] = win[j + 1][e];
+          pend[j][e] = pend[j + 1][e];
+        }
+        win[HA - 1][e] = v[e];
+        pend[HA - 1][e] = last[e];
+      }
+    }
+  };
   scales(0);
   int i = 0;
   while (i < rows) {
@@ -266,78 +287,39 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
 #pragma unroll
     for (int u = 0; u < 4; ++u) cur[u] = sc[u];
     scales(i + 4);
+    if (i >= lo + H && i + 4 <= hi && i + 3 - H < add) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u, ++i) {
-      if (i >= rows) break;
-      fetch((i + kDepth - 1) % kDepth);
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
-      if (i >= stop) {  // the next sequence that has tokens begins
+      for (int u = 0; u < 4; ++u) row(i + u, cur[u], std::true_type{});
+      i += 4;
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < 4 && i < rows; ++u, ++i) {
+        if (i >= stop) {  // the next sequence that has tokens begins
 #pragma unroll
-        for (int j = 0; j < H; ++j) emit(i - H + j, pend[j]);
-        if (i >= own) {  // it is all behind the run
-          i = rows;
-          break;
-        }
-        while (t0 + i >= s1 && n + 1 < a.num_seqs) {
-          ++n;
-          seq_bounds(a, n, s0, s1);
-        }
-        enter();
-        if (stop <= i) stop = rows;  // tokens of no sequence (inconsistent cu_seqlens, already reported): to the end
-#pragma unroll
-        for (int j = 0; j < H; ++j)
-#pragma unroll
-          for (int e = 0; e < P; ++e) {
-            win[j][e] = f2(window_at<IO>(a, n, c0 + 2 * e, j + 1), window_at<IO>(a, n, c0 + 2 * e + 1, j + 1));
-            pend[j][e] = zero;
+          for (int j = 0; j < H; ++j) emit(i - H + j, pend[j]);
+          if (i >= own) {  // it is all behind the run
+            i = rows + 1;
+            break;
           }
-      }
-      const bool outside = t0 + i < s0 || t0 + i >= s1;
-      F2 g[P], v[P], last[P];
-      unpack<IO>(&ring_y[i % kDepth][threadIdx.x * 16], g);
-      if constexpr (k8)
-        decode<E>(&ring_x[i % kDepth][threadIdx.x * kX], act8::factor(cur[u]), v);
-      else
-        unpack<IO>(&ring_x[i % kDepth][threadIdx.x * kX], v);
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        F2 pre = b[e];
-#pragma unroll
-        for (int j = 0; j < H; ++j) pre = fma2(w[j][e], win[j][e], pre);
-        pre = fma2(w[K - 1][e], v[e], pre);
-        g[e] = outside ? zero : mul2(g[e], silu_slope(pre));
-#pragma unroll
-        for (int j = 0; j < H; ++j) pend[j][e] = fma2(w[j][e], g[e], pend[j][e]);
-        last[e] = mul2(w[K - 1][e], g[e]);
-      }
-      if (i < own) {
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          db[e] = add2(db[e], g[e]);
-#pragma unroll
-          for (int j = 0; j < H; ++j) dw[j][e] = fma2(g[e], win[j][e], dw[j][e]);
-          dw[K - 1][e] = fma2(g[e], v[e], dw[K - 1][e]);
-        }
-      }
-      if constexpr (H > 0) {
-        emit(i - H, pend[0]);
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-#pragma unroll
-          for (int j = 0; j + 1 < H; ++j) {
-            win[j][e] = win[j + 1][e];
-            pend[j][e] = pend[j + 1][e];
+          while (t0 + i >= s1 && n + 1 < a.num_seqs) {
+            ++n;
+            seq_bounds(a, n, s0, s1);
           }
-          win[HA - 1][e] = v[e];
-          pend[HA - 1][e] = last[e];
-        }
-      } else {
-        emit(i, last);
-      }
-      if (i + 1 == rows) {
+          enter();
 #pragma unroll
-        for (int j = 0; j < H; ++j) emit(rows - H + j, pend[j]);
+          for (int j = 0; j < H; ++j)
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              win[j][e] = f2(window_at<IO>(a, n, c0 + 2 * e, j + 1), window_at<IO>(a, n, c0 + 2 * e + 1, j + 1));
+              pend[j][e] = zero;
+            }
+        }
+        row(i, u == 0 ? cur[0] : u == 1 ? cur[1] : u == 2 ? cur[2] : cur[3], std::false_type{});
       }
+    }
+    if (i == rows) {
+#pragma unroll
+      for (int j = 0; j < H; ++j) emit(rows - H + j, pend[j]);
     }
   }
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");  // no copy outlives the block

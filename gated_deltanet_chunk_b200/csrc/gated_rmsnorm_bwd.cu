@@ -11,6 +11,7 @@
 // stays in registers until the block's groups are joined in shared memory; a
 // second kernel joins the blocks, in a fixed order.
 #include "act8.cuh"
+#include "f32x2.cuh"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
 
@@ -18,8 +19,9 @@ namespace gdn {
 namespace rmsbwd {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;            // rows of a lane group in flight
-constexpr int kMaxBlocks = 148 * 4;   // one wave at four blocks per SM
+constexpr int kUnroll = 2;               // rows of a lane group in flight
+constexpr int kPerSm = 3;               // blocks per SM
+constexpr int kMaxBlocks = 148 * kPerSm;  // one wave
 
 template <typename IO> struct Vec;  // 16 bytes of IO
 template <> struct Vec<float> {
@@ -84,70 +86,96 @@ struct Kept {
 };
 
 template <typename IO, int DIM, bool kO8, bool kZ8>
-__global__ void __launch_bounds__(kThreads, 4) gated_rmsnorm_bwd_kernel(NormBwdArgs p, float* part) {
+__global__ void __launch_bounds__(kThreads, kPerSm) gated_rmsnorm_bwd_kernel(NormBwdArgs p, float* part) {
   constexpr int E = Vec<IO>::N, L = DIM / E, G = kThreads / L;
   __shared__ float sum[G][DIM];
   const int lr = threadIdx.x % L, grp = threadIdx.x / L;
-  float wv[E], dw[E];
+  constexpr int P = E / 2;
+  F2 wv[P], dw[P];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    wv[e] = p.w[lr * E + e];
-    dw[e] = 0.f;
+  for (int e = 0; e < P; ++e) {
+    wv[e] = f2(p.w[lr * E + 2 * e], p.w[lr * E + 2 * e + 1]);
+    dw[e] = f2(0.f, 0.f);
   }
   const int64_t step = (int64_t)G * gridDim.x;
-  // every lane of a warp takes the same number of passes (the shuffles need them all)
-  for (int64_t b0 = (int64_t)blockIdx.x * G; b0 < p.rows; b0 += step * kUnroll) {
-    uint4 dyw[kUnroll];
-    Kept<IO, kO8> ow[kUnroll];
-    Kept<IO, kZ8> zw[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = b0 + u * step + grp;
-      const size_t at = (size_t)(r < p.rows ? r : 0) * DIM + lr * E;
+  uint4 dyw[kUnroll];
+  Kept<IO, kO8> ow[kUnroll];
+  Kept<IO, kZ8> zw[kUnroll];
+  auto load = [&](int64_t b0, int u) {
+    const int64_t r = b0 + u * step + grp;
+    if (r < p.rows) {
+      const size_t at = (size_t)r * DIM + lr * E;
       dyw[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const IO*>(p.dy) + at));
       ow[u].load(p.o, p.o_scales, at);
       zw[u].load(p.z, p.z_scales, at);
     }
+  };
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) load((int64_t)blockIdx.x * G, u);
+  // every lane of a warp takes the same number of passes (the shuffles need them all)
+  for (int64_t b0 = (int64_t)blockIdx.x * G; b0 < p.rows; b0 += step * kUnroll) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t r = b0 + u * step + grp;
-      float dy[E], o[E], z[E], dn[E];
-      Vec<IO>::unpack(dyw[u], dy);
-      ow[u].unpack(o);
-      zw[u].unpack(z);
-      float ss = 0.f, c = 0.f;
+      const bool valid = r < p.rows;
+      F2 dy[P], o[P], z[P];
+      float x[E];
+      Vec<IO>::unpack(dyw[u], x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) ss = fmaf(o[e], o[e], ss);
+      for (int e = 0; e < P; ++e) dy[e] = f2(x[2 * e], x[2 * e + 1]);
+      ow[u].unpack(x);
+#pragma unroll
+      for (int e = 0; e < P; ++e) o[e] = f2(x[2 * e], x[2 * e + 1]);
+      zw[u].unpack(x);
+#pragma unroll
+      for (int e = 0; e < P; ++e) z[e] = f2(x[2 * e], x[2 * e + 1]);
+      load(b0 + step * kUnroll, u);  // comes in while this row and the next are worked on
+      F2 acc = f2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < P; ++e) acc = fma2(o[e], o[e], acc);
+      float ss = acc.x() + acc.y();
 #pragma unroll
       for (int m = L / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
       const float inv = rsqrtf(ss * (1.f / DIM) + p.eps);
-      const bool valid = r < p.rows;
+      const F2 inv2 = f2(inv, inv), one = f2(1.f, 1.f), neg = f2(-1.f, -1.f);
+      F2 dn[P];
+      acc = f2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float n = o[e] * inv;
-        // the exponent is clamped so that the divisor stays below the limit of __fdividef
-        const float sig = __fdividef(1.f, 1.f + __expf(fminf(-z[e], 80.f))), s = z[e] * sig;
-        const float g = dy[e] * wv[e];
-        dn[e] = g * s;
-        if (valid) dw[e] = fmaf(dy[e] * n, s, dw[e]);
-        z[e] = g * n * fmaf(s, 1.f - sig, sig);  // sig (1 + z (1 - sig))
+      for (int e = 0; e < P; ++e) {
+        const F2 n = mul2(o[e], inv2), sig = sigmoid2(z[e]), s = mul2(z[e], sig), g = mul2(dy[e], wv[e]);
+        dn[e] = mul2(g, s);
+        if (valid) dw[e] = fma2(mul2(dy[e], n), s, dw[e]);
+        z[e] = mul2(mul2(g, n), fma2(s, fma2(sig, neg, one), sig));  // sig (1 + z (1 - sig))
         o[e] = n;
-        c = fmaf(dn[e], n, c);
+        acc = fma2(dn[e], n, acc);
       }
+      float c = acc.x() + acc.y();
 #pragma unroll
       for (int m = L / 2; m > 0; m >>= 1) c += __shfl_xor_sync(0xffffffffu, c, m);
-      c *= 1.f / DIM;
+      c *= -1.f / DIM;
       if (valid) {
         const size_t at = (size_t)r * DIM + lr * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = inv * fmaf(-o[e], c, dn[e]);
-        Vec<IO>::store(static_cast<IO*>(p.d_o) + at, o);
-        Vec<IO>::store(static_cast<IO*>(p.d_z) + at, z);
+        for (int e = 0; e < P; ++e) {
+          const F2 d = mul2(inv2, fma2(o[e], f2(c, c), dn[e]));
+          x[2 * e] = d.x();
+          x[2 * e + 1] = d.y();
+        }
+        Vec<IO>::store(static_cast<IO*>(p.d_o) + at, x);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          x[2 * e] = z[e].x();
+          x[2 * e + 1] = z[e].y();
+        }
+        Vec<IO>::store(static_cast<IO*>(p.d_z) + at, x);
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) sum[grp][lr * E + e] = dw[e];
+  for (int e = 0; e < P; ++e) {
+    sum[grp][lr * E + 2 * e] = dw[e].x();
+    sum[grp][lr * E + 2 * e + 1] = dw[e].y();
+  }
   __syncthreads();
   if (threadIdx.x < DIM) {
     float s = 0.f;
