@@ -141,7 +141,10 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
   constexpr int HA = H > 0 ? H : 1;
   __shared__ __align__(16) uint8_t ring_y[kDepth][kThreads * 16];
   __shared__ __align__(16) uint8_t ring_x[kDepth][kThreads * kX];
+  // scale bytes of 32 rows for a warp's channels (32 E of them: E groups)
+  __shared__ __align__(4) uint8_t sbuf[k8 ? kThreads / 32 : 1][32][E];
   const int c0 = (blockIdx.x * kThreads + threadIdx.x) * E;
+  const unsigned int lanes = __ballot_sync(0xffffffffu, c0 < a.channels);
   if (c0 >= a.channels) return;
   // tokens are counted from the run's first one, t0; dx of [0, own) needs dpre of [0, rows)
   const int64_t T = a.total_tokens, t0 = (int64_t)blockIdx.y * sh.run;
@@ -152,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
   const size_t ypitch = pitch * sizeof(IO), xpitch = (size_t)a.channels * (kX / E);
   const uint8_t* px = static_cast<const uint8_t*>(a.x) + (size_t)t0 * xpitch + (size_t)c0 * (kX / E);
   const size_t spitch = (size_t)a.channels / act8::kGroup;
-  const uint8_t* ps = k8 ? a.x_scales + (size_t)t0 * spitch + c0 / act8::kGroup : nullptr;
   IO* pdx = static_cast<IO*>(a.dx) + (size_t)t0 * a.channels + c0;
   const uint32_t by = (uint32_t)__cvta_generic_to_shared(&ring_y[0][threadIdx.x * 16]);
   const uint32_t bx = (uint32_t)__cvta_generic_to_shared(&ring_x[0][threadIdx.x * kX]);
@@ -219,13 +221,22 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
     }
     store<IO>(pdx + (size_t)i * a.channels, g);
   };
-  uint32_t sc[4] = {127u, 127u, 127u, 127u};  // scale bytes of four rows, read four rows ahead
+  // before row i, a multiple of 32: the scale bytes of the 32 rows from it
   auto scales = [&](int i) {
     if constexpr (k8) {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, m = __popc(lanes);
+      const int first = (c0 - lane * E) / act8::kGroup;  // of the warp's groups; there are an even number of all
+      __syncwarp(lanes);
+      for (int r = lane; r < 32 && i + r < rows; r += m) {
+        const uint8_t* src = a.x_scales + (size_t)(t0 + i + r) * spitch + first;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sc[u] = i + u < rows ? ps[(size_t)(i + u) * spitch] : 127u;
+        for (int j = 0; j < E; j += 2)
+          if (first + j < (int)spitch) *reinterpret_cast<uint16_t*>(&sbuf[warp][r][j]) = *reinterpret_cast<const uint16_t*>(src + j);
+      }
+      __syncwarp(lanes);
     }
   };
+  auto scale_of = [&](int i) { return k8 ? (uint32_t)sbuf[threadIdx.x / 32][i & 31][(threadIdx.x & 31) * E / act8::kGroup] : 127u; };
   // Token i: its share of dw and dbias, of the pending gradients, and dx of token i - H.  kInside: the token is
   // this run's and its sequence's, and so is token i - H, which d_conv_state_out does not add to.
   auto row = [&](int i, uint32_t scale, auto inside) {
@@ -280,42 +291,37 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
       }
     }
   };
-  scales(0);
   int i = 0;
   while (i < rows) {
-    uint32_t cur[4];
+    for (const int to = min(hi - 4, add - 4 + H); i >= lo + H && i <= to; i += 4) {
+      if ((i & 31) == 0) scales(i);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) cur[u] = sc[u];
-    scales(i + 4);
-    if (i >= lo + H && i + 4 <= hi && i + 3 - H < add) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) row(i + u, cur[u], std::true_type{});
-      i += 4;
-    } else {
+      for (int u = 0; u < 4; ++u) row(i + u, scale_of(i + u), std::true_type{});
+    }
+    if (i < rows && (i & 31) == 0) scales(i);
 #pragma unroll 1
-      for (int u = 0; u < 4 && i < rows; ++u, ++i) {
-        if (i >= stop) {  // the next sequence that has tokens begins
+    for (int u = 0; u < 4 && i < rows; ++u, ++i) {
+      if (i >= stop) {  // the next sequence that has tokens begins
 #pragma unroll
-          for (int j = 0; j < H; ++j) emit(i - H + j, pend[j]);
-          if (i >= own) {  // it is all behind the run
-            i = rows + 1;
-            break;
-          }
-          while (t0 + i >= s1 && n + 1 < a.num_seqs) {
-            ++n;
-            seq_bounds(a, n, s0, s1);
-          }
-          enter();
-#pragma unroll
-          for (int j = 0; j < H; ++j)
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-              win[j][e] = f2(window_at<IO>(a, n, c0 + 2 * e, j + 1), window_at<IO>(a, n, c0 + 2 * e + 1, j + 1));
-              pend[j][e] = zero;
-            }
+        for (int j = 0; j < H; ++j) emit(i - H + j, pend[j]);
+        if (i >= own) {  // it is all behind the run
+          i = rows + 1;
+          break;
         }
-        row(i, u == 0 ? cur[0] : u == 1 ? cur[1] : u == 2 ? cur[2] : cur[3], std::false_type{});
+        while (t0 + i >= s1 && n + 1 < a.num_seqs) {
+          ++n;
+          seq_bounds(a, n, s0, s1);
+        }
+        enter();
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            win[j][e] = f2(window_at<IO>(a, n, c0 + 2 * e, j + 1), window_at<IO>(a, n, c0 + 2 * e + 1, j + 1));
+            pend[j][e] = zero;
+          }
       }
+      row(i, scale_of(i), std::false_type{});
     }
     if (i == rows) {
 #pragma unroll

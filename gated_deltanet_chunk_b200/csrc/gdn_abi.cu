@@ -661,6 +661,7 @@ GDN_API int gdn_qkv_conv_bwd(const void* dq, const void* dk, const void* dv, con
   for (const void* ptr : ptrs)
     if (ptr && !aligned16(ptr)) return GDN_ERR_ALIGN;
   if ((bias && !aligned4(bias)) || !aligned4(d_weight) || (d_bias && !aligned4(d_bias))) return GDN_ERR_ALIGN;
+  if (x_scales && (reinterpret_cast<uintptr_t>(x_scales) & 1u)) return GDN_ERR_ALIGN;
   gdn::ConvBwdArgs a{};
   a.nqk = p->num_qk_heads; a.nv = p->num_v_heads; a.dk = p->head_k_dim; a.dv = p->head_v_dim;
   a.channels = 2 * a.nqk * a.dk + a.nv * a.dv;

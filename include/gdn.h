@@ -468,7 +468,8 @@ int64_t gdn_gated_rmsnorm_bwd_workspace(int64_t rows, int32_t dim, int32_t io_dt
  *
  *   dq, dk, dv           gradients of q, k, v, io_dtype
  *   mixed_qkv            [T, C] io_dtype, or e4m3 codes with x_scales [T, C / 32]
- *                        (gdn_act_quantize); x_scales is NULL otherwise
+ *                        (gdn_act_quantize), 2-byte aligned; x_scales is NULL
+ *                        otherwise
  *   conv_state_in        [N, C, K] io_dtype or NULL, the window the call started from
  *   d_conv_state_out     [N, C, K] io_dtype or NULL: the gradient of the conv_state that
  *                        the call returned
