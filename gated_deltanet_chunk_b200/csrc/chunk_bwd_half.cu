@@ -20,6 +20,8 @@
 // a product of contractions, times k_i), |W| <= 2, |q_r . k_i| <= 1.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "chunk_bwd.cuh"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
@@ -661,47 +663,50 @@ __global__ void __launch_bounds__(kStateThreads, 2) states_half_kernel(BwdArgs a
 }
 
 // ------------------------------------------------------------------ 3. gradients
-// One block of 16 warps per (slot, qk-head).  Its items are the 64-column halves of Dv of its v-heads: while
-// one is worked on, the next one's tiles come in by cp.async.
+// One block of 16 warps per (slot, qk-head), which takes its v-heads in turn.  A v-head's tiles come in by
+// cp.async, and each buffer is filled for the next v-head as soon as this one is done with it.  Their rows' own
+// factors are first made one for the tile (exactly, but for what underflows beside the tile's largest element),
+// so that the products need no scaling on the way.
 
 constexpr int kGradThreads = 512;
 
 template <int DK, int DV>
 struct GradSmem {
-  static constexpr int DP = DK + 8;
-  // one stage: 64 rows of S^T and of dS'^T, of V'^T and dV'^T, and 64 columns of dO (raw bf16, then fp16)
-  static constexpr size_t kS = 0;
-  static constexpr size_t kD = kS + 2 * 64 * DP;
-  static constexpr size_t kV = kD + 2 * 64 * DP;
-  static constexpr size_t kX = kV + 2 * 64 * HP;
-  static constexpr size_t kO = kX + 2 * 64 * HP;
-  static constexpr size_t kStage = kO + 2 * C * HP;
-  // what belongs to a v-head, two of them: T and the record's floats up to fKw
-  static constexpr size_t kT = 0;
-  static constexpr size_t kF = kT + 2 * C * HP;
-  static constexpr size_t kHead = kF + 4 * Rec<DK, DV>::fKw;
-  static constexpr size_t kStages = 0;
-  static constexpr size_t kHeads = kStages + 2 * kStage;
-  static constexpr size_t kK = kHeads + 2 * kHead;            // fp16 [C][DP] K16, columns by swap32
+  static constexpr int DP = DK + 8, VP = DV + 8;
+  static constexpr size_t kS = 0;                             // fp16 [DV][DP] S^T
+  static constexpr size_t kD = kS + 2 * DV * DP;              // fp16 [DV][DP] dS'^T
+  static constexpr size_t kV = kD + 2 * DV * DP;              // fp16 [DV][HP] V'^T
+  static constexpr size_t kX = kV + 2 * DV * HP;              // fp16 [DV][HP] dV'^T
+  static constexpr size_t kO = kX + 2 * DV * HP;              // [C][VP] dO: bf16, then fp16
+  static constexpr size_t kT = kO + 2 * C * VP;               // fp16 [C][HP] T
+  static constexpr size_t kF = kT + 2 * C * HP;               // two of: the record's floats up to fKw
+  static constexpr size_t kFBytes = 4 * Rec<DK, DV>::fKw;
+  static constexpr size_t kK = kF + 2 * kFBytes;              // fp16 [C][DP] K16, columns by swap32
   static constexpr size_t kQ = kK + 2 * C * DP;               // fp16 [C][DP] Q16, the same
-  static constexpr size_t kDx = kQ + 2 * C * DP;              // fp16 [64][HP] dX^T
-  static constexpr size_t kN = kDx + 2 * 64 * HP;             // fp16 [C][HP] N
+  static constexpr size_t kDx = kQ + 2 * C * DP;              // fp16 [DV][HP] dX^T
+  static constexpr size_t kN = kDx + 2 * DV * HP;             // fp16 [C][HP] N
   static constexpr size_t kB = kN + 2 * C * HP;               // fp16 [C][HP] B
-  static constexpr size_t kFac = kB + 2 * C * HP;             // fp16 [5][DV] column factors, see below
-  static constexpr size_t kFs = kFac + 10 * DV;               // fp32 [8] their common factors
-  static constexpr size_t kQf = kFs + 32;                     // fp32 [4][C] kf, qf, and their shares of the norm
+  static constexpr size_t kQf = kB + 2 * C * HP;              // fp32 [4][C] kf, qf, and their shares of the norm
   static constexpr size_t kE = kQf + 16 * C;                  // fp32 [2][C] e, l
   static constexpr size_t kRed = kE + 8 * C;                  // fp32 [4][3][C] row sums by column block; [4][2][C] at the end
   static constexpr size_t kCol = kRed + 48 * C;               // fp32 [4][C] column sums by row block
   static constexpr size_t kDot = kCol + 16 * C;               // fp32 [16] <S, dS'> by warp
   static constexpr size_t kBytes = kDot + 64;
-  static_assert(kStage % 16 == 0 && kHead % 16 == 0 && kBytes <= 232448, "shared memory budget");
+  static_assert(kF % 16 == 0 && kFBytes % 16 == 0 && kBytes <= 232448, "shared memory budget");
 };
 
 // Column d of a row of 32 stands at swap32(d): lane t's columns 8 b + 2 t, + 1 of the states' accumulators
-// (b = 0..3) are next to one another, so that they were stored as one vector.  Pairs stay pairs.
+// (b = 0..3) are next to one another, so that they were stored as one vector.  Pairs stay pairs, and the swap is
+// its own inverse.
 __device__ __forceinline__ int swap32(int d) { return (d & ~31) | (((d >> 1) & 3) << 3) | (((d >> 3) & 3) << 1) | (d & 1); }
-__device__ __forceinline__ int unswap32(int p) { return (p & ~31) | (((p >> 1) & 3) << 3) | (((p >> 3) & 3) << 1) | (p & 1); }
+
+// The largest of n factors (powers of two, n = 64 or 128), by a warp, and its inverse
+__device__ __forceinline__ float top_factor(const float* f, int n, int lane) {
+  uint32_t top = 0u;
+  for (int i = lane; i < n; i += 32) top = max(top, __float_as_uint(f[i]));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+}
+__device__ __forceinline__ uint32_t half2_of(float x) { return pack2(x, x); }
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) {
@@ -710,45 +715,62 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
   using QR = QkRec<DK>;
   extern __shared__ __align__(16) uint8_t sm[];
   constexpr int NK = DK / 32;       // 8-column tiles of a warp's quarter of Dk
-  constexpr int HALVES = DV / 64;
+  constexpr int KV = DV / 16;       // steps over the columns of Dv
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int hq = blockIdx.y, group = a.nv / a.nqk, h0 = hq * group;
   const int64_t slot = blockIdx.x;
   int64_t c0, end;
   if (!bwd::chunk_at(a, slot, c0, end)) return;
+  const int rows = (int)min((int64_t)C, end - c0);
+  __half *S = reinterpret_cast<__half*>(sm + L::kS), *D = reinterpret_cast<__half*>(sm + L::kD);
+  __half *V = reinterpret_cast<__half*>(sm + L::kV), *X = reinterpret_cast<__half*>(sm + L::kX);
+  __half *O = reinterpret_cast<__half*>(sm + L::kO), *T = reinterpret_cast<__half*>(sm + L::kT);
   __half *K = reinterpret_cast<__half*>(sm + L::kK), *Q = reinterpret_cast<__half*>(sm + L::kQ);
   __half *Dx = reinterpret_cast<__half*>(sm + L::kDx), *N = reinterpret_cast<__half*>(sm + L::kN);
-  __half *B = reinterpret_cast<__half*>(sm + L::kB), *fac = reinterpret_cast<__half*>(sm + L::kFac);
-  float *fs = reinterpret_cast<float*>(sm + L::kFs), *kf = reinterpret_cast<float*>(sm + L::kQf), *qf = kf + C, *kn = qf + C, *qn = kn + C;
+  __half* B = reinterpret_cast<__half*>(sm + L::kB);
+  float *kf = reinterpret_cast<float*>(sm + L::kQf), *qf = kf + C, *kn = qf + C, *qn = kn + C;
   float *eg = reinterpret_cast<float*>(sm + L::kE), *el = eg + C, *red = reinterpret_cast<float*>(sm + L::kRed);
   float *col = reinterpret_cast<float*>(sm + L::kCol), *dots = reinterpret_cast<float*>(sm + L::kDot);
 
-  auto fetch = [&](int item) {
-    if (item < group * HALVES) {
-      const int h = h0 + item / HALVES, v0 = 64 * (item % HALVES);
-      const uint8_t* rec = rec_at<DK, DV>(a, slot, h);
-      uint8_t* st = sm + L::kStages + (item & 1) * L::kStage;
+  // [rows of 2 W bytes] from the record to a tile of pitch 2 P
+  auto copy = [&](size_t at, const uint8_t* src, auto width, auto pitch, auto count) {
+    constexpr int W = decltype(width)::value / 8, NV = decltype(count)::value * W;  // vectors of a row, of all
 #pragma unroll
-      for (int x = 0; x < 64 * DK / 8 / kGradThreads; ++x) {
-        const int v = x * kGradThreads + tid, r = v / (DK / 8), cc = v % (DK / 8);
-        cp16(st + L::kS + r * (2 * L::DP) + 16 * cc, rec + R::kS + 2 * (size_t)v0 * DK + 16 * v);
-        cp16(st + L::kD + r * (2 * L::DP) + 16 * cc, rec + R::kD + 2 * (size_t)v0 * DK + 16 * v);
+    for (int x = 0; x < NV / kGradThreads; ++x) {
+      const int v = x * kGradThreads + tid;
+      cp16(sm + at + (v / W) * (2 * decltype(pitch)::value) + 16 * (v % W), src + 16 * v);
+    }
+  };
+  using IDK = std::integral_constant<int, DK>;
+  using IDV = std::integral_constant<int, DV>;
+  using IDP = std::integral_constant<int, L::DP>;
+  using IC = std::integral_constant<int, C>;
+  using IHP = std::integral_constant<int, HP>;
+  auto fetch_early = [&](int h) {  // dV'^T, T, dS'^T, dO and the floats
+    if (h < h0 + group) {
+      const uint8_t* rec = rec_at<DK, DV>(a, slot, h);
+      copy(L::kX, rec + R::kY, IC{}, IHP{}, IDV{});
+      copy(L::kT, rec + R::kT, IC{}, IHP{}, IC{});
+      copy(L::kD, rec + R::kD, IDK{}, IDP{}, IDV{});
+#pragma unroll
+      for (int x = 0; x < C * DV / 8 / kGradThreads; ++x) {
+        const int v = x * kGradThreads + tid, r = v / (DV / 8), c = v % (DV / 8);
+        cp16_or_zero(sm + L::kO + r * (2 * L::VP) + 16 * c,
+                     static_cast<const bf16*>(a.dout) + ((size_t)(c0 + (r < rows ? r : 0)) * a.nv + h) * DV + 8 * c, r < rows);
       }
-      const int r = tid / 8, cc = tid % 8;
-      cp16(st + L::kV + r * (2 * HP) + 16 * cc, rec + R::kU + 2 * v0 * C + 16 * tid);
-      cp16(st + L::kX + r * (2 * HP) + 16 * cc, rec + R::kY + 2 * v0 * C + 16 * tid);
-      const bool valid = c0 + r < end;
-      cp16_or_zero(st + L::kO + r * (2 * HP) + 16 * cc,
-                   static_cast<const bf16*>(a.dout) + ((size_t)(valid ? c0 + r : c0) * a.nv + h) * DV + v0 + 8 * cc, valid);
-      if (v0 == 0) {
-        uint8_t* hd = sm + L::kHeads + ((item / HALVES) & 1) * L::kHead;
-        cp16(hd + L::kT + r * (2 * HP) + 16 * cc, rec + R::kT + 16 * tid);
-        if (tid < R::fKw / 4) cp16(hd + L::kF + 16 * tid, rec + R::kF + 16 * tid);
-      }
+      if (tid < R::fKw / 4) cp16(sm + L::kF + ((h - h0) & 1) * L::kFBytes + 16 * tid, rec + R::kF + 16 * tid);
+    }
+  };
+  auto fetch_late = [&](int h) {  // S^T and V'^T
+    if (h < h0 + group) {
+      const uint8_t* rec = rec_at<DK, DV>(a, slot, h);
+      copy(L::kS, rec + R::kS, IDK{}, IDP{}, IDV{});
+      copy(L::kV, rec + R::kU, IC{}, IHP{}, IDV{});
     }
     cp_commit();
   };
-  fetch(0);
+  fetch_early(h0);
+  fetch_late(h0);
   {  // K16, Q16 with their columns swapped as the states' are
     const uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
 #pragma unroll
@@ -766,132 +788,134 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
   // warp: rows 16 wr .., a quarter wc of the columns; thread: rows r0, r0 + 8
   const int wr = 16 * (warp & 3), wc = warp >> 2, r0 = wr + g8;
   const bool low = 16 * wc <= wr;  // the warp's 16 x 16 block of a [C][C] product is not above the diagonal
-  float kk[2][4] = {}, qk[2][4] = {};
-  if (low) {
+  uint32_t kk[2][2], qk[2][2];     // k_r . k_i and q_r . k_i, pairs of columns in fp16 (at most 1)
+  {
+    float xk[2][4] = {}, xq[2][4] = {};
+    if (low) {
 #pragma unroll
-    for (int k = 0; k < DK; k += 16) {
-      uint32_t ak[4], aq[4], b[4];
-      frag_a<L::DP>(ak, K, wr, k, lane);
-      frag_a<L::DP>(aq, Q, wr, k, lane);
-      frag_b<L::DP>(b, K, 16 * wc, k, lane);
+      for (int k = 0; k < DK; k += 16) {
+        uint32_t ak[4], aq[4], b[4];
+        frag_a<L::DP>(ak, K, wr, k, lane);
+        frag_a<L::DP>(aq, Q, wr, k, lane);
+        frag_b<L::DP>(b, K, 16 * wc, k, lane);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        mma_f16(kk[j], ak, b + 2 * j);
-        mma_f16(qk[j], aq, b + 2 * j);
+        for (int j = 0; j < 2; ++j) {
+          mma_f16(xk[j], ak, b + 2 * j);
+          mma_f16(xq[j], aq, b + 2 * j);
+        }
       }
     }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + 8 * e, i = 16 * wc + 8 * j + 2 * t4;
+        kk[j][e] = pack2(xk[j][2 * e] * kf[r] * kf[i], xk[j][2 * e + 1] * kf[r] * kf[i + 1]);
+        qk[j][e] = pack2(xq[j][2 * e] * qf[r] * kf[i], xq[j][2 * e + 1] * qf[r] * kf[i + 1]);
+      }
   }
   // kf dk_hat and qf dq_hat, summed over the group's v-heads
   float dq[NK][4] = {}, dk[NK][4] = {};
-  float dA[2][4], dP[2][4], s_gc[2], s_bt[2], s_th[2], s_dot = 0.f;
 
-  for (int item = 0; item < group * HALVES; ++item) {
-    const int h = h0 + item / HALVES, v0 = 64 * (item % HALVES);
-    uint8_t* st = sm + L::kStages + (item & 1) * L::kStage;
-    const uint8_t* hd = sm + L::kHeads + ((item / HALVES) & 1) * L::kHead;
-    const __half *S = reinterpret_cast<const __half*>(st + L::kS), *D = reinterpret_cast<const __half*>(st + L::kD);
-    const __half *V = reinterpret_cast<const __half*>(st + L::kV), *X = reinterpret_cast<const __half*>(st + L::kX);
-    __half* O = reinterpret_cast<__half*>(st + L::kO);
-    const __half* T = reinterpret_cast<const __half*>(hd + L::kT);
-    const float* rf = reinterpret_cast<const float*>(hd + L::kF);
+  for (int h = h0; h < h0 + group; ++h) {
+    const float* rf = reinterpret_cast<const float*>(sm + L::kF + ((h - h0) & 1) * L::kFBytes);
     cp_wait<0>();
-    __syncthreads();  // this item's tiles are here, and the one before is done with
-    fetch(item + 1);
+    __syncthreads();
+    // this thread's share of V: rows r0, r0 + 8, columns 16 k + 2 t, + 8 for k = wc and wc + 4
+    uint32_t vraw[KV / 4][4];
+#pragma unroll
+    for (int x = 0; x < KV / 4; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 8 * (e & 1), c = 16 * (wc + 4 * x) + 8 * (e >> 1) + 2 * t4;
+        vraw[x][e] = r < rows ? *reinterpret_cast<const uint32_t*>(static_cast<const bf16*>(a.v) + ((size_t)(c0 + r) * a.nv + h) * DV + c) : 0u;
+      }
+    // one factor for a tile
+    const float mS = top_factor(rf + R::fS, DV, lane), mD = top_factor(rf + R::fD, DV, lane);
+    const float mV = top_factor(rf + R::fV, DV, lane), mX = top_factor(rf + R::fDV, DV, lane);
     const float oinv = rf[R::fScal + kScalDo];
-    // this thread's share of V: rows r0, r0 + 8, columns 16 wc + 2 t, + 8
-    uint32_t vraw[4];
+    float s_dot = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t tk = c0 + r0 + 8 * (e & 1);
-      vraw[e] = tk < end ? *reinterpret_cast<const uint32_t*>(static_cast<const bf16*>(a.v) + ((size_t)tk * a.nv + h) * DV + v0 +
-                                                              16 * wc + 8 * (e >> 1) + 2 * t4)
-                         : 0u;
-    }
-    if (v0 == 0) {
+    for (int x = 0; x < DV * DK / 8 / kGradThreads; ++x) {
+      const int v = x * kGradThreads + tid, c = v / (DK / 8), at = c * L::DP + 8 * (v % (DK / 8));
+      const uint32_t fS = half2_of(__fdividef(rf[R::fS + c], mS)), fD = half2_of(__fdividef(rf[R::fD + c], mD));
+      uint4 p = *reinterpret_cast<const uint4*>(S + at), q = *reinterpret_cast<const uint4*>(D + at);
+      p = make_uint4(mul2(p.x, fS), mul2(p.y, fS), mul2(p.z, fS), mul2(p.w, fS));
+      q = make_uint4(mul2(q.x, fD), mul2(q.y, fD), mul2(q.z, fD), mul2(q.w, fD));
+      *reinterpret_cast<uint4*>(S + at) = p;
+      *reinterpret_cast<uint4*>(D + at) = q;
+      const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dA[j][e] = dP[j][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) s_gc[e] = s_bt[e] = s_th[e] = 0.f;
-      s_dot = 0.f;
-      // column factors of a pair of operands whose columns have factors of their own, over their largest:
-      // (dO, S), (dO, V'), (dX, S), (dX, V'), (V', dS')
-      if (warp < 5) {
-        const float* f0 = warp < 2 ? nullptr : rf + (warp < 4 ? R::fDV : R::fV);
-        const float* f1 = rf + (warp == 4 ? R::fD : (warp & 1 ? R::fV : R::fS));
-        float f[DV / 32], top = 0.f;
-#pragma unroll
-        for (int i = 0; i < DV / 32; ++i) {
-          f[i] = f1[32 * i + lane];
-          if (f0) f[i] = fmaxf(f[i] * f0[32 * i + lane], 0x1p-126f);  // a power of two even where the product is none
-          top = fmaxf(top, f[i]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = fminf(top, 0x1p126f);
-#pragma unroll
-        for (int i = 0; i < DV / 32; ++i) fac[warp * DV + 32 * i + lane] = __float2half_rn(f[i] / top);
-        if (lane == 0) fs[warp] = top;
-      } else if (warp < 7) {
-        const int r = 32 * (warp - 5) + lane;
-        eg[r] = expf(rf[R::fGc + r]);
-        el[r] = expf(rf[R::fGc + C - 1] - rf[R::fGc + r]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = unpack2(ps[i]), w = unpack2(qs[i]);
+        s_dot = fmaf(u.x, w.x, fmaf(u.y, w.y, s_dot));
       }
     }
-    {  // dO to fp16
-      __half* p = O + (tid / 8) * HP + 8 * (tid % 8);
-      const uint4 w = *reinterpret_cast<const uint4*>(p);
-      const float os = 1.f / oinv;  // a power of two
+#pragma unroll
+    for (int x = 0; x < DV * C / 8 / kGradThreads; ++x) {
+      const int v = x * kGradThreads + tid, c = v / (C / 8), at = c * HP + 8 * (v % (C / 8));
+      const uint32_t f = half2_of(__fdividef(rf[R::fV + c], mV));
+      const uint4 p = *reinterpret_cast<const uint4*>(V + at);
+      *reinterpret_cast<uint4*>(V + at) = make_uint4(mul2(p.x, f), mul2(p.y, f), mul2(p.z, f), mul2(p.w, f));
+    }
+#pragma unroll
+    for (int x = 0; x < C * DV / 8 / kGradThreads; ++x) {
+      const int v = x * kGradThreads + tid, at = (v / (DV / 8)) * L::VP + 8 * (v % (DV / 8));
+      const uint4 w = *reinterpret_cast<const uint4*>(O + at);
+      const float os = __fdividef(1.f, oinv);  // a power of two
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
       uint32_t r[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 v = bf2(u[i]);
-        r[i] = pack2(v.x * os, v.y * os);
+        const float2 f = bf2(u[i]);
+        r[i] = pack2(f.x * os, f.y * os);
       }
-      *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+      *reinterpret_cast<uint4*>(O + at) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    if (tid < C) {
+      eg[tid] = expf(rf[R::fGc + tid]);
+      el[tid] = expf(rf[R::fGc + C - 1] - rf[R::fGc + tid]);
     }
     __syncthreads();
-    {  // dX^T = dV'^T T, times 2^7 for T and 2^-7: this warp's 16 rows (columns of Dv) and 16 columns (tokens)
-      float x[2][4] = {};
+    {  // dX^T = dV'^T T, times 2^7 for T and 2^-7: 16 columns of Dv by two blocks of 16 tokens, of like cost together
+      const int cb = 16 * (warp % KV);
+      uint32_t af[4][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k < wc) continue;
-        uint32_t af[4], b[4];
-        frag_a<HP>(af, X, wr, 16 * k, lane);
-        frag_b_t<HP>(b, T, 16 * wc, 16 * k, lane);
-        mma_f16(x[0], af, b);
-        mma_f16(x[1], af, b + 2);
+      for (int k = 0; k < 4; ++k) frag_a<HP>(af[k], X, cb, 16 * k, lane);
+      const float f0 = __fdividef(rf[R::fDV + cb + g8], mX) * 0x1p-7f, f1 = __fdividef(rf[R::fDV + cb + g8 + 8], mX) * 0x1p-7f;
+#pragma unroll
+      for (int u = 0; u < KV / 4; ++u) {
+        // DV = 128: warps 0..7 take blocks 0 and 3, 8..15 blocks 1 and 2; DV = 64: one block a warp
+        const int ib = KV == 8 ? (warp < 8 ? 3 * u : 1 + u) : warp / KV;
+        float x[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k >= ib) {
+            uint32_t b[4];
+            frag_b_t<HP>(b, T, 16 * ib, 16 * k, lane);
+            mma_f16(x[0], af[k], b);
+            mma_f16(x[1], af[k], b + 2);
+          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          __half* dst = Dx + (cb + g8) * HP + 16 * ib + 8 * j + 2 * t4;
+          *reinterpret_cast<uint32_t*>(dst) = pack2(x[j][0] * f0, x[j][1] * f0);
+          *reinterpret_cast<uint32_t*>(dst + 8 * HP) = pack2(x[j][2] * f1, x[j][3] * f1);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2)
-          *reinterpret_cast<uint32_t*>(Dx + (r0 + 4 * e) * HP + 16 * wc + 8 * j + 2 * t4) = pack2(x[j][e] * 0x1p-7f, x[j][e + 1] * 0x1p-7f);
     }
-    // A fragment (rows wr .., columns 16 k .. of Dv) times the column factors of pair m
-    auto scaled = [&](uint32_t* r, const uint32_t* f, int m, int k) {
-      const uint32_t lo = *reinterpret_cast<const uint32_t*>(fac + m * DV + v0 + 16 * k + 2 * t4);
-      const uint32_t hi = *reinterpret_cast<const uint32_t*>(fac + m * DV + v0 + 16 * k + 8 + 2 * t4);
-      r[0] = mul2(f[0], lo);
-      r[1] = mul2(f[1], lo);
-      r[2] = mul2(f[2], hi);
-      r[3] = mul2(f[3], hi);
-    };
-    // acc[NK] += A (scaled by pair m) tile: this warp's rows, its quarter of the columns of Dk
-    auto with_state = [&](float (&x)[NK][4], const uint32_t* f, int m, int k, const __half* tile) {
-      uint32_t as[4];
-      scaled(as, f, m, k);
+    // x[NK] += A fragment times 16 rows of a [DV][DP] tile: this warp's rows, its quarter of the columns of Dk
+    auto with_state = [&](float (&x)[NK][4], const uint32_t* f, int k, const __half* tile) {
 #pragma unroll
       for (int j = 0; j < NK; j += 2) {
         uint32_t b[4];
         frag_b_t<L::DP>(b, tile, 8 * (NK * wc + j), 16 * k, lane);
-        mma_f16(x[j], as, b);
-        mma_f16(x[j + 1], as, b + 2);
+        mma_f16(x[j], f, b);
+        mma_f16(x[j + 1], f, b + 2);
       }
     };
-    auto row_dots = [&](const float (&x)[NK][4], const __half* Y, float (&dot)[2]) {
+    // rows' dots with a tile, and x times their factors into a sum
+    auto take = [&](const float (&x)[NK][4], const __half* Y, const float (&f)[2], float (&sum)[NK][4], float (&dot)[2]) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         dot[e] = 0.f;
@@ -899,148 +923,123 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         for (int j = 0; j < NK; ++j) {
           const float2 y = unpack2(*reinterpret_cast<const uint32_t*>(Y + (r0 + 8 * e) * L::DP + 8 * (NK * wc + j) + 2 * t4));
           dot[e] = fmaf(x[j][2 * e], y.x, fmaf(x[j][2 * e + 1], y.y, dot[e]));
+          sum[j][2 * e] = fmaf(f[e], x[j][2 * e], sum[j][2 * e]);
+          sum[j][2 * e + 1] = fmaf(f[e], x[j][2 * e + 1], sum[j][2 * e + 1]);
         }
       }
     };
+    float dA[2][4] = {}, dP[2][4] = {}, s_gc[2], s_bt[2] = {0.f, 0.f}, s_th[2], f[2], dot[2];
     {  // dO S^T and dP
       float x[NK][4] = {};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < KV; ++k) {
         uint32_t af[4];
-        frag_a<HP>(af, O, wr, 16 * k, lane);
-        with_state(x, af, 0, k, S);
+        frag_a<L::VP>(af, O, wr, 16 * k, lane);
+        with_state(x, af, k, S);
         if (low) {
-          uint32_t as[4], b[4];
-          scaled(as, af, 1, k);
+          uint32_t b[4];
           frag_b_t<HP>(b, V, 16 * wc, 16 * k, lane);
-          mma_f16(dP[0], as, b);
-          mma_f16(dP[1], as, b + 2);
+          mma_f16(dP[0], af, b);
+          mma_f16(dP[1], af, b + 2);
         }
       }
-      float dot[2];
-      row_dots(x, Q, dot);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float f = a.scale * eg[r0 + 8 * e] * qf[r0 + 8 * e] * oinv * fs[0];
-        s_gc[e] = fmaf(f, dot[e], s_gc[e]);
+      for (int e = 0; e < 2; ++e) f[e] = a.scale * eg[r0 + 8 * e] * qf[r0 + 8 * e] * oinv * mS;
+      take(x, Q, f, dq, dot);
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          dq[j][2 * e] = fmaf(f, x[j][2 * e], dq[j][2 * e]);
-          dq[j][2 * e + 1] = fmaf(f, x[j][2 * e + 1], dq[j][2 * e + 1]);
-        }
-      }
+      for (int e = 0; e < 2; ++e) s_gc[e] = f[e] * dot[e];
     }
     {  // V' dS'^T
       float x[NK][4] = {};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < KV; ++k) {
         uint32_t af[4];
         frag_a_t<HP>(af, V, wr, 16 * k, lane);
-        with_state(x, af, 4, k, D);
+        with_state(x, af, k, D);
       }
-      float dot[2];
-      row_dots(x, K, dot);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float f = el[r0 + 8 * e] * kf[r0 + 8 * e] * fs[4];
-        s_th[e] = fmaf(f, dot[e], s_th[e]);
+      for (int e = 0; e < 2; ++e) f[e] = el[r0 + 8 * e] * kf[r0 + 8 * e] * mV * mD;
+      take(x, K, f, dk, dot);
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          dk[j][2 * e] = fmaf(f, x[j][2 * e], dk[j][2 * e]);
-          dk[j][2 * e + 1] = fmaf(f, x[j][2 * e + 1], dk[j][2 * e + 1]);
-        }
-      }
+      for (int e = 0; e < 2; ++e) s_th[e] = f[e] * dot[e];
     }
-    {  // <S, dS'>: 8 lanes a row
-      const int r = tid / 8, cc = (DK / 8) * (tid % 8);
-      float d = 0.f;
-#pragma unroll
-      for (int i = 0; i < DK / 8; i += 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(S + r * L::DP + cc + i), y = *reinterpret_cast<const uint4*>(D + r * L::DP + cc + i);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 u = unpack2(xs[j]), w = unpack2(ys[j]);
-          d = fmaf(u.x, w.x, fmaf(u.y, w.y, d));
-        }
-      }
-      s_dot = fmaf(d * rf[R::fS + v0 + r], rf[R::fD + v0 + r], s_dot);
-    }
-    __syncthreads();  // dX is here
+    __syncthreads();  // dX is here; dV', T, dS' and dO are done with
+    fetch_early(h + 1);
     {  // dX S^T, dA; dV = diag(b) dX and its part of dbeta
       float x[NK][4] = {};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < KV; ++k) {
         uint32_t af[4];
         frag_a_t<HP>(af, Dx, wr, 16 * k, lane);
-        with_state(x, af, 2, k, S);
+        with_state(x, af, k, S);
         if (low) {
-          uint32_t as[4], b[4];
-          scaled(as, af, 3, k);
+          uint32_t b[4];
           frag_b_t<HP>(b, V, 16 * wc, 16 * k, lane);
-          mma_f16(dA[0], as, b);
-          mma_f16(dA[1], as, b + 2);
+          mma_f16(dA[0], af, b);
+          mma_f16(dA[1], af, b + 2);
         }
-        if (k == wc) {
+        if ((k & 3) == wc) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = r0 + 8 * (e & 1), cc = v0 + 16 * k + 8 * (e >> 1) + 2 * t4;
-            const float2 f = *reinterpret_cast<const float2*>(rf + R::fDV + cc);
+            const int r = r0 + 8 * (e & 1), c = 16 * k + 8 * (e >> 1) + 2 * t4;
             float2 d = unpack2(af[e]);
-            d.x *= f.x;
-            d.y *= f.y;
-            const float2 v = bf2(vraw[e]);
+            d.x *= mX;
+            d.y *= mX;
+            const float2 v = bf2(vraw[k / 4][e]);
             s_bt[e & 1] = fmaf(d.x, v.x, fmaf(d.y, v.y, s_bt[e & 1]));
             const float b = rf[R::fBeta + r];
-            if (c0 + r < end)
-              *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dv_out) + ((size_t)(c0 + r) * a.nv + h) * DV + cc) =
+            if (r < rows)
+              *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dv_out) + ((size_t)(c0 + r) * a.nv + h) * DV + c) =
                   ptx::pack_bf16x2(b * d.x, b * d.y);
           }
         }
       }
-      float dot[2];
-      row_dots(x, K, dot);
+      float u[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = r0 + 8 * e;
-        const float u = -eg[r] * kf[r] * fs[2], f = rf[R::fBeta + r] * u;
-        s_bt[e] = fmaf(u, dot[e], s_bt[e]);
-        s_gc[e] = fmaf(f, dot[e], s_gc[e]);
+        u[e] = -eg[r0 + 8 * e] * kf[r0 + 8 * e] * mX * mS;
+        f[e] = rf[R::fBeta + r0 + 8 * e] * u[e];
+      }
+      take(x, K, f, dk, dot);
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          dk[j][2 * e] = fmaf(f, x[j][2 * e], dk[j][2 * e]);
-          dk[j][2 * e + 1] = fmaf(f, x[j][2 * e + 1], dk[j][2 * e + 1]);
-        }
+      for (int e = 0; e < 2; ++e) {
+        s_bt[e] = fmaf(u[e], dot[e], s_bt[e]);
+        s_gc[e] = fmaf(f[e], dot[e], s_gc[e]);
       }
     }
-    if (v0 + 64 < DV) continue;
-    // ---- the v-head's last columns are in: what goes through A and P
-    const float *gc = rf + R::fGc, *bt = rf + R::fBeta;
-    const float sP = oinv * fs[1], sA = fs[3];
-    float cs[2][2] = {};
+    // what goes through A and P
+    const float sP = oinv * mV, sA = mX * mV;
+    float cs[2][2];
+    {
+      const float *gc = rf + R::fGc, *bt = rf + R::fBeta;
+      constexpr float kLog2e = 1.44269504f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float nv_[4], bv_[4];
+      for (int j = 0; j < 2; ++j) {
+        const int i0 = 16 * wc + 8 * j + 2 * t4;
+        cs[j][0] = cs[j][1] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = r0 + 8 * (e >> 1), i = 16 * wc + 8 * j + 2 * t4 + (e & 1);
-        const float gamma = i <= r ? expf(gc[r] - gc[i]) : 0.f;  // masked before exp
-        const float kfi = kf[i], strict = i < r ? 1.f : 0.f;
-        const float kd = kk[j][e] * kf[r] * kfi * gamma * strict;
-        const float da = sA * dA[j][e];
-        const float both = a.scale * sP * dP[j][e] * gamma * (qk[j][e] * qf[r] * kfi) * strict - bt[r] * kd * da;
-        s_bt[e >> 1] = fmaf(-da, kd, s_bt[e >> 1]);
-        s_gc[e >> 1] += both;
-        cs[j][e & 1] += both;
-        nv_[e] = dP[j][e] * gamma * (qf[r] * kfi) * 0x1p6f;                    // 2^14 for the factors, 2^-8
-        bv_[e] = -dA[j][e] * bt[r] * gamma * strict * (kf[r] * kfi) * 0x1p-2f;  // 2^14, 2^-16
-      }
-      if (low) {
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const int r = r0 + 8 * e2;
+          const float2 kd2 = unpack2(kk[j][e2]), qk2 = unpack2(qk[j][e2]);
+          float nn[2], bb[2];
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const int at = (r0 + 4 * e) * HP + 16 * wc + 8 * j + 2 * t4;
-          *reinterpret_cast<uint32_t*>(N + at) = pack2(nv_[e], nv_[e + 1]);
-          *reinterpret_cast<uint32_t*>(B + at) = pack2(bv_[e], bv_[e + 1]);
+          for (int e = 0; e < 2; ++e) {
+            const int i = i0 + e;
+            // masked before exp; the strict triangle for A
+            const float gamma = i <= r ? ptx::ex2_approx(kLog2e * (gc[r] - gc[i])) : 0.f, strict = i < r ? gamma : 0.f;
+            const float dp = dP[j][2 * e2 + e], da = dA[j][2 * e2 + e];
+            const float kd = (e ? kd2.y : kd2.x) * strict, akd = sA * da * kd;
+            const float both = fmaf(-bt[r], akd, a.scale * sP * dp * strict * (e ? qk2.y : qk2.x));
+            s_bt[e2] -= akd;
+            s_gc[e2] += both;
+            cs[j][e] += both;
+            nn[e] = dp * gamma * (qf[r] * kf[i]) * 0x1p6f;                // 2^14 for the factors, 2^-8
+            bb[e] = -da * bt[r] * strict * (kf[r] * kf[i]) * 0x1p-2f;     // 2^14, 2^-16
+          }
+          if (low) {
+            *reinterpret_cast<uint32_t*>(N + r * HP + i0) = pack2(nn[0], nn[1]);
+            *reinterpret_cast<uint32_t*>(B + r * HP + i0) = pack2(bb[0], bb[1]);
+          }
         }
       }
     }
@@ -1067,8 +1066,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         if (g8 == 0) col[(warp & 3) * C + 16 * wc + 8 * j + 2 * t4 + e] = cs[j][e];
       }
     s_dot = warp_sum(s_dot);
-    if (lane == 0) dots[warp] = s_dot;
-    __syncthreads();
+    if (lane == 0) dots[warp] = s_dot * mS * mD;
+    __syncthreads();  // N, B and the sums are here; S and V' are done with
+    fetch_late(h + 1);
     {  // qf dq_hat += N K16, kf dk_hat += N^T Q16 + (B + B^T) K16, over the blocks of the triangle
       float xq[NK][4] = {}, xn[NK][4] = {}, xb[NK][4] = {};
 #pragma unroll
@@ -1127,8 +1127,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         bsum[e] = sum[1];
       }
       th = warp_sum(th);
-      const float dot = warp_sum(lane < 16 ? dots[lane] : 0.f);
-      if (lane == 31) d[1] += th + eg[C - 1] * dot;
+      const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f);
+      if (lane == 31) d[1] += th + eg[C - 1] * dsum;
       float suf = d[0] + d[1];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -1140,7 +1140,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
       const float dg[2] = {suf, beyond + d[1]};
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if (c0 + 2 * lane + e < end) {
+        if (2 * lane + e < rows) {
           const size_t at = (size_t)(c0 + 2 * lane + e) * a.nv + h;
           static_cast<bf16*>(a.dg)[at] = __float2bfloat16_rn(dg[e]);
           static_cast<bf16*>(a.dbeta)[at] = __float2bfloat16_rn(bsum[e]);
@@ -1174,7 +1174,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = r0 + 8 * e;
-    if (c0 + r >= end) continue;
+    if (r >= rows) continue;
     const float pq = qf[r] * qf[r] * ((red[r] + red[2 * C + r]) + (red[4 * C + r] + red[6 * C + r]));
     const float pk = kf[r] * kf[r] * ((red[C + r] + red[3 * C + r]) + (red[5 * C + r] + red[7 * C + r]));
     const size_t row = ((size_t)(c0 + r) * a.nqk + hq) * DK;
@@ -1182,7 +1182,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
     for (int j = 0; j < NK; ++j) {
       const int p = 8 * (NK * wc + j) + 2 * t4;
       const float2 y = unpack2(*reinterpret_cast<const uint32_t*>(Q + r * L::DP + p)), z = unpack2(*reinterpret_cast<const uint32_t*>(K + r * L::DP + p));
-      const size_t at = row + unswap32(p);
+      const size_t at = row + swap32(p);
       *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dq) + at) =
           ptx::pack_bf16x2(qn[r] * (dq[j][2 * e] - y.x * pq), qn[r] * (dq[j][2 * e + 1] - y.y * pq));
       *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dk) + at) =
