@@ -86,8 +86,7 @@ __device__ __forceinline__ uint8_t* qk_at(const BwdArgs& a, int64_t slot, int hq
 // With g = lane / 4, t = lane % 4: A a0 (g, 2t..), a1 (g + 8, 2t..), a2 (g, 2t + 8..), a3 (g + 8, 2t + 8..),
 // B b0 (k 2t.., n g), b1 (k 2t + 8.., n g), accumulators as those of m16n8k8.
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
@@ -166,7 +165,8 @@ struct PrepSmem {
   static constexpr size_t kA = kO + 2 * C * VP;                         // fp32 [C][TP] A, then T
   static constexpr size_t kY = kA + 4 * C * TP;                         // fp32 [C / 2][TP] scratch of the inverse
   static constexpr size_t kF = kY + 2 * C * TP;                         // fp32 [C] each: gc, beta, kf, qf, T's column factors of W
-  static constexpr size_t kTop = kF + 20 * C;                           // fp32 [2][8] largest |v|, |dO| by warp
+  static constexpr size_t kQe = kF + 20 * C;                            // fp16 [C] e qf 2^7 (at most 1)
+  static constexpr size_t kTop = kQe + 2 * C;                           // fp32 [2][8] largest |v|, |dO| by warp
   static constexpr size_t kBytes = kTop + 64;
   static_assert(kBytes <= 113 * 1024, "two blocks per SM");
 };
@@ -253,6 +253,14 @@ __device__ __forceinline__ void store_v(const uint4 (&w)[C * DV / 8 / kPrepThrea
   }
 }
 
+// A warp's accumulators of 16 rows and 64 columns, times f, as the fragments of A operands
+__device__ __forceinline__ void store_frags(uint4* dst, const float (&x)[8][4], float f) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    dst[32 * j] = make_uint4(pack2(x[2 * j][0] * f, x[2 * j][1] * f), pack2(x[2 * j][2] * f, x[2 * j][3] * f),
+                             pack2(x[2 * j + 1][0] * f, x[2 * j + 1][1] * f), pack2(x[2 * j + 1][2] * f, x[2 * j + 1][3] * f));
+}
+
 template <int DK, int DV>
 __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a) {
   using L = PrepSmem<DK, DV>;
@@ -268,6 +276,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   __half *TB = Q, *P = Q + C * HP, *V = reinterpret_cast<__half*>(sm + L::kV), *O = reinterpret_cast<__half*>(sm + L::kO);
   float *A = reinterpret_cast<float*>(sm + L::kA), *Y = reinterpret_cast<float*>(sm + L::kY);
   float *gc = reinterpret_cast<float*>(sm + L::kF), *bt = gc + C, *kf = bt + C, *qf = kf + C, *wf = qf + C;
+  __half* qe = reinterpret_cast<__half*>(sm + L::kQe);
   float* tops = reinterpret_cast<float*>(sm + L::kTop);
   uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
   float* qfl = reinterpret_cast<float*>(qrec + QR::kF);
@@ -342,6 +351,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
       const float e = expf(gc[tid]);
       // 2^7 kf <= 1 (kf is at most 2^-7: the largest element of a row is at most its norm)
       wf[tid] = bt[tid] * e * kf[tid] * 0x1p13f;
+      qe[tid] = __float2half_rn(e * qf[tid] * 0x1p7f);
       rf[R::fGc + tid] = gc[tid];
       rf[R::fBeta + tid] = bt[tid];
       rf[R::fKw + tid] = expf(gc[C - 1] - gc[tid]) * kf[tid];
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = r0 + 8 * (e >> 1), i = wc + 8 * j + 2 * t4 + (e & 1);
-        const float gamma = i <= r ? expf(gc[r] - gc[i]) : 0.f;  // masked before exp
+        const float gamma = i <= r ? ptx::ex2_approx(1.44269504f * (gc[r] - gc[i])) : 0.f;  // masked before exp
         A[r * TP + i] = i < r ? -bt[r] * (kk[j][e] * gamma) : 0.f;
         p[j][e] = qk[j][e] * gamma * 0x1p8f;
       }
@@ -381,8 +391,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
       float x[NT][4] = {};
       const int n0 = (DK / 2) * (warp >> 2);
 #pragma unroll
-      for (int k = 0; k < C; k += 16) {
-        if (k >= wr + 16) break;
+      for (int k = 0; k < C; k += 16) {  // T's zeros above the diagonal are multiplied too: a branch would cost more
         uint32_t af[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -406,40 +415,40 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
           *reinterpret_cast<uint32_t*>(w + 4 * e * DK + 8 * j) = pack2(x[j][e] * 0x1p-6f, x[j][e + 1] * 0x1p-6f);
     }
     // U^T = V^T (T diag(b))^T and Y^T = dO^T P, 16 columns of Dv a unit, and the fragments of (diag(qe) dO)^T
-    for (int u = warp; u < DV / 8; u += kPrepThreads / 32) {
-      const bool isY = u >= DV / 16;
-      const int m0 = 16 * (u % (DV / 16));
-      const __half* D = isY ? O : V;
+    for (int u = warp; u < DV / 16; u += kPrepThreads / 32) {
       float x[8][4] = {};
-      uint32_t af[4][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) frag_a_t<L::VP>(af[k], D, m0, 16 * k, lane);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t af[4];
+        frag_a_t<L::VP>(af, V, 16 * u, 16 * k, lane);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (isY ? k < j : k > j) continue;  // outside the triangle
+        for (int j = k; j < 4; ++j) {  // the blocks of the triangle
           uint32_t b[4];
-          if (isY) frag_b_t<HP>(b, P, 16 * j, 16 * k, lane); else frag_b<HP>(b, TB, 16 * j, 16 * k, lane);
-          mma_f16(x[2 * j], af[k], b);
-          mma_f16(x[2 * j + 1], af[k], b + 2);
-        }
-      const float f = isY ? 0x1p-8f : 0x1p-7f;
-      uint4* dst = reinterpret_cast<uint4*>(rec + (isY ? R::kY : R::kU)) + (m0 / 16) * 128 + lane;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        dst[32 * j] = make_uint4(pack2(x[2 * j][0] * f, x[2 * j][1] * f), pack2(x[2 * j][2] * f, x[2 * j][3] * f),
-                                 pack2(x[2 * j + 1][0] * f, x[2 * j + 1][1] * f), pack2(x[2 * j + 1][2] * f, x[2 * j + 1][3] * f));
-      if (isY) {
-        dst = reinterpret_cast<uint4*>(rec + R::kO) + (m0 / 16) * 128 + lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 16 * k + 2 * t4;
-          const uint32_t lo = pack2(expf(gc[r]) * qf[r] * 0x1p7f, expf(gc[r + 1]) * qf[r + 1] * 0x1p7f);
-          const uint32_t hi = pack2(expf(gc[r + 8]) * qf[r + 8] * 0x1p7f, expf(gc[r + 9]) * qf[r + 9] * 0x1p7f);
-          dst[32 * k] = make_uint4(mul2(af[k][0], lo), mul2(af[k][1], lo), mul2(af[k][2], hi), mul2(af[k][3], hi));
+          frag_b<HP>(b, TB, 16 * j, 16 * k, lane);
+          mma_f16(x[2 * j], af, b);
+          mma_f16(x[2 * j + 1], af, b + 2);
         }
       }
+      store_frags(reinterpret_cast<uint4*>(rec + R::kU) + u * 128 + lane, x, 0x1p-7f);
+    }
+    for (int u = kPrepThreads / 32 - 1 - warp; u < DV / 16; u += kPrepThreads / 32) {
+      float x[8][4] = {};
+      uint4* dst = reinterpret_cast<uint4*>(rec + R::kO) + u * 128 + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t af[4];
+        frag_a_t<L::VP>(af, O, 16 * u, 16 * k, lane);
+#pragma unroll
+        for (int j = 0; j <= k; ++j) {
+          uint32_t b[4];
+          frag_b_t<HP>(b, P, 16 * j, 16 * k, lane);
+          mma_f16(x[2 * j], af, b);
+          mma_f16(x[2 * j + 1], af, b + 2);
+        }
+        const uint32_t lo = *reinterpret_cast<const uint32_t*>(qe + 16 * k + 2 * t4), hi = *reinterpret_cast<const uint32_t*>(qe + 16 * k + 8 + 2 * t4);
+        dst[32 * k] = make_uint4(mul2(af[0], lo), mul2(af[1], lo), mul2(af[2], hi), mul2(af[3], hi));
+      }
+      store_frags(reinterpret_cast<uint4*>(rec + R::kY) + u * 128 + lane, x, 0x1p-8f);
     }
   }
 }
@@ -889,13 +898,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         const int ib = KV == 8 ? (warp < 8 ? 3 * u : 1 + u) : warp / KV;
         float x[2][4] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k >= ib) {
-            uint32_t b[4];
-            frag_b_t<HP>(b, T, 16 * ib, 16 * k, lane);
-            mma_f16(x[0], af[k], b);
-            mma_f16(x[1], af[k], b + 2);
-          }
+        for (int k = 0; k < 4; ++k) {  // T's zeros above the diagonal are multiplied too: a branch would cost more
+          uint32_t b[4];
+          frag_b_t<HP>(b, T, 16 * ib, 16 * k, lane);
+          mma_f16(x[0], af[k], b);
+          mma_f16(x[1], af[k], b + 2);
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           __half* dst = Dx + (cb + g8) * HP + 16 * ib + 8 * j + 2 * t4;
@@ -936,8 +944,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         uint32_t af[4];
         frag_a<L::VP>(af, O, wr, 16 * k, lane);
         with_state(x, af, k, S);
-        if (low) {
-          uint32_t b[4];
+      }
+      if (low) {
+#pragma unroll
+        for (int k = 0; k < KV; ++k) {
+          uint32_t af[4], b[4];
+          frag_a<L::VP>(af, O, wr, 16 * k, lane);
           frag_b_t<HP>(b, V, 16 * wc, 16 * k, lane);
           mma_f16(dP[0], af, b);
           mma_f16(dP[1], af, b + 2);
@@ -972,26 +984,34 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         uint32_t af[4];
         frag_a_t<HP>(af, Dx, wr, 16 * k, lane);
         with_state(x, af, k, S);
-        if (low) {
-          uint32_t b[4];
+      }
+      if (low) {
+#pragma unroll
+        for (int k = 0; k < KV; ++k) {
+          uint32_t af[4], b[4];
+          frag_a_t<HP>(af, Dx, wr, 16 * k, lane);
           frag_b_t<HP>(b, V, 16 * wc, 16 * k, lane);
           mma_f16(dA[0], af, b);
           mma_f16(dA[1], af, b + 2);
         }
-        if ((k & 3) == wc) {
+      }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = r0 + 8 * (e & 1), c = 16 * k + 8 * (e >> 1) + 2 * t4;
-            float2 d = unpack2(af[e]);
-            d.x *= mX;
-            d.y *= mX;
-            const float2 v = bf2(vraw[k / 4][e]);
-            s_bt[e & 1] = fmaf(d.x, v.x, fmaf(d.y, v.y, s_bt[e & 1]));
-            const float b = rf[R::fBeta + r];
-            if (r < rows)
-              *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dv_out) + ((size_t)(c0 + r) * a.nv + h) * DV + c) =
-                  ptx::pack_bf16x2(b * d.x, b * d.y);
-          }
+      for (int m = 0; m < KV / 4; ++m) {
+        const int k = wc + 4 * m;
+        uint32_t af[4];
+        frag_a_t<HP>(af, Dx, wr, 16 * k, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 8 * (e & 1), c = 16 * k + 8 * (e >> 1) + 2 * t4;
+          float2 d = unpack2(af[e]);
+          d.x *= mX;
+          d.y *= mX;
+          const float2 v = bf2(vraw[m][e]);
+          s_bt[e & 1] = fmaf(d.x, v.x, fmaf(d.y, v.y, s_bt[e & 1]));
+          const float b = rf[R::fBeta + r];
+          if (r < rows)
+            *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dv_out) + ((size_t)(c0 + r) * a.nv + h) * DV + c) =
+                ptx::pack_bf16x2(b * d.x, b * d.y);
         }
       }
       float u[2];
@@ -1036,10 +1056,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
             nn[e] = dp * gamma * (qf[r] * kf[i]) * 0x1p6f;                // 2^14 for the factors, 2^-8
             bb[e] = -da * bt[r] * strict * (kf[r] * kf[i]) * 0x1p-2f;     // 2^14, 2^-16
           }
-          if (low) {
-            *reinterpret_cast<uint32_t*>(N + r * HP + i0) = pack2(nn[0], nn[1]);
-            *reinterpret_cast<uint32_t*>(B + r * HP + i0) = pack2(bb[0], bb[1]);
-          }
+          *reinterpret_cast<uint32_t*>(N + r * HP + i0) = pack2(nn[0], nn[1]);
+          *reinterpret_cast<uint32_t*>(B + r * HP + i0) = pack2(bb[0], bb[1]);
         }
       }
     }
@@ -1069,37 +1087,28 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
     if (lane == 0) dots[warp] = s_dot * mS * mD;
     __syncthreads();  // N, B and the sums are here; S and V' are done with
     fetch_late(h + 1);
-    {  // qf dq_hat += N K16, kf dk_hat += N^T Q16 + (B + B^T) K16, over the blocks of the triangle
+    {  // qf dq_hat += N K16, kf dk_hat += N^T Q16 + (B + B^T) K16 (zeros of the triangle included: see dX)
       float xq[NK][4] = {}, xn[NK][4] = {}, xb[NK][4] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t an[4], ant[4], ab[4], abt[4];
-        const bool lo = 16 * k <= wr, hi = 16 * k >= wr;
-        if (lo) {
-          frag_a<HP>(an, N, wr, 16 * k, lane);
-          frag_a<HP>(ab, B, wr, 16 * k, lane);
-        }
-        if (hi) {
-          frag_a_t<HP>(ant, N, wr, 16 * k, lane);
-          frag_a_t<HP>(abt, B, wr, 16 * k, lane);
-        }
+        frag_a<HP>(an, N, wr, 16 * k, lane);
+        frag_a<HP>(ab, B, wr, 16 * k, lane);
+        frag_a_t<HP>(ant, N, wr, 16 * k, lane);
+        frag_a_t<HP>(abt, B, wr, 16 * k, lane);
 #pragma unroll
         for (int j = 0; j < NK; j += 2) {
           uint32_t bk[4], bq[4];
           frag_b_t<L::DP>(bk, K, 8 * (NK * wc + j), 16 * k, lane);
-          if (lo) {
-            mma_f16(xq[j], an, bk);
-            mma_f16(xq[j + 1], an, bk + 2);
-            mma_f16(xb[j], ab, bk);
-            mma_f16(xb[j + 1], ab, bk + 2);
-          }
-          if (hi) {
-            frag_b_t<L::DP>(bq, Q, 8 * (NK * wc + j), 16 * k, lane);
-            mma_f16(xn[j], ant, bq);
-            mma_f16(xn[j + 1], ant, bq + 2);
-            mma_f16(xb[j], abt, bk);
-            mma_f16(xb[j + 1], abt, bk + 2);
-          }
+          frag_b_t<L::DP>(bq, Q, 8 * (NK * wc + j), 16 * k, lane);
+          mma_f16(xq[j], an, bk);
+          mma_f16(xq[j + 1], an, bk + 2);
+          mma_f16(xb[j], ab, bk);
+          mma_f16(xb[j + 1], ab, bk + 2);
+          mma_f16(xn[j], ant, bq);
+          mma_f16(xn[j + 1], ant, bq + 2);
+          mma_f16(xb[j], abt, bk);
+          mma_f16(xb[j + 1], abt, bk + 2);
         }
       }
       const float sN = a.scale * sP * 0x1p-6f, sB = sA * 0x1p2f;
