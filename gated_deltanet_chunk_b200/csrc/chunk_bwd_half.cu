@@ -34,40 +34,51 @@ using bwd::C;
 using bwd::TP;
 using bf16 = __nv_bfloat16;
 
-constexpr int HP = C + 8;  // pitch of [..][64] fp16 tiles: rows 16 bytes apart in the banks, as ldmatrix wants
+constexpr int HP = C + 8;  // pitch of the prepare kernel's [..][64] fp16 tiles: rows 16 bytes apart in the banks
 
-// Workspace record of one (chunk slot, v-head), in bytes.
+// Workspace record of one (chunk slot, v-head), in bytes.  An image is a tile as it stands in shared memory, so
+// that one bulk copy brings it in: rows of 128 or 256 bytes whose 16-byte vectors are swapped by their row
+// (vector v of row r at v ^ (r & 7)), which keeps ldmatrix free of bank conflicts without padding.
 template <int DK, int DV>
 struct Rec {
-  static constexpr size_t kT = 0;                      // fp16 [C][C] T 2^7
-  static constexpr size_t kW = kT + 2 * C * C;         // fp16 [C][DK] W 2^7
-  static constexpr size_t kU = kW + 2 * C * DK;        // fp16 U^T fragments, then V'^T [DV][C]
-  static constexpr size_t kY = kU + 2 * C * DV;        // fp16 (P^T dO)^T fragments, then dV'^T [DV][C]
-  static constexpr size_t kO = kY + 2 * C * DV;        // fp16 (diag(qe) dO)^T fragments
-  static constexpr size_t kS = kO + 2 * C * DV;        // fp16 [DV][DK] S^T before the chunk, columns by swap32
-  static constexpr size_t kD = kS + 2 * DK * DV;       // fp16 [DV][DK] dS'^T behind the chunk, the same
-  static constexpr size_t kF = kD + 2 * DK * DV;       // floats from here:
+  static constexpr size_t kX = 0;                      // (P^T dO)^T fragments, then the image of dV'^T [DV][C]
+  static constexpr size_t kT = kX + 2 * C * DV;        // image of T 2^7 [C][C]
+  static constexpr size_t kV = kT + 2 * C * C;         // U^T fragments, then the image of V'^T [DV][C]
+  static constexpr size_t kS = kV + 2 * C * DV;        // image of S^T [DV][DK] before the chunk, columns by swap32
+  static constexpr size_t kO = kS + 2 * DK * DV;       // image of dO [C][DV]
+  static constexpr size_t kD = kO + 2 * C * DV;        // image of dS'^T [DV][DK] behind the chunk, columns by swap32
+  static constexpr size_t kW = kD + 2 * DK * DV;       // image of W 2^7 [C][DK]
+  static constexpr size_t kOq = kW + 2 * C * DK;       // (diag(qe) dO)^T fragments
+  static constexpr size_t kF = kOq + 2 * C * DV;       // floats from here:
   static constexpr int fGc = 0;                        // [C] gcum
   static constexpr int fBeta = fGc + C;                // [C] beta
   static constexpr int fScal = fBeta + C;              // [8] see Scal
-  static constexpr int fS = fScal + 8;                 // [DV] factor of every row of S^T
-  static constexpr int fD = fS + DV;                   // [DV] of dS'^T
-  static constexpr int fV = fD + DV;                   // [DV] of V'^T
+  static constexpr int fV = fScal + 8;                 // [DV] factor of every row of V'^T
   static constexpr int fDV = fV + DV;                  // [DV] of dV'^T
   static constexpr int fKw = fDV + DV;                 // [C] l_r / |k_r| in units of K16
   static constexpr int kFloats = fKw + C;
   static constexpr size_t kBytes = kF + 4 * kFloats;
-  static_assert(kBytes % 16 == 0 && fScal % 4 == 0, "16-byte copies");
+  static_assert(kBytes % 16 == 0 && fScal % 4 == 0 && fKw % 4 == 0, "16-byte copies");
 };
-enum Scal { kScalU, kScalY, kScalO, kScalGl, kScalDo };  // factors of U, Y, diag(qe) dO; e_last; factor of dO
+// factors of U, Y, diag(qe) dO, dO, S and dS', and e_last
+enum Scal { kScalU, kScalY, kScalO, kScalGl, kScalDo, kScalS, kScalD };
 
 // Workspace record of one (chunk slot, qk-head), in bytes.
 template <int DK>
 struct QkRec {
-  static constexpr size_t kK = 0;                 // fp16 [C][DK] K16
-  static constexpr size_t kQ = kK + 2 * C * DK;   // fp16 [C][DK] Q16
-  static constexpr size_t kF = kQ + 2 * C * DK;   // floats [4][C]: k_hat = kf K16, q_hat = qf Q16, and kf |k|, qf |q| inverted
+  static constexpr size_t kK = 0;                 // image of K16 [C][DK]
+  static constexpr size_t kQ = kK + 2 * C * DK;   // of Q16
+  static constexpr size_t kKs = kQ + 2 * C * DK;  // of K16 with its columns by swap32
+  static constexpr size_t kQs = kKs + 2 * C * DK;
+  static constexpr size_t kF = kQs + 2 * C * DK;  // floats [4][C]: k_hat = kf K16, q_hat = qf Q16, and kf |k|, qf |q| inverted
   static constexpr size_t kBytes = kF + 16 * C;
+};
+
+// What the gradients kernel has to know of a slot.
+struct SlotInfo {
+  int64_t c0;     // first token
+  int32_t rows;   // tokens, 0: an empty slot
+  int32_t pad;
 };
 
 template <int DK, int DV>
@@ -81,6 +92,19 @@ __device__ __forceinline__ uint8_t* qk_at(const BwdArgs& a, int64_t slot, int hq
   return reinterpret_cast<uint8_t*>(a.ws) + (size_t)slots_of<DK, DV>(a) * a.nv * Rec<DK, DV>::kBytes +
          ((size_t)slot * a.nqk + hq) * QkRec<DK>::kBytes;
 }
+template <int DK, int DV>
+__device__ __forceinline__ SlotInfo* slot_info(const BwdArgs& a, int64_t slot) {
+  return reinterpret_cast<SlotInfo*>(qk_at<DK, DV>(a, slots_of<DK, DV>(a), 0)) + slot;
+}
+
+// Where element (r, col) of an image with rows of RB bytes stands, in bytes.
+template <int RB> __device__ __forceinline__ int image(int r, int col) {
+  return r * RB + ((((col >> 3) ^ (r & 7)) << 4) | ((col & 7) * 2));
+}
+// Column d of a row of 32 stands at swap32(d): lane t's columns 8 b + 2 t, + 1 of the states' accumulators
+// (b = 0..3) are next to one another, so that they are stored as one vector.  Pairs stay pairs, and the swap is its
+// own inverse.
+__device__ __forceinline__ int swap32(int d) { return (d & ~31) | (((d >> 1) & 3) << 3) | (((d >> 3) & 3) << 1) | (d & 1); }
 
 // ------------------------------------------------------------------ fragments
 // With g = lane / 4, t = lane % 4: A a0 (g, 2t..), a1 (g + 8, 2t..), a2 (g, 2t + 8..), a3 (g + 8, 2t + 8..),
@@ -118,6 +142,57 @@ template <int P> __device__ __forceinline__ void frag_b_t(uint32_t* r, const __h
   ldsm_t(r, tile + (k0 + (lane & 15)) * P + n0 + 8 * (lane >> 4));
 }
 
+// What a lane adds to the address of a fragment in an image: its row and the swap of the 16-byte vectors (m0, n0 and
+// k0 are multiples of 16, so a lane's row is lane & 7 mod 8).  `again` hides the values from the compiler, which
+// would otherwise form the addresses of every product ahead of the loop around them, and spill them.
+struct Lane {
+  uint32_t ra, rb, sa, sb;   // rows of kind a (lane & 15) and b, and their swaps
+  int g, t;
+  __device__ __forceinline__ explicit Lane(int lane)
+      : ra(lane & 15), rb((lane & 7) + 8 * (lane >> 4)), sa(((lane >> 4) ^ (lane & 7)) << 4),
+        sb((((lane >> 3) & 1) ^ (lane & 7)) << 4), g(lane >> 2), t(lane & 3) {}
+  __device__ __forceinline__ void again() {
+    asm volatile("" : "+r"(ra), "+r"(rb), "+r"(sa), "+r"(sb), "+r"(g), "+r"(t));
+  }
+};
+template <int RB> __device__ __forceinline__ uint32_t img_addr(uint32_t img, int row, int col, uint32_t r, uint32_t s) {
+  return img + (uint32_t)(row * RB) + r * RB + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) + (((uint32_t)col >> 6) << 7);
+}
+__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(p)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(p)
+               : "memory");
+}
+template <int RB> __device__ __forceinline__ void img_a(uint32_t* r, uint32_t img, int m0, int k0, const Lane& l) {
+  ldsm(r, img_addr<RB>(img, m0, k0, l.ra, l.sa));
+}
+template <int RB> __device__ __forceinline__ void img_a_t(uint32_t* r, uint32_t img, int m0, int k0, const Lane& l) {
+  ldsm_t(r, img_addr<RB>(img, k0, m0, l.rb, l.sb));
+}
+template <int RB> __device__ __forceinline__ void img_b(uint32_t* r, uint32_t img, int n0, int k0, const Lane& l) {
+  ldsm(r, img_addr<RB>(img, n0, k0, l.rb, l.sb));
+}
+template <int RB> __device__ __forceinline__ void img_b_t(uint32_t* r, uint32_t img, int n0, int k0, const Lane& l) {
+  ldsm_t(r, img_addr<RB>(img, k0, n0, l.ra, l.sa));
+}
+// Words of an image in shared memory: row r (r & 7 = g), columns col, col + 1
+template <int RB> __device__ __forceinline__ uint32_t img_word(uint32_t img, int r, int col, int g) {
+  return img + (uint32_t)(r * RB + ((((((col >> 3) & 7) ^ (g & 7)) << 4) | ((col & 7) * 2)) + ((col >> 6) << 7)));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -139,15 +214,14 @@ __device__ __forceinline__ void pow2_factor(float top, float& f, float& inv) {
   inv = __uint_as_float((e - 7u) << 23);
 }
 
-__device__ __forceinline__ void cp16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp16_or_zero(void* dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
+// A bulk copy from global to shared memory that completes on `bar` (sizes and addresses: multiples of 16 bytes).
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   ptx::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // as in chunk_tc.cu
 
 // ------------------------------------------------------------------ 1. prepare
 // One block per (slot, qk-head): K16, Q16 and their products once, then its v-heads in turn.
@@ -175,8 +249,8 @@ struct PrepSmem {
 // and the factors.  DK / 8 lanes per row.  Rows so small that the norm's eps decides are scaled by 2^17, so
 // that kf and qf stay within a few powers of two of one another.
 template <int DK>
-__device__ __forceinline__ void load_qk(const bf16* x, int64_t c0, int64_t end, int heads, int head, __half* tile, __half* ws,
-                                        float* f, float* wf, float* wn, int tid) {
+__device__ __forceinline__ void load_qk(const bf16* x, int64_t c0, int64_t end, int heads, int head, __half* tile, uint8_t* plain,
+                                        uint8_t* swapped, float* f, float* wf, float* wn, int tid) {
   constexpr int L = DK / 8, R = kPrepThreads / L;
   const int lr = tid % L;
 #pragma unroll
@@ -207,7 +281,10 @@ __device__ __forceinline__ void load_qk(const bf16* x, int64_t c0, int64_t end, 
     h.z = pack2(v[2].x * s, v[2].y * s);
     h.w = pack2(v[3].x * s, v[3].y * s);
     *reinterpret_cast<uint4*>(tile + r * (DK + 8) + 8 * lr) = h;
-    *reinterpret_cast<uint4*>(ws + r * DK + 8 * lr) = h;
+    *reinterpret_cast<uint4*>(plain + image<2 * DK>(r, 8 * lr)) = h;
+    const uint32_t pairs[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(swapped + image<2 * DK>(r, swap32(8 * lr + 2 * i))) = pairs[i];
     if (lr == 0) {
       f[r] = inv / sqrtf(ss + kNormEps);
       wf[r] = f[r];
@@ -238,7 +315,7 @@ __device__ __forceinline__ void load_v(const bf16* x, int64_t c0, int64_t end, i
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 }
 template <int DV>
-__device__ __forceinline__ void store_v(const uint4 (&w)[C * DV / 8 / kPrepThreads], float s, __half* tile, int tid) {
+__device__ __forceinline__ void store_v(const uint4 (&w)[C * DV / 8 / kPrepThreads], float s, __half* tile, uint8_t* img, int tid) {
   constexpr int L = DV / 8, R = kPrepThreads / L;
 #pragma unroll
   for (int p = 0; p < C / R; ++p) {
@@ -249,7 +326,9 @@ __device__ __forceinline__ void store_v(const uint4 (&w)[C * DV / 8 / kPrepThrea
       const float2 v = bf2(u[i]);
       h[i] = pack2(v.x * s, v.y * s);
     }
-    *reinterpret_cast<uint4*>(tile + (p * R + tid / L) * (DV + 8) + 8 * (tid % L)) = make_uint4(h[0], h[1], h[2], h[3]);
+    const int r = p * R + tid / L, c = 8 * (tid % L);
+    *reinterpret_cast<uint4*>(tile + r * (DV + 8) + c) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (img) *reinterpret_cast<uint4*>(img + image<2 * DV>(r, c)) = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 
@@ -271,7 +350,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   const int hq = blockIdx.y, group = a.nv / a.nqk;
   const int64_t slot = blockIdx.x;
   int64_t c0, end;
-  if (!bwd::chunk_at(a, slot, c0, end)) return;
+  const bool any = bwd::chunk_at(a, slot, c0, end);
+  if (hq == 0 && tid == 0) *slot_info<DK, DV>(a, slot) = SlotInfo{c0, any ? (int32_t)min((int64_t)C, end - c0) : 0, 0};
+  if (!any) return;
   __half *K = reinterpret_cast<__half*>(sm + L::kK), *Q = reinterpret_cast<__half*>(sm + L::kQ);
   __half *TB = Q, *P = Q + C * HP, *V = reinterpret_cast<__half*>(sm + L::kV), *O = reinterpret_cast<__half*>(sm + L::kO);
   float *A = reinterpret_cast<float*>(sm + L::kA), *Y = reinterpret_cast<float*>(sm + L::kY);
@@ -281,8 +362,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
   float* qfl = reinterpret_cast<float*>(qrec + QR::kF);
 
-  load_qk<DK>(static_cast<const bf16*>(a.k), c0, end, a.nqk, hq, K, reinterpret_cast<__half*>(qrec + QR::kK), kf, qfl, qfl + 2 * C, tid);
-  load_qk<DK>(static_cast<const bf16*>(a.q), c0, end, a.nqk, hq, Q, reinterpret_cast<__half*>(qrec + QR::kQ), qf, qfl + C, qfl + 3 * C, tid);
+  load_qk<DK>(static_cast<const bf16*>(a.k), c0, end, a.nqk, hq, K, qrec + QR::kK, qrec + QR::kKs, kf, qfl, qfl + 2 * C, tid);
+  load_qk<DK>(static_cast<const bf16*>(a.q), c0, end, a.nqk, hq, Q, qrec + QR::kQ, qrec + QR::kQs, qf, qfl + C, qfl + 3 * C, tid);
   __syncthreads();
   // warp: rows 16 wr .., columns 32 wc .. of the [C][C] products; blocks above the diagonal are not formed
   const int wr = 16 * (warp & 3), wc = 32 * (warp >> 2), r0 = wr + g8;
@@ -344,8 +425,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     float vs, vinv, os, oinv;
     pow2_factor(vtop, vs, vinv);
     pow2_factor(otop, os, oinv);
-    store_v<DV>(vw, vs, V, tid);
-    store_v<DV>(ow, os, O, tid);
+    store_v<DV>(vw, vs, V, nullptr, tid);
+    store_v<DV>(ow, os, O, rec + R::kO, tid);
     __syncthreads();
     if (tid < C) {
       const float e = expf(gc[tid]);
@@ -383,7 +464,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         const float2 t = *reinterpret_cast<const float2*>(A + r * TP + i);
         *reinterpret_cast<uint32_t*>(P + r * HP + i) = pack2(p[j][e], p[j][e + 1]);
         *reinterpret_cast<uint32_t*>(TB + r * HP + i) = pack2(t.x * bt[i] * 0x1p6f, t.y * bt[i + 1] * 0x1p6f);
-        *reinterpret_cast<uint32_t*>(rec + R::kT + 2 * (r * C + i)) = pack2(t.x * 0x1p7f, t.y * 0x1p7f);
+        *reinterpret_cast<uint32_t*>(rec + R::kT + image<2 * C>(r, i)) = pack2(t.x * 0x1p7f, t.y * 0x1p7f);
       }
     __syncthreads();
     {  // W 2^7 = (T diag(b e kf) 2^13) K16 2^-6: this warp's 16 rows, one half of the columns
@@ -407,12 +488,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
           mma_f16(x[j + 1], af, b + 2);
         }
       }
-      __half* w = reinterpret_cast<__half*>(rec + R::kW) + (size_t)r0 * DK + n0 + 2 * t4;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; e += 2)
-          *reinterpret_cast<uint32_t*>(w + 4 * e * DK + 8 * j) = pack2(x[j][e] * 0x1p-6f, x[j][e + 1] * 0x1p-6f);
+          *reinterpret_cast<uint32_t*>(rec + R::kW + image<2 * DK>(r0 + 4 * e, n0 + 8 * j + 2 * t4)) =
+              pack2(x[j][e] * 0x1p-6f, x[j][e + 1] * 0x1p-6f);
     }
     // U^T = V^T (T diag(b))^T and Y^T = dO^T P, 16 columns of Dv a unit, and the fragments of (diag(qe) dO)^T
     for (int u = warp; u < DV / 16; u += kPrepThreads / 32) {
@@ -429,11 +510,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
           mma_f16(x[2 * j + 1], af, b + 2);
         }
       }
-      store_frags(reinterpret_cast<uint4*>(rec + R::kU) + u * 128 + lane, x, 0x1p-7f);
+      store_frags(reinterpret_cast<uint4*>(rec + R::kV) + u * 128 + lane, x, 0x1p-7f);
     }
     for (int u = kPrepThreads / 32 - 1 - warp; u < DV / 16; u += kPrepThreads / 32) {
       float x[8][4] = {};
-      uint4* dst = reinterpret_cast<uint4*>(rec + R::kO) + u * 128 + lane;
+      uint4* dst = reinterpret_cast<uint4*>(rec + R::kOq) + u * 128 + lane;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t af[4];
@@ -448,62 +529,47 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         const uint32_t lo = *reinterpret_cast<const uint32_t*>(qe + 16 * k + 2 * t4), hi = *reinterpret_cast<const uint32_t*>(qe + 16 * k + 8 + 2 * t4);
         dst[32 * k] = make_uint4(mul2(af[0], lo), mul2(af[1], lo), mul2(af[2], hi), mul2(af[3], hi));
       }
-      store_frags(reinterpret_cast<uint4*>(rec + R::kY) + u * 128 + lane, x, 0x1p-8f);
+      store_frags(reinterpret_cast<uint4*>(rec + R::kX) + u * 128 + lane, x, 0x1p-8f);
     }
   }
 }
 
 // ------------------------------------------------------------------ 2. states
+// One block per (sequence, v-head, direction), one warp per 16 Dv columns.  A chunk's tiles come in two chunks
+// ahead, by bulk copies.  The state's largest element is joined over the block (with the barrier that frees the
+// stage), so that its image has one factor; V' and dV' keep a factor for each row (column of Dv).
 
-constexpr int kStateWarps = 4;  // 64 Dv columns per block
-constexpr int kStateThreads = 32 * kStateWarps;
-
-template <int DK>
+template <int DK, int DV>
 struct StateSmem {
-  static constexpr int DP = DK + 8;
-  static constexpr size_t kW = 0;                       // fp16 [C][DP] W
-  static constexpr size_t kK = kW + 2 * C * DP;         // fp16 [C][DP] K16
-  static constexpr size_t kQ = kK + 2 * C * DP;         // fp16 [C][DP] Q16 (backwards)
-  static constexpr size_t kKw = kQ + 2 * C * DP;        // fp32 [C]
-  static constexpr size_t kStage = kKw + 4 * C;
-  static constexpr size_t kBytes = 2 * kStage;
-  static_assert(kBytes <= 113 * 1024, "two blocks per SM");
+  static constexpr int kThreads = 2 * DV;
+  static constexpr size_t kTile = 2 * C * DK;
+  static constexpr size_t kStage = 3 * kTile + 4 * C;   // W, K16, Q16 (backwards), kw
+  static constexpr size_t kTop = 2 * kStage;            // fp32 [2][8] the warps' largest
+  static constexpr size_t kBar = kTop + 64;             // two barriers
+  static constexpr size_t kBytes = kBar + 16;
+  static_assert(kStage % 128 == 0 && kBytes <= 232448, "shared memory budget");
 };
 
-// Rows c, c + 8 of an accumulator [NT] (16 x 8 tiles) as fp16 with a factor of two for each row:
-// the A fragments of the next product, and 1 / factor.
-template <int NT>
-__device__ __forceinline__ void scale_rows(const float (&s)[NT][4], uint32_t (&f)[NT / 2][4], float (&inv)[2]) {
-  float top[2] = {0.f, 0.f}, fac[2];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    top[0] = fmaxf(top[0], fmaxf(fabsf(s[j][0]), fabsf(s[j][1])));
-    top[1] = fmaxf(top[1], fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
-  }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-    pow2_factor(top[e], fac[e], inv[e]);
-  }
-#pragma unroll
-  for (int j = 0; j < NT / 2; ++j) {
-    f[j][0] = pack2(s[2 * j][0] * fac[0], s[2 * j][1] * fac[0]);
-    f[j][1] = pack2(s[2 * j][2] * fac[1], s[2 * j][3] * fac[1]);
-    f[j][2] = pack2(s[2 * j + 1][0] * fac[0], s[2 * j + 1][1] * fac[0]);
-    f[j][3] = pack2(s[2 * j + 1][2] * fac[1], s[2 * j + 1][3] * fac[1]);
-  }
+// Two 16 x 8 tiles of accumulators as an A fragment, rows g and g + 8 times f0 and f1
+__device__ __forceinline__ void pack_frag(const float* lo, const float* hi, float f0, float f1, uint32_t* f) {
+  f[0] = pack2(lo[0] * f0, lo[1] * f0);
+  f[1] = pack2(lo[2] * f1, lo[3] * f1);
+  f[2] = pack2(hi[0] * f0, hi[1] * f0);
+  f[3] = pack2(hi[2] * f1, hi[3] * f1);
 }
 
 template <int DK, int DV, bool kBackward>
-__device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h, int col0) {
-  using L = StateSmem<DK>;
+__device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h) {
+  using L = StateSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
-  constexpr int ND = DK / 8;
+  constexpr int ND = DK / 8, RB = 2 * DK, NW = DV / 16;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int slice = col0 / 16 + warp, c = 16 * slice + g;  // this thread's columns of Dv: c and c + 8
+  const int c = 16 * warp + g;  // this thread's columns of Dv: c and c + 8
   const int hq = h / (a.nv / a.nqk);
+  Lane ln(lane);
+  float* tops = reinterpret_cast<float*>(sm + L::kTop);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);
   int64_t start, end;
   seq_bounds(a, n, start, end);
   const int64_t chunks = (end - start + C - 1) / C, slot0 = start / C + n;
@@ -518,59 +584,68 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       s[j][e] = init ? init[state_off + (size_t)(8 * j + 2 * t + (e & 1)) * DV + c + 8 * (e >> 1)] : 0.f;
 
   auto slot_of = [&](int64_t i) { return slot0 + (kBackward ? chunks - 1 - i : i); };
-  auto fetch = [&](int64_t i) {
-    if (i < chunks) {
-      uint8_t* st = sm + (i & 1) * L::kStage;
-      const uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
-      const uint8_t* qrec = qk_at<DK, DV>(a, slot_of(i), hq);
-#pragma unroll
-      for (int m = 0; m < (kBackward ? 3 : 2); ++m) {
-        const uint8_t* src = m == 0 ? rec + R::kW : (m == 1 ? qrec + QR::kK : qrec + QR::kQ);
-        uint8_t* dst = st + (m == 0 ? L::kW : (m == 1 ? L::kK : L::kQ));
-#pragma unroll
-        for (int x = 0; x < C * DK / 8 / kStateThreads; ++x) {
-          const int v = x * kStateThreads + tid, r = v / (DK / 8), cc = v % (DK / 8);
-          cp16(dst + r * (2 * L::DP) + 16 * cc, src + 16 * v);
-        }
-      }
-      if (tid < C / 4) cp16(st + L::kKw + 16 * tid, rec + R::kF + 4 * R::fKw + 16 * tid);
-    }
-    cp_commit();
+  auto fetch = [&](int64_t i) {  // by one thread
+    if (i >= chunks) return;
+    uint8_t* st = sm + (i & 1) * L::kStage;
+    const uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
+    const uint8_t* qrec = qk_at<DK, DV>(a, slot_of(i), hq);
+    constexpr uint32_t tiles = (kBackward ? 2 : 1) * L::kTile;
+    ptx::mbar_arrive_expect_tx(bar + (i & 1), (uint32_t)(L::kTile + tiles + 4 * C));
+    bulk_copy(st, rec + R::kW, L::kTile, bar + (i & 1));
+    bulk_copy(st + L::kTile, qrec + QR::kK, tiles, bar + (i & 1));  // Q16 stands behind K16
+    bulk_copy(st + 3 * L::kTile, rec + R::kF + 4 * R::fKw, 4 * C, bar + (i & 1));
   };
-  fetch(0);
+  // the largest element of the state over the block; also the barrier behind which a chunk's stage is free
+  auto join_top = [&](int64_t i, bool ok) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < ND; ++j) top = fmaxf(fmaxf(top, fmaxf(fabsf(s[j][0]), fabsf(s[j][1]))), fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
+    const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if (lane == 0) tops[8 * (i & 1) + warp] = __uint_as_float(w);
+    return __syncthreads_or(!ok);
+  };
+  if (tid == 0) {
+    ptx::mbar_init(bar, 1);
+    ptx::mbar_init(bar + 1, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  if (tid == 0) {
+    fetch(0);
+    fetch(1);
+  }
+  join_top(1, true);
   for (int64_t i = 0; i < chunks; ++i) {
     uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
     float* rf = reinterpret_cast<float*>(rec + R::kF);
     uint4 uw[4], ow[4];  // U^T or Y^T as accumulators, and (diag(qe) dO)^T as A fragments
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uw[j] = reinterpret_cast<const uint4*>(rec + (kBackward ? R::kY : R::kU))[slice * 128 + 32 * j + lane];
-      if (kBackward) ow[j] = reinterpret_cast<const uint4*>(rec + R::kO)[slice * 128 + 32 * j + lane];
+      uw[j] = reinterpret_cast<const uint4*>(rec + (kBackward ? R::kX : R::kV))[warp * 128 + 32 * j + lane];
+      if (kBackward) ow[j] = reinterpret_cast<const uint4*>(rec + R::kOq)[warp * 128 + 32 * j + lane];
     }
     const float us = rf[R::fScal + (kBackward ? kScalY : kScalU)], os = rf[R::fScal + kScalO], gl = rf[R::fScal + kScalGl];
-    fetch(i + 1);
     // the state as this chunk meets it, in fp16: kept for the gradients, and the next product's operand
-    uint32_t sf[ND / 2][4];
-    float sinv[2];
-    scale_rows<ND>(s, sf, sinv);
-    {
-      __half* sv = reinterpret_cast<__half*>(rec + (kBackward ? R::kD : R::kS)) + (size_t)c * DK + 8 * t;
+    float top = 0.f, sfac, sinv;
 #pragma unroll
-      for (int j = 0; j < ND / 4; ++j) {  // 32 columns: each lane its 8 in one vector (columns 8 b + 2 t, + 1 at 8 t + 2 b, + 1)
-        *reinterpret_cast<uint4*>(sv + 32 * j) = make_uint4(sf[2 * j][0], sf[2 * j][2], sf[2 * j + 1][0], sf[2 * j + 1][2]);
-        *reinterpret_cast<uint4*>(sv + 8 * DK + 32 * j) = make_uint4(sf[2 * j][1], sf[2 * j][3], sf[2 * j + 1][1], sf[2 * j + 1][3]);
+    for (int j = 0; j < NW; ++j) top = fmaxf(top, tops[8 * ((i + 1) & 1) + j]);
+    pow2_factor(top, sfac, sinv);
+    uint32_t sf[ND / 2][4];
+#pragma unroll
+    for (int j = 0; j < ND / 2; ++j) pack_frag(s[2 * j], s[2 * j + 1], sfac, sfac, sf[j]);
+    {
+      uint8_t* img = rec + (kBackward ? R::kD : R::kS);
+#pragma unroll
+      for (int j = 0; j < ND / 4; ++j) {  // 32 columns: each lane its 8 in one vector
+        *reinterpret_cast<uint4*>(img + image<RB>(c, 32 * j + 8 * t)) = make_uint4(sf[2 * j][0], sf[2 * j][2], sf[2 * j + 1][0], sf[2 * j + 1][2]);
+        *reinterpret_cast<uint4*>(img + image<RB>(c + 8, 32 * j + 8 * t)) = make_uint4(sf[2 * j][1], sf[2 * j][3], sf[2 * j + 1][1], sf[2 * j + 1][3]);
       }
-      if (t == 0) {
-        rf[(kBackward ? R::fD : R::fS) + c] = sinv[0];
-        rf[(kBackward ? R::fD : R::fS) + c + 8] = sinv[1];
-      }
+      if (tid == 0) rf[R::fScal + (kBackward ? kScalD : kScalS)] = sinv;
     }
-    cp_wait<1>();
-    __syncthreads();
+    const bool ok = ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
     const uint8_t* st = sm + (i & 1) * L::kStage;
-    const __half *W = reinterpret_cast<const __half*>(st + L::kW), *K = reinterpret_cast<const __half*>(st + L::kK);
-    const __half* Q = reinterpret_cast<const __half*>(st + L::kQ);
-    const float* kw = reinterpret_cast<const float*>(st + L::kKw);
+    const uint32_t W = ptx::smem_u32(st), K = W + (uint32_t)L::kTile, Q = K + (uint32_t)L::kTile;
+    const float* kw = reinterpret_cast<const float*>(st + 3 * L::kTile);
     // x = S^T W^T (forwards) or dS'^T K^T (backwards), [16 x C]
     float x[8][4] = {};
 #pragma unroll
@@ -578,31 +653,46 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t b[4];
-        frag_b<L::DP>(b, kBackward ? K : W, 16 * j, 16 * k, lane);
+        img_b<RB>(b, kBackward ? K : W, 16 * j, 16 * k, ln);
         mma_f16(x[2 * j], sf[k], b);
         mma_f16(x[2 * j + 1], sf[k], b + 2);
       }
     // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw)
+    float rtop[2] = {0.f, 0.f}, vfac[2], vinv[2];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint4 w = uw[j / 2];
       const float2 u0 = unpack2(j & 1 ? w.z : w.x), u1 = unpack2(j & 1 ? w.w : w.y);
-      const float2 f = kBackward ? *reinterpret_cast<const float2*>(kw + 8 * j + 2 * t) : make_float2(-0x1p-7f, -0x1p-7f);
-      x[j][0] = fmaf(x[j][0] * sinv[0], f.x, us * u0.x);
-      x[j][1] = fmaf(x[j][1] * sinv[0], f.y, us * u0.y);
-      x[j][2] = fmaf(x[j][2] * sinv[1], f.x, us * u1.x);
-      x[j][3] = fmaf(x[j][3] * sinv[1], f.y, us * u1.y);
+      float2 f = make_float2(-0x1p-7f * sinv, -0x1p-7f * sinv);
+      if (kBackward) {
+        f = *reinterpret_cast<const float2*>(kw + 8 * j + 2 * t);
+        f.x *= sinv;
+        f.y *= sinv;
+      }
+      x[j][0] = fmaf(x[j][0], f.x, us * u0.x);
+      x[j][1] = fmaf(x[j][1], f.y, us * u0.y);
+      x[j][2] = fmaf(x[j][2], f.x, us * u1.x);
+      x[j][3] = fmaf(x[j][3], f.y, us * u1.y);
+      rtop[0] = fmaxf(rtop[0], fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
+      rtop[1] = fmaxf(rtop[1], fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      rtop[e] = fmaxf(rtop[e], __shfl_xor_sync(0xffffffffu, rtop[e], 1));
+      rtop[e] = fmaxf(rtop[e], __shfl_xor_sync(0xffffffffu, rtop[e], 2));
+      pow2_factor(rtop[e], vfac[e], vinv[e]);
     }
     uint32_t vf[4][4];
-    float vinv[2];
-    scale_rows<8>(x, vf, vinv);
-    __syncwarp();  // the fragments of U or Y that these rows replace are all read
+#pragma unroll
+    for (int j = 0; j < 4; ++j) pack_frag(x[2 * j], x[2 * j + 1], vfac[0], vfac[1], vf[j]);
+    __syncwarp();  // the fragments of U or Y that these rows replace (the same 2 KB) are all read
     {
-      __half* vv = reinterpret_cast<__half*>(rec + (kBackward ? R::kY : R::kU)) + c * C + 2 * t;
+      uint8_t* img = rec + (kBackward ? R::kX : R::kV);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(vv + (e & 1) * 8 * C + 16 * j + 8 * (e >> 1)) = vf[j][e];
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint32_t*>(img + image<2 * C>(c + 8 * (e & 1), 16 * j + 8 * (e >> 1) + 2 * t)) = vf[j][e];
       if (t == 0) {
         rf[(kBackward ? R::fDV : R::fV) + c] = vinv[0];
         rf[(kBackward ? R::fDV : R::fV) + c + 8] = vinv[1];
@@ -630,12 +720,12 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t b[4];
-          frag_b_t<L::DP>(b, kBackward ? W : K, 8 * m + 16 * j, 16 * k, lane);
+          img_b_t<RB>(b, kBackward ? W : K, 8 * m + 16 * j, 16 * k, ln);
           mma_f16(y[2 * j], vf[k], b);
           mma_f16(y[2 * j + 1], vf[k], b + 2);
           if (kBackward) {
             const uint32_t of[4] = {ow[k].x, ow[k].y, ow[k].z, ow[k].w};
-            frag_b_t<L::DP>(b, Q, 8 * m + 16 * j, 16 * k, lane);
+            img_b_t<RB>(b, Q, 8 * m + 16 * j, 16 * k, ln);
             mma_f16(z[2 * j], of, b);
             mma_f16(z[2 * j + 1], of, b + 2);
           }
@@ -649,7 +739,15 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
           s[m + j][e] = fmaf(e < 2 ? f0 : f1, y[j][e], v);
         }
     }
-    __syncthreads();  // the stage is free for the fetch after next
+    if (join_top(i, ok)) {  // a copy never came: report it, wait once more for what is in flight, and leave
+      if (tid == 0) {
+        report_status(a.status, kStatusTimeout);
+        ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
+        if (i + 1 < chunks) ptx::mbar_wait_bounded(bar + ((i + 1) & 1), (uint32_t)(((i + 1) >> 1) & 1), kWaitLimitNs);
+      }
+      return;
+    }
+    if (tid == 0) fetch(i + 2);
   }
   if (kBackward && a.ds0) {
 #pragma unroll
@@ -660,543 +758,598 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
   }
 }
 
-// blockIdx.x: direction and 64-column slice, y: v-head, z: sequence
+// blockIdx.x: direction, y: v-head, z: sequence
 template <int DK, int DV>
-__global__ void __launch_bounds__(kStateThreads, 2) states_half_kernel(BwdArgs a) {
-  extern __shared__ __align__(16) uint8_t sm[];
-  const int col0 = 16 * kStateWarps * (blockIdx.x >> 1);
-  if (blockIdx.x & 1)
-    walk<DK, DV, true>(a, sm, blockIdx.z, blockIdx.y, col0);
+__global__ void __launch_bounds__(2 * DV) states_half_kernel(BwdArgs a) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  if (blockIdx.x == 0)
+    walk<DK, DV, true>(a, sm, blockIdx.z, blockIdx.y);
   else
-    walk<DK, DV, false>(a, sm, blockIdx.z, blockIdx.y, col0);
+    walk<DK, DV, false>(a, sm, blockIdx.z, blockIdx.y);
 }
 
 // ------------------------------------------------------------------ 3. gradients
-// One block of 16 warps per (slot, qk-head), which takes its v-heads in turn.  A v-head's tiles come in by
-// cp.async, and each buffer is filled for the next v-head as soon as this one is done with it.  Their rows' own
-// factors are first made one for the tile (exactly, but for what underflows beside the tile's largest element),
-// so that the products need no scaling on the way.
+// One block of 16 warps per SM takes (slot, qk-head) items, and their v-heads in turn.  The tiles of the next
+// v-head (of the next item, after an item's last one) are fetched by bulk copies as soon as this one's are used:
+//   1. all warps: dX^T = dV'^T T; V'^T to one factor for all its rows
+//   2. warps 0-7: dO S^T, then dA and dP; warps 8-15: V' dS'^T, then dX S^T; all: <S, dS'>
+//   3. warps 0-7: N and B; warps 8-15: dV
+//   4. warps 0-7: N K, and keep dq; warps 8-15: N^T Q + (B + B^T) K, and keep dk
+// with a block barrier after 1 and after 3.
 
 constexpr int kGradThreads = 512;
+constexpr int kSms = 148;  // one block on each
 
 template <int DK, int DV>
 struct GradSmem {
-  static constexpr int DP = DK + 8, VP = DV + 8;
-  static constexpr size_t kS = 0;                             // fp16 [DV][DP] S^T
-  static constexpr size_t kD = kS + 2 * DV * DP;              // fp16 [DV][DP] dS'^T
-  static constexpr size_t kV = kD + 2 * DV * DP;              // fp16 [DV][HP] V'^T
-  static constexpr size_t kX = kV + 2 * DV * HP;              // fp16 [DV][HP] dV'^T
-  static constexpr size_t kO = kX + 2 * DV * HP;              // [C][VP] dO: bf16, then fp16
-  static constexpr size_t kT = kO + 2 * C * VP;               // fp16 [C][HP] T
-  static constexpr size_t kF = kT + 2 * C * HP;               // two of: the record's floats up to fKw
-  static constexpr size_t kFBytes = 4 * Rec<DK, DV>::fKw;
-  static constexpr size_t kK = kF + 2 * kFBytes;              // fp16 [C][DP] K16, columns by swap32
-  static constexpr size_t kQ = kK + 2 * C * DP;               // fp16 [C][DP] Q16, the same
-  static constexpr size_t kDx = kQ + 2 * C * DP;              // fp16 [DV][HP] dX^T
-  static constexpr size_t kN = kDx + 2 * DV * HP;             // fp16 [C][HP] N
-  static constexpr size_t kB = kN + 2 * C * HP;               // fp16 [C][HP] B
-  static constexpr size_t kQf = kB + 2 * C * HP;              // fp32 [4][C] kf, qf, and their shares of the norm
-  static constexpr size_t kE = kQf + 16 * C;                  // fp32 [2][C] e, l
-  static constexpr size_t kRed = kE + 8 * C;                  // fp32 [4][3][C] row sums by column block; [4][2][C] at the end
-  static constexpr size_t kCol = kRed + 48 * C;               // fp32 [4][C] column sums by row block
+  using R = Rec<DK, DV>;
+  static constexpr size_t kX = 0;                             // dV'^T and T
+  static constexpr size_t kXBytes = R::kV - R::kX;
+  static constexpr size_t kV = kX + kXBytes;                  // V'^T
+  static constexpr size_t kVBytes = R::kS - R::kV;
+  static constexpr size_t kS = kV + kVBytes;                  // S^T, dO and dS'^T
+  static constexpr size_t kSBytes = R::kW - R::kS;
+  static constexpr size_t kDx = kS + kSBytes;                 // dX^T, an image [DV][C]
+  static constexpr size_t kN = kDx + 2 * C * DV;              // N and B, images [C][C]
+  static constexpr size_t kB = kN + 2 * C * C;
+  static constexpr size_t kK = kB + 2 * C * C;                // two of: K16, Q16 (columns by swap32) and their floats
+  static constexpr size_t kKBytes = QkRec<DK>::kBytes - QkRec<DK>::kKs;
+  static constexpr size_t kF = kK + 2 * kKBytes;              // two of: the record's floats up to fKw
+  static constexpr size_t kFBytes = 4 * R::fKw;
+  static constexpr size_t kE = kF + 2 * kFBytes;              // fp32 [C] e
+  static constexpr size_t kRed = kE + 4 * C;                  // fp32 [3][4][C] rows' dots by column block
+  static constexpr size_t kRedA = kRed + 48 * C;              // fp32 [6][C] row sums: through A and P (two halves: dgc, dbeta), dX V (two)
+  static constexpr size_t kCol = kRedA + 24 * C;              // fp32 [4][C] column sums by row block
   static constexpr size_t kDot = kCol + 16 * C;               // fp32 [16] <S, dS'> by warp
-  static constexpr size_t kBytes = kDot + 64;
-  static_assert(kF % 16 == 0 && kFBytes % 16 == 0 && kBytes <= 232448, "shared memory budget");
+  static constexpr size_t kBar = kDot + 64;                   // barriers: X, V, S, K16 and Q16 (two)
+  static constexpr size_t kBytes = kBar + 40;
+  static_assert(kXBytes % 128 == 0 && kK % 128 == 0 && kF % 16 == 0 && kFBytes % 16 == 0, "images and bulk copies");
+  static_assert(kBytes <= 232448, "shared memory budget");
 };
 
-// Column d of a row of 32 stands at swap32(d): lane t's columns 8 b + 2 t, + 1 of the states' accumulators
-// (b = 0..3) are next to one another, so that they were stored as one vector.  Pairs stay pairs, and the swap is
-// its own inverse.
-__device__ __forceinline__ int swap32(int d) { return (d & ~31) | (((d >> 1) & 3) << 3) | (((d >> 3) & 3) << 1) | (d & 1); }
-
-// The largest of n factors (powers of two, n = 64 or 128), by a warp, and its inverse
+// The largest of n factors (powers of two), by a warp
 __device__ __forceinline__ float top_factor(const float* f, int n, int lane) {
   uint32_t top = 0u;
   for (int i = lane; i < n; i += 32) top = max(top, __float_as_uint(f[i]));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
 }
-__device__ __forceinline__ uint32_t half2_of(float x) { return pack2(x, x); }
+
+// x[2][NT] (32 rows from m0, 8 NT columns from n0) += A B over k in [16 K0, 16 K1).
+// A: an image [m][k], or [k][m]; B: an image [k][n].
+template <int NT, int K0, int K1, int RA, bool kAT, int RBB>
+__device__ __forceinline__ void gemm32(float (&x)[2][NT][4], uint32_t A, int m0, uint32_t B, int n0, const Lane& l) {
+#pragma unroll
+  for (int k = K0; k < K1; ++k) {
+    uint32_t a0[4], a1[4];
+    if (kAT) {
+      img_a_t<RA>(a0, A, m0, 16 * k, l);
+      img_a_t<RA>(a1, A, m0 + 16, 16 * k, l);
+    } else {
+      img_a<RA>(a0, A, m0, 16 * k, l);
+      img_a<RA>(a1, A, m0 + 16, 16 * k, l);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+      uint32_t b[4];
+      img_b_t<RBB>(b, B, n0 + 8 * j, 16 * k, l);
+      mma_f16(x[0][j], a0, b);
+      mma_f16(x[0][j + 1], a0, b + 2);
+      mma_f16(x[1][j], a1, b);
+      mma_f16(x[1][j + 1], a1, b + 2);
+    }
+  }
+}
+
+// Rows' dots of x (as gemm32 leaves it) with an image Y, this thread's part of row m0 + 16 m + 8 e + g in dot[m][e];
+// and sum += f x by rows.
+template <int NT, int RB>
+__device__ __forceinline__ void take(const float (&x)[2][NT][4], uint32_t Y, int m0, int n0, const float (&f)[2][2],
+                                     float (&sum)[2][NT][4], float (&dot)[2][2], const Lane& l) {
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = m0 + 16 * m + 8 * e + l.g;
+      dot[m][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float2 y = unpack2(lds32(img_word<RB>(Y, r, n0 + 8 * j + 2 * l.t, l.g)));
+        dot[m][e] = fmaf(x[m][j][2 * e], y.x, fmaf(x[m][j][2 * e + 1], y.y, dot[m][e]));
+        sum[m][j][2 * e] = fmaf(f[m][e], x[m][j][2 * e], sum[m][j][2 * e]);
+        sum[m][j][2 * e + 1] = fmaf(f[m][e], x[m][j][2 * e + 1], sum[m][j][2 * e + 1]);
+      }
+    }
+}
+
+// A row's sum over the quad of lanes, to dst[row] by one of them
+__device__ __forceinline__ void put_row(float v, float* dst, int t) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  if (t == 0) *dst = v;
+}
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) {
   using L = GradSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
-  extern __shared__ __align__(16) uint8_t sm[];
-  constexpr int NK = DK / 32;       // 8-column tiles of a warp's quarter of Dk
-  constexpr int KV = DV / 16;       // steps over the columns of Dv
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
-  const int hq = blockIdx.y, group = a.nv / a.nqk, h0 = hq * group;
-  const int64_t slot = blockIdx.x;
-  int64_t c0, end;
-  if (!bwd::chunk_at(a, slot, c0, end)) return;
-  const int rows = (int)min((int64_t)C, end - c0);
-  __half *S = reinterpret_cast<__half*>(sm + L::kS), *D = reinterpret_cast<__half*>(sm + L::kD);
-  __half *V = reinterpret_cast<__half*>(sm + L::kV), *X = reinterpret_cast<__half*>(sm + L::kX);
-  __half *O = reinterpret_cast<__half*>(sm + L::kO), *T = reinterpret_cast<__half*>(sm + L::kT);
-  __half *K = reinterpret_cast<__half*>(sm + L::kK), *Q = reinterpret_cast<__half*>(sm + L::kQ);
-  __half *Dx = reinterpret_cast<__half*>(sm + L::kDx), *N = reinterpret_cast<__half*>(sm + L::kN);
-  __half* B = reinterpret_cast<__half*>(sm + L::kB);
-  float *kf = reinterpret_cast<float*>(sm + L::kQf), *qf = kf + C, *kn = qf + C, *qn = kn + C;
-  float *eg = reinterpret_cast<float*>(sm + L::kE), *el = eg + C, *red = reinterpret_cast<float*>(sm + L::kRed);
+  extern __shared__ __align__(128) uint8_t sm[];
+  constexpr int NT = DK / 32;        // 8-column tiles of a warp's quarter of Dk
+  constexpr int KV = DV / 16;        // steps over the columns of Dv
+  constexpr int RK = 2 * DK, RV = 2 * DV, RC = 2 * C;  // bytes of an image's rows
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Lane ln(lane);
+  const bool first = warp < 8;       // warps 0-7, which keep dq
+  const int w8 = warp & 7;
+  const int group = a.nv / a.nqk;
+  const int64_t items = slots_of<DK, DV>(a) * a.nqk;
+  const uint32_t base = ptx::smem_u32(sm);
+  const uint32_t X = base + L::kX, T = X + 2 * C * DV, V = base + L::kV, S = base + L::kS, O = S + 2 * DK * DV, D = O + 2 * C * DV;
+  const uint32_t Dx = base + L::kDx, N = base + L::kN, B = base + L::kB;
+  float* eg = reinterpret_cast<float*>(sm + L::kE);
+  float *red = reinterpret_cast<float*>(sm + L::kRed), *reda = reinterpret_cast<float*>(sm + L::kRedA);
   float *col = reinterpret_cast<float*>(sm + L::kCol), *dots = reinterpret_cast<float*>(sm + L::kDot);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);
 
-  // [rows of 2 W bytes] from the record to a tile of pitch 2 P
-  auto copy = [&](size_t at, const uint8_t* src, auto width, auto pitch, auto count) {
-    constexpr int W = decltype(width)::value / 8, NV = decltype(count)::value * W;  // vectors of a row, of all
-#pragma unroll
-    for (int x = 0; x < NV / kGradThreads; ++x) {
-      const int v = x * kGradThreads + tid;
-      cp16(sm + at + (v / W) * (2 * decltype(pitch)::value) + 16 * (v % W), src + 16 * v);
+  // The next item from `w` on whose slot is not empty, its first token and tokens
+  int64_t c0 = 0;
+  int rows = 0;
+  auto seek = [&](int64_t w, int64_t& first_token, int& tokens) {
+    for (; w < items; w += gridDim.x) {
+      const SlotInfo s = *slot_info<DK, DV>(a, w / a.nqk);
+      first_token = s.c0;
+      tokens = s.rows;
+      if (s.rows > 0) break;
     }
+    return w;
   };
-  using IDK = std::integral_constant<int, DK>;
-  using IDV = std::integral_constant<int, DV>;
-  using IDP = std::integral_constant<int, L::DP>;
-  using IC = std::integral_constant<int, C>;
-  using IHP = std::integral_constant<int, HP>;
-  auto fetch_early = [&](int h) {  // dV'^T, T, dS'^T, dO and the floats
-    if (h < h0 + group) {
-      const uint8_t* rec = rec_at<DK, DV>(a, slot, h);
-      copy(L::kX, rec + R::kY, IC{}, IHP{}, IDV{});
-      copy(L::kT, rec + R::kT, IC{}, IHP{}, IC{});
-      copy(L::kD, rec + R::kD, IDK{}, IDP{}, IDV{});
-#pragma unroll
-      for (int x = 0; x < C * DV / 8 / kGradThreads; ++x) {
-        const int v = x * kGradThreads + tid, r = v / (DV / 8), c = v % (DV / 8);
-        cp16_or_zero(sm + L::kO + r * (2 * L::VP) + 16 * c,
-                     static_cast<const bf16*>(a.dout) + ((size_t)(c0 + (r < rows ? r : 0)) * a.nv + h) * DV + 8 * c, r < rows);
-      }
-      if (tid < R::fKw / 4) cp16(sm + L::kF + ((h - h0) & 1) * L::kFBytes + 16 * tid, rec + R::kF + 16 * tid);
-    }
+  int64_t item = seek(blockIdx.x, c0, rows);
+  if (item >= items) return;
+  // by one thread; nh: v-heads taken so far, ni: items
+  auto fetch_x = [&](int64_t w, int h, uint32_t nh) {
+    const uint8_t* rec = rec_at<DK, DV>(a, w / a.nqk, h);
+    ptx::mbar_arrive_expect_tx(bar, (uint32_t)(L::kXBytes + L::kFBytes));
+    bulk_copy(sm + L::kX, rec + R::kX, L::kXBytes, bar);
+    bulk_copy(sm + L::kF + (nh & 1) * L::kFBytes, rec + R::kF, L::kFBytes, bar);
   };
-  auto fetch_late = [&](int h) {  // S^T and V'^T
-    if (h < h0 + group) {
-      const uint8_t* rec = rec_at<DK, DV>(a, slot, h);
-      copy(L::kS, rec + R::kS, IDK{}, IDP{}, IDV{});
-      copy(L::kV, rec + R::kU, IC{}, IHP{}, IDV{});
-    }
-    cp_commit();
+  auto fetch_rest = [&](int64_t w, int h) {
+    const uint8_t* rec = rec_at<DK, DV>(a, w / a.nqk, h);
+    ptx::mbar_arrive_expect_tx(bar + 1, (uint32_t)L::kVBytes);
+    bulk_copy(sm + L::kV, rec + R::kV, L::kVBytes, bar + 1);
+    ptx::mbar_arrive_expect_tx(bar + 2, (uint32_t)L::kSBytes);
+    bulk_copy(sm + L::kS, rec + R::kS, L::kSBytes, bar + 2);
   };
-  fetch_early(h0);
-  fetch_late(h0);
-  {  // K16, Q16 with their columns swapped as the states' are
-    const uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
-#pragma unroll
-    for (int x = 0; x < 2 * C * DK / 8 / kGradThreads; ++x) {
-      const int v = x * kGradThreads + tid, m = v / (C * DK / 8), r = v / (DK / 8) % C, d = 8 * (v % (DK / 8));
-      const uint4 w = *reinterpret_cast<const uint4*>(qrec + 16 * v);
-      __half* dst = (m ? Q : K) + r * L::DP;
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(dst + swap32(d + 2 * i)) = u[i];
-    }
-    if (tid < 4 * C) kf[tid] = reinterpret_cast<const float*>(qrec + QR::kF)[tid];
+  auto fetch_k = [&](int64_t w, uint32_t ni) {
+    const uint8_t* qrec = qk_at<DK, DV>(a, w / a.nqk, (int)(w % a.nqk));
+    ptx::mbar_arrive_expect_tx(bar + 3 + (ni & 1), (uint32_t)L::kKBytes);
+    bulk_copy(sm + L::kK + (ni & 1) * L::kKBytes, qrec + QR::kKs, L::kKBytes, bar + 3 + (ni & 1));
+  };
+  if (tid == 0) {
+    for (int i = 0; i < 5; ++i) ptx::mbar_init(bar + i, 1);
+    ptx::fence_mbar_init();
   }
   __syncthreads();
-  // warp: rows 16 wr .., a quarter wc of the columns; thread: rows r0, r0 + 8
-  const int wr = 16 * (warp & 3), wc = warp >> 2, r0 = wr + g8;
-  const bool low = 16 * wc <= wr;  // the warp's 16 x 16 block of a [C][C] product is not above the diagonal
-  uint32_t kk[2][2], qk[2][2];     // k_r . k_i and q_r . k_i, pairs of columns in fp16 (at most 1)
-  {
-    float xk[2][4] = {}, xq[2][4] = {};
-    if (low) {
+  if (tid == 0) {
+    fetch_k(item, 0);
+    fetch_x(item, (int)(item % a.nqk) * group, 0);
+    fetch_rest(item, (int)(item % a.nqk) * group);
+  }
+  // a warp's 32 rows and quarter of the columns of Dk for products with the state, its 16 rows and 32 columns of
+  // the [C][C] products (warps 0-7), and its 16 rows and half of the columns of Dv for dV (warps 8-15)
+  const int m0 = 32 * (w8 & 1), n0 = (DK / 4) * (w8 >> 1);
+  
+  bool ok = true, quit = false;
+  uint32_t nh = 0, ni = 0;
+  while (item < items) {
+    const int hq = (int)(item % a.nqk), h0 = hq * group;
+    int64_t next_c0 = 0;
+    int next_rows = 0;
+    const int64_t next = seek(item + gridDim.x, next_c0, next_rows);
+    const uint32_t K = base + L::kK + (ni & 1) * (uint32_t)L::kKBytes, Q = K + 2 * C * DK;
+    const float *kf = reinterpret_cast<const float*>(sm + L::kK + (ni & 1) * L::kKBytes + 4 * C * DK), *qf = kf + C, *kn = qf + C, *qn = kn + C;
+    ok &= ptx::mbar_wait_bounded(bar + 3 + (ni & 1), (ni >> 1) & 1, kWaitLimitNs);
+    if (tid == 0 && next < items) fetch_k(next, ni + 1);  // its buffer was last read before the item before ended
+    ln.again();
+    uint32_t kk[4][2], qk[4][2];  // warps 0-7: k_r . k_i and q_r . k_i, pairs of columns in fp16 (at most 1)
+    if (first) {
+      const int r0 = 16 * (w8 & 3) + ln.g, i0 = 32 * (w8 >> 2) + 2 * ln.t;
+      float xk[4][4] = {}, xq[4][4] = {};
 #pragma unroll
       for (int k = 0; k < DK; k += 16) {
-        uint32_t ak[4], aq[4], b[4];
-        frag_a<L::DP>(ak, K, wr, k, lane);
-        frag_a<L::DP>(aq, Q, wr, k, lane);
-        frag_b<L::DP>(b, K, 16 * wc, k, lane);
+        uint32_t ak[4], aq[4], b[8];
+        img_a<RK>(ak, K, 16 * (w8 & 3), k, ln);
+        img_a<RK>(aq, Q, 16 * (w8 & 3), k, ln);
+        img_b<RK>(b, K, 32 * (w8 >> 2), k, ln);
+        img_b<RK>(b + 4, K, 32 * (w8 >> 2) + 16, k, ln);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
           mma_f16(xk[j], ak, b + 2 * j);
           mma_f16(xq[j], aq, b + 2 * j);
         }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 8 * e, i = i0 + 8 * j;
+          kk[j][e] = pack2(xk[j][2 * e] * kf[r] * kf[i], xk[j][2 * e + 1] * kf[r] * kf[i + 1]);
+          qk[j][e] = pack2(xq[j][2 * e] * qf[r] * kf[i], xq[j][2 * e + 1] * qf[r] * kf[i + 1]);
+        }
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = r0 + 8 * e, i = 16 * wc + 8 * j + 2 * t4;
-        kk[j][e] = pack2(xk[j][2 * e] * kf[r] * kf[i], xk[j][2 * e + 1] * kf[r] * kf[i + 1]);
-        qk[j][e] = pack2(xq[j][2 * e] * qf[r] * kf[i], xq[j][2 * e + 1] * qf[r] * kf[i + 1]);
-      }
-  }
-  // kf dk_hat and qf dq_hat, summed over the group's v-heads
-  float dq[NK][4] = {}, dk[NK][4] = {};
+    float sum[2][NT][4] = {};  // qf dq_hat (warps 0-7) or kf dk_hat (warps 8-15), over the group's v-heads
 
-  for (int h = h0; h < h0 + group; ++h) {
-    const float* rf = reinterpret_cast<const float*>(sm + L::kF + ((h - h0) & 1) * L::kFBytes);
-    cp_wait<0>();
-    __syncthreads();
-    // this thread's share of V: rows r0, r0 + 8, columns 16 k + 2 t, + 8 for k = wc and wc + 4
-    uint32_t vraw[KV / 4][4];
+    for (int h = h0; h < h0 + group; ++h, ++nh) {
+      const float* rf = reinterpret_cast<const float*>(sm + L::kF + (nh & 1) * L::kFBytes);
+      const bool last = h + 1 == h0 + group;
+      // ---- 1.
+      ln.again();
+      ok &= ptx::mbar_wait_bounded(bar, nh & 1, kWaitLimitNs);
+      ok &= ptx::mbar_wait_bounded(bar + 1, nh & 1, kWaitLimitNs);
+      const float mV = top_factor(rf + R::fV, DV, lane), mX = top_factor(rf + R::fDV, DV, lane);
 #pragma unroll
-    for (int x = 0; x < KV / 4; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = r0 + 8 * (e & 1), c = 16 * (wc + 4 * x) + 8 * (e >> 1) + 2 * t4;
-        vraw[x][e] = r < rows ? *reinterpret_cast<const uint32_t*>(static_cast<const bf16*>(a.v) + ((size_t)(c0 + r) * a.nv + h) * DV + c) : 0u;
+      for (int x = 0; x < DV * C / 8 / kGradThreads; ++x) {
+        const int v = x * kGradThreads + tid;
+        const float f = __fdividef(rf[R::fV + v / (C / 8)], mV);
+        const uint32_t f2 = pack2(f, f);
+        uint4* at = reinterpret_cast<uint4*>(sm + L::kV) + v;
+        const uint4 p = *at;
+        *at = make_uint4(mul2(p.x, f2), mul2(p.y, f2), mul2(p.z, f2), mul2(p.w, f2));
       }
-    // one factor for a tile
-    const float mS = top_factor(rf + R::fS, DV, lane), mD = top_factor(rf + R::fD, DV, lane);
-    const float mV = top_factor(rf + R::fV, DV, lane), mX = top_factor(rf + R::fDV, DV, lane);
-    const float oinv = rf[R::fScal + kScalDo];
-    float s_dot = 0.f;
+      if (tid < C) eg[tid] = expf(rf[R::fGc + tid]);
+      {  // times 2^7 for T and 2^-7: 16 columns of Dv by 16 or 32 tokens (T's zeros above the diagonal included)
+        constexpr int NB = DV / 64;  // blocks of 16 tokens
+        const int cb = 16 * (warp % KV), ib = 16 * NB * (warp / KV);
+        const float f0 = __fdividef(rf[R::fDV + cb + ln.g], mX) * 0x1p-7f, f1 = __fdividef(rf[R::fDV + cb + ln.g + 8], mX) * 0x1p-7f;
+        float x[2 * NB][4] = {};
 #pragma unroll
-    for (int x = 0; x < DV * DK / 8 / kGradThreads; ++x) {
-      const int v = x * kGradThreads + tid, c = v / (DK / 8), at = c * L::DP + 8 * (v % (DK / 8));
-      const uint32_t fS = half2_of(__fdividef(rf[R::fS + c], mS)), fD = half2_of(__fdividef(rf[R::fD + c], mD));
-      uint4 p = *reinterpret_cast<const uint4*>(S + at), q = *reinterpret_cast<const uint4*>(D + at);
-      p = make_uint4(mul2(p.x, fS), mul2(p.y, fS), mul2(p.z, fS), mul2(p.w, fS));
-      q = make_uint4(mul2(q.x, fD), mul2(q.y, fD), mul2(q.z, fD), mul2(q.w, fD));
-      *reinterpret_cast<uint4*>(S + at) = p;
-      *reinterpret_cast<uint4*>(D + at) = q;
-      const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
+        for (int k = 0; k < 4; ++k) {
+          uint32_t af[4];
+          img_a<RC>(af, X, cb, 16 * k, ln);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = unpack2(ps[i]), w = unpack2(qs[i]);
-        s_dot = fmaf(u.x, w.x, fmaf(u.y, w.y, s_dot));
+          for (int u = 0; u < NB; ++u) {
+            uint32_t b[4];
+            img_b_t<RC>(b, T, ib + 16 * u, 16 * k, ln);
+            mma_f16(x[2 * u], af, b);
+            mma_f16(x[2 * u + 1], af, b + 2);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) {
+          sts32(img_word<RC>(Dx, cb + ln.g, ib + 8 * j + 2 * ln.t, ln.g), pack2(x[j][0] * f0, x[j][1] * f0));
+          sts32(img_word<RC>(Dx, cb + ln.g + 8, ib + 8 * j + 2 * ln.t, ln.g), pack2(x[j][2] * f1, x[j][3] * f1));
+        }
       }
-    }
-#pragma unroll
-    for (int x = 0; x < DV * C / 8 / kGradThreads; ++x) {
-      const int v = x * kGradThreads + tid, c = v / (C / 8), at = c * HP + 8 * (v % (C / 8));
-      const uint32_t f = half2_of(__fdividef(rf[R::fV + c], mV));
-      const uint4 p = *reinterpret_cast<const uint4*>(V + at);
-      *reinterpret_cast<uint4*>(V + at) = make_uint4(mul2(p.x, f), mul2(p.y, f), mul2(p.z, f), mul2(p.w, f));
-    }
-#pragma unroll
-    for (int x = 0; x < C * DV / 8 / kGradThreads; ++x) {
-      const int v = x * kGradThreads + tid, at = (v / (DV / 8)) * L::VP + 8 * (v % (DV / 8));
-      const uint4 w = *reinterpret_cast<const uint4*>(O + at);
-      const float os = __fdividef(1.f, oinv);  // a power of two
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      uint32_t r[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = bf2(u[i]);
-        r[i] = pack2(f.x * os, f.y * os);
-      }
-      *reinterpret_cast<uint4*>(O + at) = make_uint4(r[0], r[1], r[2], r[3]);
-    }
-    if (tid < C) {
-      eg[tid] = expf(rf[R::fGc + tid]);
-      el[tid] = expf(rf[R::fGc + C - 1] - rf[R::fGc + tid]);
-    }
-    __syncthreads();
-    {  // dX^T = dV'^T T, times 2^7 for T and 2^-7: 16 columns of Dv by two blocks of 16 tokens, of like cost together
-      const int cb = 16 * (warp % KV);
-      uint32_t af[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) frag_a<HP>(af[k], X, cb, 16 * k, lane);
-      const float f0 = __fdividef(rf[R::fDV + cb + g8], mX) * 0x1p-7f, f1 = __fdividef(rf[R::fDV + cb + g8 + 8], mX) * 0x1p-7f;
-#pragma unroll
-      for (int u = 0; u < KV / 4; ++u) {
-        // DV = 128: warps 0..7 take blocks 0 and 3, 8..15 blocks 1 and 2; DV = 64: one block a warp
-        const int ib = KV == 8 ? (warp < 8 ? 3 * u : 1 + u) : warp / KV;
+      quit = __syncthreads_or(!ok);
+      if (quit) break;
+      if (tid == 0 && (!last || next < items))
+        fetch_x(last ? next : item, last ? (int)(next % a.nqk) * group : h + 1, nh + 1);
+      // ---- 2.
+      ln.again();
+      ok &= ptx::mbar_wait_bounded(bar + 2, nh & 1, kWaitLimitNs);
+      const float mS = rf[R::fScal + kScalS], mD = rf[R::fScal + kScalD], oinv = rf[R::fScal + kScalDo];
+      {  // <S, dS'>: the diagonal of S^T dS', 16 columns of Dv and a share of Dk a warp
+        constexpr int KS = DK * KV / 256;  // steps of a share
+        const int cb = 16 * (warp % KV), k0 = KS * (warp / KV);
         float x[2][4] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // T's zeros above the diagonal are multiplied too: a branch would cost more
-          uint32_t b[4];
-          frag_b_t<HP>(b, T, 16 * ib, 16 * k, lane);
-          mma_f16(x[0], af[k], b);
-          mma_f16(x[1], af[k], b + 2);
+        for (int k = 0; k < KS; ++k) {
+          uint32_t af[4], b[4];
+          img_a<RK>(af, S, cb, 16 * (k0 + k), ln);
+          img_b<RK>(b, D, cb, 16 * (k0 + k), ln);
+          mma_f16(x[0], af, b);
+          mma_f16(x[1], af, b + 2);
+        }
+        const float d = warp_sum((2 * ln.t == ln.g ? x[0][0] + x[1][2] : 0.f) + (2 * ln.t + 1 == ln.g ? x[0][1] + x[1][3] : 0.f));
+        if (lane == 0) dots[warp] = d * mS * mD;
+      }
+      const float sP = oinv * mV, sA = mX * mV;
+      if (first) {
+        float f[2][2], dot[2][2];
+        {
+          float x[2][NT][4] = {};
+          gemm32<NT, 0, KV, RV, false, RK>(x, O, m0, S, n0, ln);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = m0 + 16 * m + 8 * e + ln.g;
+              f[m][e] = a.scale * eg[r] * qf[r] * oinv * mS;
+            }
+          take<NT, RK>(x, Q, m0, n0, f, sum, dot, ln);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          __half* dst = Dx + (cb + g8) * HP + 16 * ib + 8 * j + 2 * t4;
-          *reinterpret_cast<uint32_t*>(dst) = pack2(x[j][0] * f0, x[j][1] * f0);
-          *reinterpret_cast<uint32_t*>(dst + 8 * HP) = pack2(x[j][2] * f1, x[j][3] * f1);
-        }
-      }
-    }
-    // x[NK] += A fragment times 16 rows of a [DV][DP] tile: this warp's rows, its quarter of the columns of Dk
-    auto with_state = [&](float (&x)[NK][4], const uint32_t* f, int k, const __half* tile) {
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int j = 0; j < NK; j += 2) {
-        uint32_t b[4];
-        frag_b_t<L::DP>(b, tile, 8 * (NK * wc + j), 16 * k, lane);
-        mma_f16(x[j], f, b);
-        mma_f16(x[j + 1], f, b + 2);
-      }
-    };
-    // rows' dots with a tile, and x times their factors into a sum
-    auto take = [&](const float (&x)[NK][4], const __half* Y, const float (&f)[2], float (&sum)[NK][4], float (&dot)[2]) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        dot[e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          const float2 y = unpack2(*reinterpret_cast<const uint32_t*>(Y + (r0 + 8 * e) * L::DP + 8 * (NK * wc + j) + 2 * t4));
-          dot[e] = fmaf(x[j][2 * e], y.x, fmaf(x[j][2 * e + 1], y.y, dot[e]));
-          sum[j][2 * e] = fmaf(f[e], x[j][2 * e], sum[j][2 * e]);
-          sum[j][2 * e + 1] = fmaf(f[e], x[j][2 * e + 1], sum[j][2 * e + 1]);
-        }
-      }
-    };
-    float dA[2][4] = {}, dP[2][4] = {}, s_gc[2], s_bt[2] = {0.f, 0.f}, s_th[2], f[2], dot[2];
-    {  // dO S^T and dP
-      float x[NK][4] = {};
-#pragma unroll
-      for (int k = 0; k < KV; ++k) {
-        uint32_t af[4];
-        frag_a<L::VP>(af, O, wr, 16 * k, lane);
-        with_state(x, af, k, S);
-      }
-      if (low) {
+          for (int e = 0; e < 2; ++e) put_row(f[m][e] * dot[m][e], red + (w8 >> 1) * C + m0 + 16 * m + 8 * e + ln.g, ln.t);
+        ln.again();
+        const int r0 = 16 * (w8 & 3) + ln.g, i0 = 32 * (w8 >> 2) + 2 * ln.t;
+        float dA[4][4] = {}, dP[4][4] = {};
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
-          uint32_t af[4], b[4];
-          frag_a<L::VP>(af, O, wr, 16 * k, lane);
-          frag_b_t<HP>(b, V, 16 * wc, 16 * k, lane);
-          mma_f16(dP[0], af, b);
-          mma_f16(dP[1], af, b + 2);
+          uint32_t ax[4], ao[4], b[8];
+          img_a_t<RC>(ax, Dx, 16 * (w8 & 3), 16 * k, ln);
+          img_a<RV>(ao, O, 16 * (w8 & 3), 16 * k, ln);
+          img_b_t<RC>(b, V, 32 * (w8 >> 2), 16 * k, ln);
+          img_b_t<RC>(b + 4, V, 32 * (w8 >> 2) + 16, 16 * k, ln);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma_f16(dA[j], ax, b + 2 * j);
+            mma_f16(dP[j], ao, b + 2 * j);
+          }
         }
-      }
+        // ---- 3. what goes through A and P
+        const float *gc = rf + R::fGc, *bt = rf + R::fBeta;
+        float s_gc[2] = {0.f, 0.f}, s_bt[2] = {0.f, 0.f}, gr[2], br[2], qr[2], kr[2], cs[4][2];
+        constexpr float kLog2e = 1.44269504f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) f[e] = a.scale * eg[r0 + 8 * e] * qf[r0 + 8 * e] * oinv * mS;
-      take(x, Q, f, dq, dot);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) s_gc[e] = f[e] * dot[e];
-    }
-    {  // V' dS'^T
-      float x[NK][4] = {};
-#pragma unroll
-      for (int k = 0; k < KV; ++k) {
-        uint32_t af[4];
-        frag_a_t<HP>(af, V, wr, 16 * k, lane);
-        with_state(x, af, k, D);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) f[e] = el[r0 + 8 * e] * kf[r0 + 8 * e] * mV * mD;
-      take(x, K, f, dk, dot);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) s_th[e] = f[e] * dot[e];
-    }
-    __syncthreads();  // dX is here; dV', T, dS' and dO are done with
-    fetch_early(h + 1);
-    {  // dX S^T, dA; dV = diag(b) dX and its part of dbeta
-      float x[NK][4] = {};
-#pragma unroll
-      for (int k = 0; k < KV; ++k) {
-        uint32_t af[4];
-        frag_a_t<HP>(af, Dx, wr, 16 * k, lane);
-        with_state(x, af, k, S);
-      }
-      if (low) {
-#pragma unroll
-        for (int k = 0; k < KV; ++k) {
-          uint32_t af[4], b[4];
-          frag_a_t<HP>(af, Dx, wr, 16 * k, lane);
-          frag_b_t<HP>(b, V, 16 * wc, 16 * k, lane);
-          mma_f16(dA[0], af, b);
-          mma_f16(dA[1], af, b + 2);
+        for (int e = 0; e < 2; ++e) {
+          gr[e] = kLog2e * gc[r0 + 8 * e];
+          br[e] = -bt[r0 + 8 * e];
+          qr[e] = qf[r0 + 8 * e] * 0x1p6f;    // 2^14 for the factors, 2^-8
+          kr[e] = kf[r0 + 8 * e] * 0x1p-2f;   // 2^14, 2^-16
         }
-      }
+        const float sQ = a.scale * sP;
 #pragma unroll
-      for (int m = 0; m < KV / 4; ++m) {
-        const int k = wc + 4 * m;
-        uint32_t af[4];
-        frag_a_t<HP>(af, Dx, wr, 16 * k, lane);
+        for (int j = 0; j < 4; ++j)  // hidden as in Lane::again, or they would be kept unpacked
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = r0 + 8 * (e & 1), c = 16 * k + 8 * (e >> 1) + 2 * t4;
-          float2 d = unpack2(af[e]);
-          d.x *= mX;
-          d.y *= mX;
-          const float2 v = bf2(vraw[m][e]);
-          s_bt[e & 1] = fmaf(d.x, v.x, fmaf(d.y, v.y, s_bt[e & 1]));
-          const float b = rf[R::fBeta + r];
-          if (r < rows)
-            *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dv_out) + ((size_t)(c0 + r) * a.nv + h) * DV + c) =
-                ptx::pack_bf16x2(b * d.x, b * d.y);
+          for (int e = 0; e < 2; ++e) asm volatile("" : "+r"(kk[j][e]), "+r"(qk[j][e]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + 8 * j;
+          const float2 gi = *reinterpret_cast<const float2*>(gc + i), ki = *reinterpret_cast<const float2*>(kf + i);
+          cs[j][0] = cs[j][1] = 0.f;
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            const int r = r0 + 8 * e2;
+            const float2 kd2 = unpack2(kk[j][e2]), qk2 = unpack2(qk[j][e2]);
+            float nn[2], bb[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // masked before exp; the strict triangle for A
+              const float gamma = i + e <= r ? ptx::ex2_approx(fmaf(-kLog2e, e ? gi.y : gi.x, gr[e2])) : 0.f;
+              const float strict = i + e < r ? gamma : 0.f, kc = e ? ki.y : ki.x;
+              const float dp = dP[j][2 * e2 + e], da = dA[j][2 * e2 + e];
+              const float akd = sA * da * ((e ? kd2.y : kd2.x) * strict);
+              const float both = fmaf(br[e2], akd, sQ * dp * strict * (e ? qk2.y : qk2.x));
+              s_bt[e2] -= akd;
+              s_gc[e2] += both;
+              cs[j][e] += both;
+              nn[e] = dp * gamma * (qr[e2] * kc);
+              bb[e] = da * br[e2] * strict * (kr[e2] * kc);
+            }
+            sts32(img_word<RC>(N, r, i, ln.g), pack2(nn[0], nn[1]));
+            sts32(img_word<RC>(B, r, i, ln.g), pack2(bb[0], bb[1]));
+          }
         }
-      }
-      float u[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        u[e] = -eg[r0 + 8 * e] * kf[r0 + 8 * e] * mX * mS;
-        f[e] = rf[R::fBeta + r0 + 8 * e] * u[e];
-      }
-      take(x, K, f, dk, dot);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s_bt[e] = fmaf(u[e], dot[e], s_bt[e]);
-        s_gc[e] = fmaf(f[e], dot[e], s_gc[e]);
-      }
-    }
-    // what goes through A and P
-    const float sP = oinv * mV, sA = mX * mV;
-    float cs[2][2];
-    {
-      const float *gc = rf + R::fGc, *bt = rf + R::fBeta;
-      constexpr float kLog2e = 1.44269504f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i0 = 16 * wc + 8 * j + 2 * t4;
-        cs[j][0] = cs[j][1] = 0.f;
-#pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {
-          const int r = r0 + 8 * e2;
-          const float2 kd2 = unpack2(kk[j][e2]), qk2 = unpack2(qk[j][e2]);
-          float nn[2], bb[2];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int i = i0 + e;
-            // masked before exp; the strict triangle for A
-            const float gamma = i <= r ? ptx::ex2_approx(kLog2e * (gc[r] - gc[i])) : 0.f, strict = i < r ? gamma : 0.f;
-            const float dp = dP[j][2 * e2 + e], da = dA[j][2 * e2 + e];
-            const float kd = (e ? kd2.y : kd2.x) * strict, akd = sA * da * kd;
-            const float both = fmaf(-bt[r], akd, a.scale * sP * dp * strict * (e ? qk2.y : qk2.x));
-            s_bt[e2] -= akd;
-            s_gc[e2] += both;
-            cs[j][e] += both;
-            nn[e] = dp * gamma * (qf[r] * kf[i]) * 0x1p6f;                // 2^14 for the factors, 2^-8
-            bb[e] = -da * bt[r] * strict * (kf[r] * kf[i]) * 0x1p-2f;     // 2^14, 2^-16
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) cs[j][e] += __shfl_xor_sync(0xffffffffu, cs[j][e], o);
+            if (ln.g == 0) col[(w8 & 3) * C + i0 + 8 * j + e] = cs[j][e];
           }
-          *reinterpret_cast<uint32_t*>(N + r * HP + i0) = pack2(nn[0], nn[1]);
-          *reinterpret_cast<uint32_t*>(B + r * HP + i0) = pack2(bb[0], bb[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          put_row(s_gc[e], reda + (2 * (w8 >> 2)) * C + r0 + 8 * e, ln.t);
+          put_row(s_bt[e], reda + (2 * (w8 >> 2) + 1) * C + r0 + 8 * e, ln.t);
         }
+      } else {
+        float f[2][2], dot[2][2];
+        {
+          float x[2][NT][4] = {};
+          gemm32<NT, 0, KV, RC, true, RK>(x, V, m0, D, n0, ln);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = m0 + 16 * m + 8 * e + ln.g;
+              f[m][e] = expf(rf[R::fGc + C - 1] - rf[R::fGc + r]) * kf[r] * mV * mD;
+            }
+          take<NT, RK>(x, K, m0, n0, f, sum, dot, ln);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) put_row(f[m][e] * dot[m][e], red + (4 + (w8 >> 1)) * C + m0 + 16 * m + 8 * e + ln.g, ln.t);
+        ln.again();
+        const int r0 = 16 * (w8 & 3) + ln.g;
+        // this thread's share of V: rows r0, r0 + 8, columns 16 k + 2 t, + 8 of its half of the steps
+        const int k0 = (KV / 2) * (w8 >> 2);
+        uint32_t vraw[KV / 2][4];
+#pragma unroll
+        for (int k = 0; k < KV / 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = r0 + 8 * (e & 1), c = 16 * (k0 + k) + 8 * (e >> 1) + 2 * ln.t;
+            vraw[k][e] = r < rows ? *reinterpret_cast<const uint32_t*>(static_cast<const bf16*>(a.v) + ((size_t)(c0 + r) * a.nv + h) * DV + c) : 0u;
+          }
+        {
+          float x[2][NT][4] = {};
+          gemm32<NT, 0, KV, RC, true, RK>(x, Dx, m0, S, n0, ln);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = m0 + 16 * m + 8 * e + ln.g;
+              f[m][e] = -rf[R::fBeta + r] * eg[r] * kf[r] * mX * mS;
+            }
+          take<NT, RK>(x, K, m0, n0, f, sum, dot, ln);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = m0 + 16 * m + 8 * e + ln.g;
+            put_row(-eg[r] * kf[r] * mX * mS * dot[m][e], red + (8 + (w8 >> 1)) * C + r, ln.t);
+          }
+        ln.again();
+        // ---- 3. dV = diag(b) dX and its part of dbeta
+        float s_v[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KV / 2; ++k) {
+          uint32_t w[4];
+          img_a_t<RC>(w, Dx, 16 * (w8 & 3), 16 * (k0 + k), ln);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 d = unpack2(w[e]);
+            d.x *= mX;
+            d.y *= mX;
+            const float2 v = bf2(vraw[k][e]);
+            s_v[e & 1] = fmaf(d.x, v.x, fmaf(d.y, v.y, s_v[e & 1]));
+            const float b = rf[R::fBeta + r0 + 8 * (e & 1)];
+            w[e] = ptx::pack_bf16x2(b * d.x, b * d.y);
+          }
+          // lane t of a quad takes all four pairs of word t: a vector of 8 columns
+          const bool odd = ln.t & 1, up = ln.t & 2;
+          const uint32_t p0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), p1 = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+          const uint32_t a0 = odd ? p0 : w[0], a1 = odd ? w[1] : p0, b0 = odd ? p1 : w[2], b1 = odd ? w[3] : p1;
+          const uint32_t q0 = __shfl_xor_sync(0xffffffffu, up ? a0 : b0, 2), q1 = __shfl_xor_sync(0xffffffffu, up ? a1 : b1, 2);
+          const int r = r0 + 8 * (ln.t & 1), c = 16 * (k0 + k) + 8 * (ln.t >> 1);
+          if (r < rows)
+            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dv_out) + ((size_t)(c0 + r) * a.nv + h) * DV + c) =
+                up ? make_uint4(q0, q1, b0, b1) : make_uint4(a0, a1, q0, q1);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) put_row(s_v[e], reda + (4 + (w8 >> 2)) * C + r0 + 8 * e, ln.t);
+      }
+      ptx::fence_proxy_async_smem();  // V' was rewritten in place before a copy comes over it
+      __syncthreads();
+      if (tid == 0 && (!last || next < items)) fetch_rest(last ? next : item, last ? (int)(next % a.nqk) * group : h + 1);
+      // ---- 4.
+      ln.again();
+      if (first) {
+        float x[2][NT][4] = {};
+        if (m0 == 0)
+          gemm32<NT, 0, 2, RC, false, RK>(x, N, m0, K, n0, ln);
+        else
+          gemm32<NT, 0, 4, RC, false, RK>(x, N, m0, K, n0, ln);
+        const float sN = a.scale * sP * 0x1p-6f;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[m][j][e] = fmaf(sN, x[m][j][e], sum[m][j][e]);
+      } else {
+        float x[2][NT][4] = {};
+        if (m0 == 0)
+          gemm32<NT, 0, 4, RC, true, RK>(x, N, m0, Q, n0, ln);
+        else
+          gemm32<NT, 2, 4, RC, true, RK>(x, N, m0, Q, n0, ln);
+        const float sN = a.scale * sP * 0x1p-6f, sB = sA * 0x1p2f;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sum[m][j][e] = fmaf(sN, x[m][j][e], sum[m][j][e]);
+              x[m][j][e] = 0.f;
+            }
+        if (m0 == 0) {
+          gemm32<NT, 0, 2, RC, false, RK>(x, B, m0, K, n0, ln);
+          gemm32<NT, 0, 4, RC, true, RK>(x, B, m0, K, n0, ln);
+        } else {
+          gemm32<NT, 0, 4, RC, false, RK>(x, B, m0, K, n0, ln);
+          gemm32<NT, 2, 4, RC, true, RK>(x, B, m0, K, n0, ln);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[m][j][e] = fmaf(sB, x[m][j][e], sum[m][j][e]);
+      }
+      if (warp == 0) {
+        // dgc of rows 2 lane, 2 lane + 1; then the suffix sums
+        auto four = [&](int m, int r) { return (red[(4 * m) * C + r] + red[(4 * m + 1) * C + r]) + (red[(4 * m + 2) * C + r] + red[(4 * m + 3) * C + r]); };
+        float d[2], th = 0.f, bsum[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 2 * lane + e;
+          const float through = four(1, r), u = four(2, r);
+          const float cols = (col[r] + col[C + r]) + (col[2 * C + r] + col[3 * C + r]);
+          th += through;
+          d[e] = (reda[r] + reda[2 * C + r]) + four(0, r) + rf[R::fBeta + r] * u - through - cols;
+          bsum[e] = (reda[C + r] + reda[3 * C + r]) + (reda[4 * C + r] + reda[5 * C + r]) + u;
+        }
+        th = warp_sum(th);
+        const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f);
+        if (lane == 31) d[1] += th + rf[R::fScal + kScalGl] * dsum;
+        float suf = d[0] + d[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_down_sync(0xffffffffu, suf, o);
+          if (lane + o < 32) suf += y;
+        }
+        float beyond = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (lane == 31) beyond = 0.f;
+        const float dg[2] = {suf, beyond + d[1]};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (2 * lane + e < rows) {
+            const size_t at = (size_t)(c0 + 2 * lane + e) * a.nv + h;
+            static_cast<bf16*>(a.dg)[at] = __float2bfloat16_rn(dg[e]);
+            static_cast<bf16*>(a.dbeta)[at] = __float2bfloat16_rn(bsum[e]);
+          }
       }
     }
+    if (quit) break;
+    __syncthreads();  // the last v-head's sums are read
+    ln.again();
+    // the norms: with y = qf dq_hat, dq = (y - qf^2 Q16 (Q16 . y)) / (qf |q|), and dk alike
+    {
+      const uint32_t Y = first ? Q : K;
+      const float *yf = first ? qf : kf, *yn = first ? qn : kn;
+      float* part = red + (first ? 0 : 4 * C);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        s_gc[e] += __shfl_xor_sync(0xffffffffu, s_gc[e], o);
-        s_bt[e] += __shfl_xor_sync(0xffffffffu, s_bt[e], o);
-        s_th[e] += __shfl_xor_sync(0xffffffffu, s_th[e], o);
-      }
-      if (t4 == 0) {
-        red[(3 * wc + 0) * C + r0 + 8 * e] = s_gc[e];
-        red[(3 * wc + 1) * C + r0 + 8 * e] = s_bt[e];
-        red[(3 * wc + 2) * C + r0 + 8 * e] = s_th[e];
-      }
-    }
+        for (int e = 0; e < 2; ++e) {
+          const int r = m0 + 16 * m + 8 * e + ln.g;
+          float dot = 0.f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) cs[j][e] += __shfl_xor_sync(0xffffffffu, cs[j][e], o);
-        if (g8 == 0) col[(warp & 3) * C + 16 * wc + 8 * j + 2 * t4 + e] = cs[j][e];
-      }
-    s_dot = warp_sum(s_dot);
-    if (lane == 0) dots[warp] = s_dot * mS * mD;
-    __syncthreads();  // N, B and the sums are here; S and V' are done with
-    fetch_late(h + 1);
-    {  // qf dq_hat += N K16, kf dk_hat += N^T Q16 + (B + B^T) K16 (zeros of the triangle included: see dX)
-      float xq[NK][4] = {}, xn[NK][4] = {}, xb[NK][4] = {};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t an[4], ant[4], ab[4], abt[4];
-        frag_a<HP>(an, N, wr, 16 * k, lane);
-        frag_a<HP>(ab, B, wr, 16 * k, lane);
-        frag_a_t<HP>(ant, N, wr, 16 * k, lane);
-        frag_a_t<HP>(abt, B, wr, 16 * k, lane);
-#pragma unroll
-        for (int j = 0; j < NK; j += 2) {
-          uint32_t bk[4], bq[4];
-          frag_b_t<L::DP>(bk, K, 8 * (NK * wc + j), 16 * k, lane);
-          frag_b_t<L::DP>(bq, Q, 8 * (NK * wc + j), 16 * k, lane);
-          mma_f16(xq[j], an, bk);
-          mma_f16(xq[j + 1], an, bk + 2);
-          mma_f16(xb[j], ab, bk);
-          mma_f16(xb[j + 1], ab, bk + 2);
-          mma_f16(xn[j], ant, bq);
-          mma_f16(xn[j + 1], ant, bq + 2);
-          mma_f16(xb[j], abt, bk);
-          mma_f16(xb[j + 1], abt, bk + 2);
+          for (int j = 0; j < NT; ++j) {
+            const float2 y = unpack2(lds32(img_word<RK>(Y, r, n0 + 8 * j + 2 * ln.t, ln.g)));
+            dot = fmaf(sum[m][j][2 * e], y.x, fmaf(sum[m][j][2 * e + 1], y.y, dot));
+          }
+          put_row(dot, part + (w8 >> 1) * C + r, ln.t);
         }
-      }
-      const float sN = a.scale * sP * 0x1p-6f, sB = sA * 0x1p2f;
+      __syncthreads();
+      bf16* out = static_cast<bf16*>(first ? a.dq : a.dk);
 #pragma unroll
-      for (int j = 0; j < NK; ++j)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dq[j][e] = fmaf(sN, xq[j][e], dq[j][e]);
-          dk[j][e] = fmaf(sN, xn[j][e], fmaf(sB, xb[j][e], dk[j][e]));
+        for (int e = 0; e < 2; ++e) {
+          const int r = m0 + 16 * m + 8 * e + ln.g;
+          const float p = yf[r] * yf[r] * ((part[r] + part[C + r]) + (part[2 * C + r] + part[3 * C + r])), fn = yn[r];
+          uint32_t w[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const float2 y = unpack2(lds32(img_word<RK>(Y, r, n0 + 8 * j + 2 * ln.t, ln.g)));
+            w[j] = ptx::pack_bf16x2(fn * (sum[m][j][2 * e] - y.x * p), fn * (sum[m][j][2 * e + 1] - y.y * p));
+          }
+          // by swap32 this thread's pairs are neighbours: 8 columns (Dk = 128) or 4 (Dk = 64)
+          if (r < rows) {
+            bf16* dst = out + ((size_t)(c0 + r) * a.nqk + hq) * DK + swap32(n0 + 2 * ln.t);
+            if constexpr (NT == 4)
+              *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+              *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+          }
         }
     }
-    if (warp == 0) {
-      // dgc of rows 2 lane, 2 lane + 1; then the suffix sums
-      float d[2], th = 0.f, bsum[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 2 * lane + e;
-        float sum[3], cols = 0.f;
-#pragma unroll
-        for (int m = 0; m < 3; ++m) sum[m] = (red[m * C + r] + red[(3 + m) * C + r]) + (red[(6 + m) * C + r] + red[(9 + m) * C + r]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) cols += col[m * C + r];
-        th += sum[2];
-        d[e] = sum[0] - sum[2] - cols;
-        bsum[e] = sum[1];
-      }
-      th = warp_sum(th);
-      const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f);
-      if (lane == 31) d[1] += th + eg[C - 1] * dsum;
-      float suf = d[0] + d[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, suf, o);
-        if (lane + o < 32) suf += y;
-      }
-      float beyond = __shfl_down_sync(0xffffffffu, suf, 1);
-      if (lane == 31) beyond = 0.f;
-      const float dg[2] = {suf, beyond + d[1]};
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (2 * lane + e < rows) {
-          const size_t at = (size_t)(c0 + 2 * lane + e) * a.nv + h;
-          static_cast<bf16*>(a.dg)[at] = __float2bfloat16_rn(dg[e]);
-          static_cast<bf16*>(a.dbeta)[at] = __float2bfloat16_rn(bsum[e]);
-        }
-    }
+    item = next;
+    c0 = next_c0;
+    rows = next_rows;
+    ++ni;
+    __syncthreads();  // the sums and the floats of this item's last v-head are read
   }
-  __syncthreads();
-  // the norms: with y = qf dq_hat, dq = (y - qf^2 Q16 (Q16 . y)) / (qf |q|)
-  float dotq[2], dotk[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    dotq[e] = dotk[e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) {
-      const int at = (r0 + 8 * e) * L::DP + 8 * (NK * wc + j) + 2 * t4;
-      const float2 y = unpack2(*reinterpret_cast<const uint32_t*>(Q + at)), z = unpack2(*reinterpret_cast<const uint32_t*>(K + at));
-      dotq[e] = fmaf(dq[j][2 * e], y.x, fmaf(dq[j][2 * e + 1], y.y, dotq[e]));
-      dotk[e] = fmaf(dk[j][2 * e], z.x, fmaf(dk[j][2 * e + 1], z.y, dotk[e]));
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      dotq[e] += __shfl_xor_sync(0xffffffffu, dotq[e], o);
-      dotk[e] += __shfl_xor_sync(0xffffffffu, dotk[e], o);
-    }
-    if (t4 == 0) {
-      red[(2 * wc) * C + r0 + 8 * e] = dotq[e];
-      red[(2 * wc + 1) * C + r0 + 8 * e] = dotk[e];
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = r0 + 8 * e;
-    if (r >= rows) continue;
-    const float pq = qf[r] * qf[r] * ((red[r] + red[2 * C + r]) + (red[4 * C + r] + red[6 * C + r]));
-    const float pk = kf[r] * kf[r] * ((red[C + r] + red[3 * C + r]) + (red[5 * C + r] + red[7 * C + r]));
-    const size_t row = ((size_t)(c0 + r) * a.nqk + hq) * DK;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) {
-      const int p = 8 * (NK * wc + j) + 2 * t4;
-      const float2 y = unpack2(*reinterpret_cast<const uint32_t*>(Q + r * L::DP + p)), z = unpack2(*reinterpret_cast<const uint32_t*>(K + r * L::DP + p));
-      const size_t at = row + swap32(p);
-      *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dq) + at) =
-          ptx::pack_bf16x2(qn[r] * (dq[j][2 * e] - y.x * pq), qn[r] * (dq[j][2 * e + 1] - y.y * pq));
-      *reinterpret_cast<uint32_t*>(static_cast<bf16*>(a.dk) + at) =
-          ptx::pack_bf16x2(kn[r] * (dk[j][2 * e] - z.x * pk), kn[r] * (dk[j][2 * e + 1] - z.y * pk));
-    }
+  if (quit && tid == 0) {  // a copy never came: report it, wait once more for what is in flight, and leave
+    report_status(a.status, kStatusTimeout);
+    for (int i = 0; i < 3; ++i) ptx::mbar_wait_bounded(bar + i, nh & 1, kWaitLimitNs);
+    for (uint32_t i = ni; i < ni + 2; ++i) ptx::mbar_wait_bounded(bar + 3 + (i & 1), (i >> 1) & 1, kWaitLimitNs);
   }
 }
 
@@ -1214,11 +1367,13 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
     prepare_half_kernel<DK, DV><<<dim3(slots, a.nqk), kPrepThreads, PrepSmem<DK, DV>::kBytes, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = set_smem(states_half_kernel<DK, DV>, StateSmem<DK>::kBytes)) != cudaSuccess) return e;
-  states_half_kernel<DK, DV><<<dim3(2 * DV / (16 * kStateWarps), a.nv, a.num_seqs), kStateThreads, StateSmem<DK>::kBytes, stream>>>(a);
+  if ((e = set_smem(states_half_kernel<DK, DV>, StateSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
+  states_half_kernel<DK, DV><<<dim3(2, a.nv, a.num_seqs), StateSmem<DK, DV>::kThreads, StateSmem<DK, DV>::kBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.total_tokens == 0) return e;
   if ((e = set_smem(grads_half_kernel<DK, DV>, GradSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
-  grads_half_kernel<DK, DV><<<dim3(slots, a.nqk), kGradThreads, GradSmem<DK, DV>::kBytes, stream>>>(a);
+  const int64_t items = (int64_t)slots * a.nqk;
+  const unsigned int grid = (unsigned int)(items < kSms ? items : kSms);
+  grads_half_kernel<DK, DV><<<grid, kGradThreads, GradSmem<DK, DV>::kBytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -1226,14 +1381,14 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
 
 int64_t chunk_bwd_half_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv) {
   if (total_tokens == 0) return 0;
-  const int64_t c = bwdh::C;
-  const int64_t rec = 2 * (c * (c + dk + 3 * dv) + 2 * (int64_t)dk * dv) + 4 * (3 * c + 8 + 4 * dv);
-  return (total_tokens / c + num_seqs) * (nv * rec + nqk * (4 * c * dk + 16 * c));
+  const int64_t c = bwdh::C, slots = total_tokens / c + num_seqs;
+  const int64_t rec = 2 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (3 * c + 8 + 2 * dv);
+  return slots * (nv * rec + nqk * (8 * c * dk + 16 * c) + (int64_t)sizeof(bwdh::SlotInfo));
 }
 
 cudaError_t launch_chunk_bwd_half(const BwdArgs& a, int dk, int dv, cudaStream_t s) {
-  static_assert(bwdh::Rec<128, 64>::kBytes == 2 * (64 * (64 + 128 + 3 * 64) + 2 * 128 * 64) + 4 * (3 * 64 + 8 + 4 * 64), "workspace size");
-  static_assert(bwdh::QkRec<128>::kBytes == 4 * 64 * 128 + 16 * 64, "workspace size");
+  static_assert(bwdh::Rec<128, 64>::kBytes == 2 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (3 * 64 + 8 + 2 * 64), "workspace size");
+  static_assert(bwdh::QkRec<128>::kBytes == 8 * 64 * 128 + 16 * 64, "workspace size");
   if (dk == 64 && dv == 64) return bwdh::launch_one<64, 64>(a, s);
   if (dk == 64 && dv == 128) return bwdh::launch_one<64, 128>(a, s);
   if (dk == 128 && dv == 64) return bwdh::launch_one<128, 64>(a, s);
