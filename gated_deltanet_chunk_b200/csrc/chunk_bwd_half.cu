@@ -158,17 +158,17 @@ struct Lane {
 template <int RB> __device__ __forceinline__ uint32_t img_addr(uint32_t img, int row, int col, uint32_t r, uint32_t s) {
   return img + (uint32_t)(row * RB) + r * RB + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) + (((uint32_t)col >> 6) << 7);
 }
+// By address, without a memory clobber: volatile statements and barriers keep their order, and images are written
+// and read by such statements only, or on two sides of a barrier.
 __device__ __forceinline__ void ldsm(uint32_t* r, uint32_t p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(p)
-               : "memory");
+               : "r"(p));
 }
 __device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(p)
-               : "memory");
+               : "r"(p));
 }
 template <int RB> __device__ __forceinline__ void img_a(uint32_t* r, uint32_t img, int m0, int k0, const Lane& l) {
   ldsm(r, img_addr<RB>(img, m0, k0, l.ra, l.sa));
@@ -188,10 +188,10 @@ template <int RB> __device__ __forceinline__ uint32_t img_word(uint32_t img, int
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t p) {
   uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p));
   return v;
 }
-__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(p), "r"(v)); }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   using L = PrepSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
-  extern __shared__ __align__(16) uint8_t sm[];
+  extern __shared__ __align__(128) uint8_t sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int hq = blockIdx.y, group = a.nv / a.nqk;
   const int64_t slot = blockIdx.x;
@@ -937,21 +937,28 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
   // a warp's 32 rows and quarter of the columns of Dk for products with the state, its 16 rows and 32 columns of
   // the [C][C] products (warps 0-7), and its 16 rows and half of the columns of Dv for dV (warps 8-15)
   const int m0 = 32 * (w8 & 1), n0 = (DK / 4) * (w8 >> 1);
-  
+  const bool above = w8 == 4 || w8 == 5;  // rows 0..31 and columns 32..63: all above the diagonal, and never read
+  if (first && above) {
+    col[(w8 & 3) * C + 32 + lane] = 0.f;
+    if (lane < 16) reda[2 * C + 16 * (w8 & 3) + lane] = reda[3 * C + 16 * (w8 & 3) + lane] = 0.f;
+  }
   bool ok = true, quit = false;
   uint32_t nh = 0, ni = 0;
   while (item < items) {
     const int hq = (int)(item % a.nqk), h0 = hq * group;
-    int64_t next_c0 = 0;
+    int64_t next = item + gridDim.x, next_c0 = 0;
     int next_rows = 0;
-    const int64_t next = seek(item + gridDim.x, next_c0, next_rows);
+    if (next < items) {  // looked at when it has arrived
+      const SlotInfo s = *slot_info<DK, DV>(a, next / a.nqk);
+      next_c0 = s.c0;
+      next_rows = s.rows;
+    }
     const uint32_t K = base + L::kK + (ni & 1) * (uint32_t)L::kKBytes, Q = K + 2 * C * DK;
     const float *kf = reinterpret_cast<const float*>(sm + L::kK + (ni & 1) * L::kKBytes + 4 * C * DK), *qf = kf + C, *kn = qf + C, *qn = kn + C;
     ok &= ptx::mbar_wait_bounded(bar + 3 + (ni & 1), (ni >> 1) & 1, kWaitLimitNs);
-    if (tid == 0 && next < items) fetch_k(next, ni + 1);  // its buffer was last read before the item before ended
     ln.again();
     uint32_t kk[4][2], qk[4][2];  // warps 0-7: k_r . k_i and q_r . k_i, pairs of columns in fp16 (at most 1)
-    if (first) {
+    if (first && !above) {
       const int r0 = 16 * (w8 & 3) + ln.g, i0 = 32 * (w8 >> 2) + 2 * ln.t;
       float xk[4][4] = {}, xq[4][4] = {};
 #pragma unroll
@@ -1021,6 +1028,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
       }
       quit = __syncthreads_or(!ok);
       if (quit) break;
+      if (h == h0) {
+        if (next < items && next_rows == 0) next = seek(next + gridDim.x, next_c0, next_rows);
+        if (tid == 0 && next < items) fetch_k(next, ni + 1);  // its buffer was last read before the item before ended
+      }
       if (tid == 0 && (!last || next < items))
         fetch_x(last ? next : item, last ? (int)(next % a.nqk) * group : h + 1, nh + 1);
       // ---- 2.
@@ -1061,78 +1072,88 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) put_row(f[m][e] * dot[m][e], red + (w8 >> 1) * C + m0 + 16 * m + 8 * e + ln.g, ln.t);
-        ln.again();
-        const int r0 = 16 * (w8 & 3) + ln.g, i0 = 32 * (w8 >> 2) + 2 * ln.t;
-        float dA[4][4] = {}, dP[4][4] = {};
+        if (!above) {
+          ln.again();
+          const int r0 = 16 * (w8 & 3) + ln.g, i0 = 32 * (w8 >> 2) + 2 * ln.t;
+          float dA[4][4] = {}, dP[4][4] = {};
 #pragma unroll
-        for (int k = 0; k < KV; ++k) {
-          uint32_t ax[4], ao[4], b[8];
-          img_a_t<RC>(ax, Dx, 16 * (w8 & 3), 16 * k, ln);
-          img_a<RV>(ao, O, 16 * (w8 & 3), 16 * k, ln);
-          img_b_t<RC>(b, V, 32 * (w8 >> 2), 16 * k, ln);
-          img_b_t<RC>(b + 4, V, 32 * (w8 >> 2) + 16, 16 * k, ln);
+          for (int k = 0; k < KV; ++k) {
+            uint32_t ax[4], ao[4], b[8];
+            img_a_t<RC>(ax, Dx, 16 * (w8 & 3), 16 * k, ln);
+            img_a<RV>(ao, O, 16 * (w8 & 3), 16 * k, ln);
+            img_b_t<RC>(b, V, 32 * (w8 >> 2), 16 * k, ln);
+            img_b_t<RC>(b + 4, V, 32 * (w8 >> 2) + 16, 16 * k, ln);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma_f16(dA[j], ax, b + 2 * j);
+              mma_f16(dP[j], ao, b + 2 * j);
+            }
+          }
+          // ---- 3. what goes through A and P
+          const float *gc = rf + R::fGc, *bt = rf + R::fBeta;
+          float s_gc[2] = {0.f, 0.f}, s_bt[2] = {0.f, 0.f}, gr[2], br[2], qr[2], kr[2], cs[8];
+          float2 gi[4], ki[4];
+          constexpr float kLog2e = 1.44269504f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            mma_f16(dA[j], ax, b + 2 * j);
-            mma_f16(dP[j], ao, b + 2 * j);
+            gi[j] = *reinterpret_cast<const float2*>(gc + i0 + 8 * j);
+            ki[j] = *reinterpret_cast<const float2*>(kf + i0 + 8 * j);
           }
-        }
-        // ---- 3. what goes through A and P
-        const float *gc = rf + R::fGc, *bt = rf + R::fBeta;
-        float s_gc[2] = {0.f, 0.f}, s_bt[2] = {0.f, 0.f}, gr[2], br[2], qr[2], kr[2], cs[4][2];
-        constexpr float kLog2e = 1.44269504f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          gr[e] = kLog2e * gc[r0 + 8 * e];
-          br[e] = -bt[r0 + 8 * e];
-          qr[e] = qf[r0 + 8 * e] * 0x1p6f;    // 2^14 for the factors, 2^-8
-          kr[e] = kf[r0 + 8 * e] * 0x1p-2f;   // 2^14, 2^-16
-        }
-        const float sQ = a.scale * sP;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // hidden as in Lane::again, or they would be kept unpacked
-#pragma unroll
-          for (int e = 0; e < 2; ++e) asm volatile("" : "+r"(kk[j][e]), "+r"(qk[j][e]));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = i0 + 8 * j;
-          const float2 gi = *reinterpret_cast<const float2*>(gc + i), ki = *reinterpret_cast<const float2*>(kf + i);
-          cs[j][0] = cs[j][1] = 0.f;
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            const int r = r0 + 8 * e2;
-            const float2 kd2 = unpack2(kk[j][e2]), qk2 = unpack2(qk[j][e2]);
-            float nn[2], bb[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              // masked before exp; the strict triangle for A
-              const float gamma = i + e <= r ? ptx::ex2_approx(fmaf(-kLog2e, e ? gi.y : gi.x, gr[e2])) : 0.f;
-              const float strict = i + e < r ? gamma : 0.f, kc = e ? ki.y : ki.x;
-              const float dp = dP[j][2 * e2 + e], da = dA[j][2 * e2 + e];
-              const float akd = sA * da * ((e ? kd2.y : kd2.x) * strict);
-              const float both = fmaf(br[e2], akd, sQ * dp * strict * (e ? qk2.y : qk2.x));
-              s_bt[e2] -= akd;
-              s_gc[e2] += both;
-              cs[j][e] += both;
-              nn[e] = dp * gamma * (qr[e2] * kc);
-              bb[e] = da * br[e2] * strict * (kr[e2] * kc);
-            }
-            sts32(img_word<RC>(N, r, i, ln.g), pack2(nn[0], nn[1]));
-            sts32(img_word<RC>(B, r, i, ln.g), pack2(bb[0], bb[1]));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) cs[j][e] += __shfl_xor_sync(0xffffffffu, cs[j][e], o);
-            if (ln.g == 0) col[(w8 & 3) * C + i0 + 8 * j + e] = cs[j][e];
+            gr[e] = kLog2e * gc[r0 + 8 * e];
+            br[e] = -bt[r0 + 8 * e];
+            qr[e] = qf[r0 + 8 * e] * 0x1p6f;    // 2^14 for the factors, 2^-8
+            kr[e] = kf[r0 + 8 * e] * 0x1p-2f;   // 2^14, 2^-16
           }
+          const float sQ = a.scale * sP;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          put_row(s_gc[e], reda + (2 * (w8 >> 2)) * C + r0 + 8 * e, ln.t);
-          put_row(s_bt[e], reda + (2 * (w8 >> 2) + 1) * C + r0 + 8 * e, ln.t);
+          for (int j = 0; j < 4; ++j)  // hidden as in Lane::again, or they would be kept unpacked
+#pragma unroll
+            for (int e = 0; e < 2; ++e) asm volatile("" : "+r"(kk[j][e]), "+r"(qk[j][e]));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 8 * j;
+            cs[2 * j] = cs[2 * j + 1] = 0.f;
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              const int r = r0 + 8 * e2;
+              const float2 kd2 = unpack2(kk[j][e2]), qk2 = unpack2(qk[j][e2]);
+              float nn[2], bb[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // masked before exp; the strict triangle for A
+                const float gamma = i + e <= r ? ptx::ex2_approx(fmaf(-kLog2e, e ? gi[j].y : gi[j].x, gr[e2])) : 0.f;
+                const float strict = i + e < r ? gamma : 0.f, kc = e ? ki[j].y : ki[j].x;
+                const float dp = dP[j][2 * e2 + e], da = dA[j][2 * e2 + e];
+                const float akd = sA * da * ((e ? kd2.y : kd2.x) * strict);
+                const float both = fmaf(br[e2], akd, sQ * dp * strict * (e ? qk2.y : qk2.x));
+                s_bt[e2] -= akd;
+                s_gc[e2] += both;
+                cs[2 * j + e] += both;
+                nn[e] = dp * gamma * (qr[e2] * kc);
+                bb[e] = da * br[e2] * strict * (kr[e2] * kc);
+              }
+              sts32(img_word<RC>(N, r, i, ln.g), pack2(nn[0], nn[1]));
+              sts32(img_word<RC>(B, r, i, ln.g), pack2(bb[0], bb[1]));
+            }
+          }
+          // eight columns over eight rows of lanes: a lane passes on half of what it has, and ends with one column
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) {
+            const bool upper = ln.g & o;
+#pragma unroll
+            for (int m = 0; m < o; ++m) {
+              const float give = upper ? cs[m] : cs[m + o], keep = upper ? cs[m + o] : cs[m];
+              cs[m] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * o);
+            }
+          }
+          col[(w8 & 3) * C + i0 + 8 * (ln.g >> 1) + (ln.g & 1)] = cs[0];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            put_row(s_gc[e], reda + (2 * (w8 >> 2)) * C + r0 + 8 * e, ln.t);
+            put_row(s_bt[e], reda + (2 * (w8 >> 2) + 1) * C + r0 + 8 * e, ln.t);
+          }
         }
       } else {
         float f[2][2], dot[2][2];
