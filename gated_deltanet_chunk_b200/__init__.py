@@ -147,13 +147,16 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    """The raw handle of ``stream``, or of the current device's current stream (read without building a Stream object:
+    the small calls are bound by the host)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def make_params(nqk, nv, dk, dv, io_bf16, qk_l2norm=True, scale=0.0, kernel="auto") -> GdnParams:
@@ -468,6 +471,7 @@ def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu
     T, nqk, dk_ = q.shape
     nv, dv_ = v.shape[1], v.shape[2]
     n = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
+    p = make_params(nqk, nv, dk_, dv_, q.dtype == torch.bfloat16, qk_l2norm, scale, kernel)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -477,13 +481,11 @@ def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu
                                     else output_d_initial_state):
         d_initial_state = torch.empty((n, nv, dk_, dv_), dtype=torch.float32, device=q.device)
     if workspace is None:
-        need = chunk_bwd_workspace(q, v, cu_seqlens, num_seqs, qk_l2norm, kernel)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    p = make_params(nqk, nv, dk_, dv_, q.dtype == torch.bfloat16, qk_l2norm, scale, kernel)
+        workspace = _workspace(lib().gdn_chunk_bwd_workspace(int(n), int(T), ctypes.byref(p)), "gdn_chunk_bwd", q.device)
     rc = lib().gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(A_log), _ptr(dt_bias),
                              _ptr(initial_state), _ptr(dout), _ptr(d_final_state), _ptr(cu_seqlens), int(n), int(T),
                              _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(d_initial_state),
-                             _ptr(workspace), int(workspace.numel() * workspace.element_size()), ctypes.byref(p),
+                             _ptr(workspace), _bytes(workspace), ctypes.byref(p),
                              _stream(stream))
     if check and rc != GDN_OK:
         raise GdnError(rc, "gdn_chunk_bwd")
@@ -495,11 +497,15 @@ def _kept(x):
     return x if isinstance(x, tuple) else (x, None)
 
 
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
 def _workspace(need, what, device):
     import torch
     if need < 0:
         raise GdnError(need, what)
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
 def act_quantize(x, codes=None, scales=None, stream=None, check=True):
@@ -554,8 +560,8 @@ def gated_rmsnorm_bwd(dy, o, z, weight, eps=1e-6, d_o=None, d_z=None, d_weight=N
     if workspace is None:
         workspace = _workspace(lib().gdn_gated_rmsnorm_bwd_workspace(rows, int(dim), io), "gdn_gated_rmsnorm_bwd", dy.device)
     rc = lib().gdn_gated_rmsnorm_bwd(_ptr(dy), _ptr(o), _ptr(os_), _ptr(z), _ptr(zs), _ptr(weight), float(eps), _ptr(d_o),
-                                     _ptr(d_z), _ptr(d_weight), rows, int(dim), io, _ptr(workspace),
-                                     int(workspace.numel() * workspace.element_size()), _stream(stream))
+                                     _ptr(d_z), _ptr(d_weight), rows, int(dim), io, _ptr(workspace), _bytes(workspace),
+                                     _stream(stream))
     if check and rc != GDN_OK:
         raise GdnError(rc, "gdn_gated_rmsnorm_bwd")
     return d_o, d_z, d_weight
@@ -593,8 +599,8 @@ def qkv_conv_bwd(dq, dk, dv, mixed_qkv, weight, bias=None, conv_state=None, cu_s
         workspace = _workspace(lib().gdn_qkv_conv_bwd_workspace(int(T), int(K), ctypes.byref(p)), "gdn_qkv_conv_bwd", dev)
     rc = lib().gdn_qkv_conv_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(x), _ptr(xs), _ptr(weight), _ptr(bias),
                                 _ptr(conv_state), _ptr(d_state_out), _ptr(cu_seqlens), int(n), int(T), int(K), _ptr(dx),
-                                _ptr(d_weight), _ptr(d_bias), _ptr(d_state), _ptr(workspace),
-                                int(workspace.numel() * workspace.element_size()), ctypes.byref(p), _stream(stream))
+                                _ptr(d_weight), _ptr(d_bias), _ptr(d_state), _ptr(workspace), _bytes(workspace),
+                                ctypes.byref(p), _stream(stream))
     if check and rc != GDN_OK:
         raise GdnError(rc, "gdn_qkv_conv_bwd")
     return dx, d_weight, d_bias, d_state
@@ -612,14 +618,17 @@ def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt
     T, nv = a.shape
     da = torch.empty_like(dg) if da is None else da
     db = torch.empty_like(dg) if db is None else db
-    dA_log = torch.empty(nv, dtype=torch.float32, device=dg.device) if dA_log is None else dA_log
-    ddt_bias = torch.empty(nv, dtype=torch.float32, device=dg.device) if ddt_bias is None else ddt_bias
+    if dA_log is None and ddt_bias is None:
+        dA_log, ddt_bias = torch.empty((2, nv), dtype=torch.float32, device=dg.device).unbind(0)
+    elif dA_log is None or ddt_bias is None:
+        new = torch.empty(nv, dtype=torch.float32, device=dg.device)
+        dA_log, ddt_bias = (new, ddt_bias) if dA_log is None else (dA_log, new)
     if workspace is None:
         workspace = _workspace(lib().gdn_gate_bwd_workspace(int(T), int(nv)), "gdn_gate_bwd", dg.device)
     rc = lib().gdn_gate_bwd(_ptr(dg), _ptr(dbeta), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(da), _ptr(db),
                             _ptr(dA_log), _ptr(ddt_bias), int(T), int(nv),
-                            DTYPE_BF16 if dg.dtype == torch.bfloat16 else DTYPE_F32, _ptr(workspace),
-                            int(workspace.numel() * workspace.element_size()), _stream(stream))
+                            DTYPE_BF16 if dg.dtype == torch.bfloat16 else DTYPE_F32, _ptr(workspace), _bytes(workspace),
+                            _stream(stream))
     if check and rc != GDN_OK:
         raise GdnError(rc, "gdn_gate_bwd")
     return da, db, dA_log, ddt_bias
