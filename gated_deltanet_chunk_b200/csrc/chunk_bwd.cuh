@@ -1,6 +1,9 @@
 // chunk_bwd.cuh -- what the two kernel families of gdn_chunk_bwd share: chunk
-// slots, the split-TF32 warp product, the in-chunk cumsum and the inverse.
+// slots, the split-TF32 warp product, the in-chunk cumsum, the inverse, and fp16
+// products of tiles that bulk copies bring in.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "gdn_common.cuh"
 #include "sm100_ptx.cuh"
@@ -65,7 +68,14 @@ __device__ __forceinline__ void warp_gemm(float (&acc)[NT][4], int k0, int k1, F
       uint32_t bh[2], bl[2];
       split_tf32(b(kk + t, 8 * j + g), bh[0], bl[0]);
       split_tf32(b(kk + t + 4, 8 * j + g), bh[1], bl[1]);
-      mma3<!kPairs, !kPairs>(acc[j], ah, al, bh, bl);
+      if constexpr (kPairs) {  // the MMA truncates as it adds: only its 8 terms are its own
+        float d[4] = {};
+        mma3<false, false>(d, ah, al, bh, bl);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
+      } else {
+        mma3<true, true>(acc[j], ah, al, bh, bl);
+      }
     }
   }
 }
@@ -141,6 +151,108 @@ __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int l
     __syncthreads();
   }
 }
+
+// ------------------------------------------------------------------ fp16 products from images
+// An image is a tile of fp16 as it stands in shared memory, so that one bulk copy brings it in: rows of 128 or 256
+// bytes whose 16-byte vectors are swapped by their row (vector v of row r at v ^ (r & 7)), which keeps ldmatrix free
+// of bank conflicts without padding.
+
+// Where element (r, col) of an image with rows of RB bytes stands, in bytes.
+template <int RB> __device__ __forceinline__ int image(int r, int col) {
+  return r * RB + ((((col >> 3) ^ (r & 7)) << 4) | ((col & 7) * 2));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// f = 2^k with top f in [2^7, 2^8), and 1 / f.  Magnitudes below 2^-119 count as 2^-119; an infinite or
+// NaN `top` gives a finite factor, so such values stay what they are.
+__device__ __forceinline__ void pow2_factor(float top, float& f, float& inv) {
+  const uint32_t e = max((__float_as_uint(top) >> 23) & 255u, 8u);
+  f = __uint_as_float((261u - e) << 23);
+  inv = __uint_as_float((e - 7u) << 23);
+}
+
+// With g = lane / 4, t = lane % 4: A a0 (g, 2t..), a1 (g + 8, 2t..), a2 (g, 2t + 8..), a3 (g + 8, 2t + 8..),
+// B b0 (k 2t.., n g), b1 (k 2t + 8.., n g), accumulators as those of m16n8k8.
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void ldsm(uint32_t* r, const __half* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(ptx::smem_u32(p))
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t* r, const __half* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(ptx::smem_u32(p))
+               : "memory");
+}
+// What a lane adds to the address of a fragment in an image: its row and the swap of the 16-byte vectors (m0, n0 and
+// k0 are multiples of 16, so a lane's row is lane & 7 mod 8).  `again` hides the values from the compiler, which
+// would otherwise form the addresses of every product ahead of the loop around them, and spill them.
+struct Lane {
+  uint32_t ra, rb, sa, sb;   // rows of kind a (lane & 15) and b, and their swaps
+  int g, t;
+  __device__ __forceinline__ explicit Lane(int lane)
+      : ra(lane & 15), rb((lane & 7) + 8 * (lane >> 4)), sa(((lane >> 4) ^ (lane & 7)) << 4),
+        sb((((lane >> 3) & 1) ^ (lane & 7)) << 4), g(lane >> 2), t(lane & 3) {}
+  __device__ __forceinline__ void again() {
+    asm volatile("" : "+r"(ra), "+r"(rb), "+r"(sa), "+r"(sb), "+r"(g), "+r"(t));
+  }
+};
+template <int RB> __device__ __forceinline__ uint32_t img_addr(uint32_t img, int row, int col, uint32_t r, uint32_t s) {
+  return img + (uint32_t)(row * RB) + r * RB + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) + (((uint32_t)col >> 6) << 7);
+}
+// By address, without a memory clobber: volatile statements and barriers keep their order, and images are written
+// and read by such statements only, or on two sides of a barrier.
+__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(p));
+}
+__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(p));
+}
+template <int RB> __device__ __forceinline__ void img_a(uint32_t* r, uint32_t img, int m0, int k0, const Lane& l) {
+  ldsm(r, img_addr<RB>(img, m0, k0, l.ra, l.sa));
+}
+template <int RB> __device__ __forceinline__ void img_a_t(uint32_t* r, uint32_t img, int m0, int k0, const Lane& l) {
+  ldsm_t(r, img_addr<RB>(img, k0, m0, l.rb, l.sb));
+}
+template <int RB> __device__ __forceinline__ void img_b(uint32_t* r, uint32_t img, int n0, int k0, const Lane& l) {
+  ldsm(r, img_addr<RB>(img, n0, k0, l.rb, l.sb));
+}
+template <int RB> __device__ __forceinline__ void img_b_t(uint32_t* r, uint32_t img, int n0, int k0, const Lane& l) {
+  ldsm_t(r, img_addr<RB>(img, k0, n0, l.ra, l.sa));
+}
+// Words of an image in shared memory: row r (r & 7 = g), columns col, col + 1
+template <int RB> __device__ __forceinline__ uint32_t img_word(uint32_t img, int r, int col, int g) {
+  return img + (uint32_t)(r * RB + ((((((col >> 3) & 7) ^ (g & 7)) << 4) | ((col & 7) * 2)) + ((col >> 6) << 7)));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(p), "r"(v)); }
+
+// A bulk copy from global to shared memory that completes on `bar` (sizes and addresses: multiples of 16 bytes).
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   ptx::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+               : "memory");
+}
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // as in chunk_tc.cu
 
 }  // namespace bwd
 }  // namespace gdn

@@ -30,15 +30,12 @@
 namespace gdn {
 namespace bwdh {
 
-using bwd::C;
-using bwd::TP;
+using namespace bwd;
 using bf16 = __nv_bfloat16;
 
 constexpr int HP = C + 8;  // pitch of the prepare kernel's [..][64] fp16 tiles: rows 16 bytes apart in the banks
 
-// Workspace record of one (chunk slot, v-head), in bytes.  An image is a tile as it stands in shared memory, so
-// that one bulk copy brings it in: rows of 128 or 256 bytes whose 16-byte vectors are swapped by their row
-// (vector v of row r at v ^ (r & 7)), which keeps ldmatrix free of bank conflicts without padding.
+// Workspace record of one (chunk slot, v-head), in bytes; images: see chunk_bwd.cuh.
 template <int DK, int DV>
 struct Rec {
   static constexpr size_t kX = 0;                      // (P^T dO)^T fragments, then the image of dV'^T [DV][C]
@@ -97,36 +94,12 @@ __device__ __forceinline__ SlotInfo* slot_info(const BwdArgs& a, int64_t slot) {
   return reinterpret_cast<SlotInfo*>(qk_at<DK, DV>(a, slots_of<DK, DV>(a), 0)) + slot;
 }
 
-// Where element (r, col) of an image with rows of RB bytes stands, in bytes.
-template <int RB> __device__ __forceinline__ int image(int r, int col) {
-  return r * RB + ((((col >> 3) ^ (r & 7)) << 4) | ((col & 7) * 2));
-}
 // Column d of a row of 32 stands at swap32(d): lane t's columns 8 b + 2 t, + 1 of the states' accumulators
 // (b = 0..3) are next to one another, so that they are stored as one vector.  Pairs stay pairs, and the swap is its
 // own inverse.
 __device__ __forceinline__ int swap32(int d) { return (d & ~31) | (((d >> 1) & 3) << 3) | (((d >> 3) & 3) << 1) | (d & 1); }
 
 // ------------------------------------------------------------------ fragments
-// With g = lane / 4, t = lane % 4: A a0 (g, 2t..), a1 (g + 8, 2t..), a2 (g, 2t + 8..), a3 (g + 8, 2t + 8..),
-// B b0 (k 2t.., n g), b1 (k 2t + 8.., n g), accumulators as those of m16n8k8.
-__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-__device__ __forceinline__ void ldsm(uint32_t* r, const __half* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(ptx::smem_u32(p))
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_t(uint32_t* r, const __half* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(ptx::smem_u32(p))
-               : "memory");
-}
 // A (16 x 16 at row m0, k0) of a tile [m][k], or [k][m] (_t); B (16 k x 16 n: two 8-column tiles) of a
 // tile [n][k], or [k][n] (_t).  P: the tile's pitch.
 template <int P> __device__ __forceinline__ void frag_a(uint32_t* r, const __half* tile, int m0, int k0, int lane) {
@@ -142,62 +115,6 @@ template <int P> __device__ __forceinline__ void frag_b_t(uint32_t* r, const __h
   ldsm_t(r, tile + (k0 + (lane & 15)) * P + n0 + 8 * (lane >> 4));
 }
 
-// What a lane adds to the address of a fragment in an image: its row and the swap of the 16-byte vectors (m0, n0 and
-// k0 are multiples of 16, so a lane's row is lane & 7 mod 8).  `again` hides the values from the compiler, which
-// would otherwise form the addresses of every product ahead of the loop around them, and spill them.
-struct Lane {
-  uint32_t ra, rb, sa, sb;   // rows of kind a (lane & 15) and b, and their swaps
-  int g, t;
-  __device__ __forceinline__ explicit Lane(int lane)
-      : ra(lane & 15), rb((lane & 7) + 8 * (lane >> 4)), sa(((lane >> 4) ^ (lane & 7)) << 4),
-        sb((((lane >> 3) & 1) ^ (lane & 7)) << 4), g(lane >> 2), t(lane & 3) {}
-  __device__ __forceinline__ void again() {
-    asm volatile("" : "+r"(ra), "+r"(rb), "+r"(sa), "+r"(sb), "+r"(g), "+r"(t));
-  }
-};
-template <int RB> __device__ __forceinline__ uint32_t img_addr(uint32_t img, int row, int col, uint32_t r, uint32_t s) {
-  return img + (uint32_t)(row * RB) + r * RB + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) + (((uint32_t)col >> 6) << 7);
-}
-// By address, without a memory clobber: volatile statements and barriers keep their order, and images are written
-// and read by such statements only, or on two sides of a barrier.
-__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(p));
-}
-__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(p));
-}
-template <int RB> __device__ __forceinline__ void img_a(uint32_t* r, uint32_t img, int m0, int k0, const Lane& l) {
-  ldsm(r, img_addr<RB>(img, m0, k0, l.ra, l.sa));
-}
-template <int RB> __device__ __forceinline__ void img_a_t(uint32_t* r, uint32_t img, int m0, int k0, const Lane& l) {
-  ldsm_t(r, img_addr<RB>(img, k0, m0, l.rb, l.sb));
-}
-template <int RB> __device__ __forceinline__ void img_b(uint32_t* r, uint32_t img, int n0, int k0, const Lane& l) {
-  ldsm(r, img_addr<RB>(img, n0, k0, l.rb, l.sb));
-}
-template <int RB> __device__ __forceinline__ void img_b_t(uint32_t* r, uint32_t img, int n0, int k0, const Lane& l) {
-  ldsm_t(r, img_addr<RB>(img, k0, n0, l.ra, l.sa));
-}
-// Words of an image in shared memory: row r (r & 7 = g), columns col, col + 1
-template <int RB> __device__ __forceinline__ uint32_t img_word(uint32_t img, int r, int col, int g) {
-  return img + (uint32_t)(r * RB + ((((((col >> 3) & 7) ^ (g & 7)) << 4) | ((col & 7) * 2)) + ((col >> 6) << 7)));
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t p) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(p));
-  return v;
-}
-__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(p), "r"(v)); }
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -205,23 +122,6 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float2 bf2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-
-// f = 2^k with top f in [2^7, 2^8), and 1 / f.  Magnitudes below 2^-119 count as 2^-119; an infinite or
-// NaN `top` gives a finite factor, so such values stay what they are.
-__device__ __forceinline__ void pow2_factor(float top, float& f, float& inv) {
-  const uint32_t e = max((__float_as_uint(top) >> 23) & 255u, 8u);
-  f = __uint_as_float((261u - e) << 23);
-  inv = __uint_as_float((e - 7u) << 23);
-}
-
-// A bulk copy from global to shared memory that completes on `bar` (sizes and addresses: multiples of 16 bytes).
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   ptx::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
-               : "memory");
-}
-constexpr uint64_t kWaitLimitNs = 1000000000ull;  // as in chunk_tc.cu
 
 // ------------------------------------------------------------------ 1. prepare
 // One block per (slot, qk-head): K16, Q16 and their products once, then its v-heads in turn.

@@ -496,9 +496,8 @@ GDN_API int64_t gdn_chunk_bwd_workspace(int32_t num_seqs, int64_t total_tokens, 
   if (rc) return rc;
   if (num_seqs < 1 || num_seqs > 65535) return GDN_ERR_SHAPE;
   if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31)) return GDN_ERR_SHAPE;
-  return bwd_half(p) ? gdn::chunk_bwd_half_workspace(total_tokens, num_seqs, p->num_qk_heads, p->num_v_heads,
-                                                     p->head_k_dim, p->head_v_dim)
-                     : gdn::chunk_bwd_workspace(total_tokens, num_seqs, p->num_v_heads, p->head_k_dim, p->head_v_dim);
+  const auto bytes = bwd_half(p) ? gdn::chunk_bwd_half_workspace : gdn::chunk_bwd_workspace;
+  return bytes(total_tokens, num_seqs, p->num_qk_heads, p->num_v_heads, p->head_k_dim, p->head_v_dim);
 }
 
 GDN_API int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,

@@ -30,7 +30,7 @@ cudaError_t launch_conv_fwd(const ConvArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_conv_update(const ConvArgs& a, int io_bf16, cudaStream_t s);
 
 // Gradients of the chunked forward; dk, dv in {64,128}.  Workspace bytes and launch.
-int64_t chunk_bwd_workspace(int64_t total_tokens, int num_seqs, int nv, int dk, int dv);
+int64_t chunk_bwd_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv);
 cudaError_t launch_chunk_bwd(const BwdArgs& a, int dk, int dv, int io_bf16, cudaStream_t s);
 // The same for bf16 io with normalised q, k, and fp16 operands.
 int64_t chunk_bwd_half_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv);
