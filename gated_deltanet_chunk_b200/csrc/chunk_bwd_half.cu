@@ -149,17 +149,25 @@ struct PrepSmem {
 // and the factors.  DK / 8 lanes per row.  Rows so small that the norm's eps decides are scaled by 2^17, so
 // that kf and qf stay within a few powers of two of one another.
 template <int DK>
-__device__ __forceinline__ void load_qk(const bf16* x, int64_t c0, int64_t end, int heads, int head, __half* tile, uint8_t* plain,
-                                        uint8_t* swapped, float* f, float* wf, float* wn, int tid) {
+__device__ __forceinline__ void load_rows(const bf16* x, int64_t c0, int64_t end, int heads, int head,
+                                          uint4 (&w)[C * DK / 8 / kPrepThreads], int tid) {
+  constexpr int L = DK / 8, R = kPrepThreads / L;
+#pragma unroll
+  for (int p = 0; p < C / R; ++p) {
+    const int r = p * R + tid / L;
+    w[p] = make_uint4(0u, 0u, 0u, 0u);
+    if (c0 + r < end) w[p] = *reinterpret_cast<const uint4*>(x + ((size_t)(c0 + r) * heads + head) * DK + 8 * (tid % L));
+  }
+}
+template <int DK>
+__device__ __forceinline__ void store_qk(const uint4 (&vec)[C * DK / 8 / kPrepThreads], __half* tile, uint8_t* plain,
+                                         uint8_t* swapped, float* f, float* wf, float* wn, int tid) {
   constexpr int L = DK / 8, R = kPrepThreads / L;
   const int lr = tid % L;
 #pragma unroll
   for (int p = 0; p < C / R; ++p) {
     const int r = p * R + tid / L;
-    const bool valid = c0 + r < end;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (valid) w = *reinterpret_cast<const uint4*>(x + ((size_t)(c0 + r) * heads + head) * DK + 8 * lr);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t u[4] = {vec[p].x, vec[p].y, vec[p].z, vec[p].w};
     float2 v[4];
     float ss = 0.f, top = 0.f;
 #pragma unroll
@@ -191,6 +199,15 @@ __device__ __forceinline__ void load_qk(const bf16* x, int64_t c0, int64_t end, 
       wn[r] = s;
     }
   }
+}
+
+// Brings [C x DV] of v or dout into L2, a line of 128 bytes a thread
+template <int DV>
+__device__ __forceinline__ void prefetch_v(const bf16* x, int64_t c0, int64_t end, int nv, int h, int tid) {
+  constexpr int L = DV / 64;
+  const int r = tid / L;
+  if (r < C && c0 + r < end)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(x + ((size_t)(c0 + r) * nv + h) * DV + 64 * (tid % L)));
 }
 
 // [C x DV] of v or dout for this thread: NV vectors of 8, vector i at row i R + tid / L
@@ -262,8 +279,17 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
   float* qfl = reinterpret_cast<float*>(qrec + QR::kF);
 
-  load_qk<DK>(static_cast<const bf16*>(a.k), c0, end, a.nqk, hq, K, qrec + QR::kK, qrec + QR::kKs, kf, qfl, qfl + 2 * C, tid);
-  load_qk<DK>(static_cast<const bf16*>(a.q), c0, end, a.nqk, hq, Q, qrec + QR::kQ, qrec + QR::kQs, qf, qfl + C, qfl + 3 * C, tid);
+  {
+    uint4 kw[C * DK / 8 / kPrepThreads], qw[C * DK / 8 / kPrepThreads];  // all loads before the first store
+    load_rows<DK>(static_cast<const bf16*>(a.k), c0, end, a.nqk, hq, kw, tid);
+    load_rows<DK>(static_cast<const bf16*>(a.q), c0, end, a.nqk, hq, qw, tid);
+    for (int h = hq * group; h < (hq + 1) * group; ++h) {
+      prefetch_v<DV>(static_cast<const bf16*>(a.v), c0, end, a.nv, h, tid);
+      prefetch_v<DV>(static_cast<const bf16*>(a.dout), c0, end, a.nv, h, tid);
+    }
+    store_qk<DK>(kw, K, qrec + QR::kK, qrec + QR::kKs, kf, qfl, qfl + 2 * C, tid);
+    store_qk<DK>(qw, Q, qrec + QR::kQ, qrec + QR::kQs, qf, qfl + C, qfl + 3 * C, tid);
+  }
   __syncthreads();
   // warp: rows 16 wr .., columns 32 wc .. of the [C][C] products; blocks above the diagonal are not formed
   const int wr = 16 * (warp & 3), wc = 32 * (warp >> 2), r0 = wr + g8;
