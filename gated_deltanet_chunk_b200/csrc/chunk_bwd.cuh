@@ -161,6 +161,11 @@ __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int l
 template <int RB> __device__ __forceinline__ int image(int r, int col) {
   return r * RB + ((((col >> 3) ^ (r & 7)) << 4) | ((col & 7) * 2));
 }
+// Column d of a row of 32 stands at swap32(d): lane t's columns 8 b + 2 t, + 1 of the states' accumulators
+// (b = 0..3) are next to one another, so that they are stored as one vector.  Pairs stay pairs, and the swap is its
+// own inverse.
+__device__ __forceinline__ int swap32(int d) { return (d & ~31) | (((d >> 1) & 3) << 3) | (((d >> 3) & 3) << 1) | (d & 1); }
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -207,8 +212,10 @@ struct Lane {
     asm volatile("" : "+r"(ra), "+r"(rb), "+r"(sa), "+r"(sb), "+r"(g), "+r"(t));
   }
 };
-template <int RB> __device__ __forceinline__ uint32_t img_addr(uint32_t img, int row, int col, uint32_t r, uint32_t s) {
-  return img + (uint32_t)(row * RB) + r * RB + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) + (((uint32_t)col >> 6) << 7);
+// kPair: the image is a pair hi, lo, in blocks of 16 rows, hi then lo (see chunk_bwd.cu); `row` is a multiple of 16.
+template <int RB, bool kPair = false>
+__device__ __forceinline__ uint32_t img_addr(uint32_t img, int row, int col, uint32_t r, uint32_t s) {
+  return img + (uint32_t)(row * RB * (kPair ? 2 : 1)) + r * RB + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) + (((uint32_t)col >> 6) << 7);
 }
 // By address, without a memory clobber: volatile statements and barriers keep their order, and images are written
 // and read by such statements only, or on two sides of a barrier.

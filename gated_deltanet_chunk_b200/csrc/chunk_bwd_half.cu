@@ -94,11 +94,6 @@ __device__ __forceinline__ SlotInfo* slot_info(const BwdArgs& a, int64_t slot) {
   return reinterpret_cast<SlotInfo*>(qk_at<DK, DV>(a, slots_of<DK, DV>(a), 0)) + slot;
 }
 
-// Column d of a row of 32 stands at swap32(d): lane t's columns 8 b + 2 t, + 1 of the states' accumulators
-// (b = 0..3) are next to one another, so that they are stored as one vector.  Pairs stay pairs, and the swap is its
-// own inverse.
-__device__ __forceinline__ int swap32(int d) { return (d & ~31) | (((d >> 1) & 3) << 3) | (((d >> 3) & 3) << 1) | (d & 1); }
-
 // ------------------------------------------------------------------ fragments
 // A (16 x 16 at row m0, k0) of a tile [m][k], or [k][m] (_t); B (16 k x 16 n: two 8-column tiles) of a
 // tile [n][k], or [k][n] (_t).  P: the tile's pitch.
