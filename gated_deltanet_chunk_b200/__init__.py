@@ -28,6 +28,7 @@ act_quantize(x) / act_dequantize       -> (codes, scales) / x   activations kept
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -442,6 +443,40 @@ def qkv_conv_update(mixed_qkv, weight, conv_state, nqk, nv, dk, dv, bias=None, s
     return q, k, v
 
 
+def _checked(what, device, *specs):
+    """Raise ``GdnError`` (GDN_ERR_SHAPE) unless every (name, tensor, shape, dtype) given is a contiguous tensor of that
+    shape and type on ``device``: gradients often come as views, expanded or in another type."""
+    for name, t, shape, dtype in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device):
+            raise GdnError(-2, "%s (%s is not a contiguous %s tensor of shape %s on %s)"
+                           % (what, name, str(dtype).replace("torch.", ""), tuple(shape), device))
+
+
+def _on_stream(call):
+    """With ``stream=`` the whole call, its allocations too, belongs to that stream."""
+    @functools.wraps(call)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on_stream
+
+
+def _run(what, device, check, *args):
+    """Call ``what`` on the tensors' device and its current stream."""
+    import torch
+    if device.type != "cuda":
+        raise GdnError(-2, "%s (tensors on %s)" % (what, device))
+    if torch._C._cuda_getDevice() != device.index:
+        with torch.cuda.device(device):
+            return _run(what, device, check, *args)
+    rc = getattr(lib(), what)(*args, _stream(None))
+    if check and rc != GDN_OK:
+        raise GdnError(rc, what)
+
+
 def chunk_bwd_workspace(q, v, cu_seqlens=None, num_seqs=None, qk_l2norm=True, kernel="auto") -> int:
     """Bytes of workspace that ``chunk_bwd`` needs for these arguments (``gdn_chunk_bwd_workspace``)."""
     import torch
@@ -453,10 +488,10 @@ def chunk_bwd_workspace(q, v, cu_seqlens=None, num_seqs=None, qk_l2norm=True, ke
     return need
 
 
+@_on_stream
 def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu_seqlens=None, num_seqs=None,
               A_log=None, dt_bias=None, dq=None, dk=None, dv=None, dg=None, dbeta=None, d_initial_state=None,
-              output_d_initial_state=None, qk_l2norm=True, scale=0.0, kernel="auto", workspace=None, stream=None,
-              check=True):
+              output_d_initial_state=None, qk_l2norm=True, scale=0.0, kernel="auto", workspace=None, check=True):
     """Gradients of ``chunk_fwd`` (``gdn_chunk_bwd``); the inputs are those of the forward call.
 
     dout [T, Nv, Dv] (dtype of v), d_final_state [N, Nv, Dk, Dv] fp32 or None (zeros).
@@ -466,12 +501,24 @@ def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu
     when not given.  Returns ``(dq, dk, dv, dg, dbeta, d_initial_state)``, the token
     gradients in the dtype of q; d_initial_state is None unless an initial state was
     given or it was asked for.
+
+    Of this call and the training calls below: tensors of another type, shape or device
+    than stated, or that are not contiguous, are refused (``GdnError``, GDN_ERR_SHAPE).
+    The call runs on the tensors' device; with ``stream=`` it belongs to that stream as
+    if made under ``torch.cuda.stream(stream)``, what it allocates too.
     """
     import torch
     T, nqk, dk_ = q.shape
     nv, dv_ = v.shape[1], v.shape[2]
     n = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
     p = make_params(nqk, nv, dk_, dv_, q.dtype == torch.bfloat16, qk_l2norm, scale, kernel)
+    io, dev, f32, state = q.dtype, q.device, torch.float32, (n, nv, dk_, dv_)
+    _checked("gdn_chunk_bwd", dev, ("q", q, q.shape, torch.bfloat16 if io == torch.bfloat16 else f32), ("k", k, q.shape, io),
+             ("v", v, (T, nv, dv_), io), ("g", g, (T, nv), f32), ("beta", beta, (T, nv), f32), ("dout", dout, v.shape, io),
+             ("A_log", A_log, (nv,), f32), ("dt_bias", dt_bias, (nv,), f32), ("initial_state", initial_state, state, f32),
+             ("d_final_state", d_final_state, state, f32), ("cu_seqlens", cu_seqlens, (n + 1,), torch.int32), ("dq", dq, q.shape, io),
+             ("dk", dk, q.shape, io), ("dv", dv, v.shape, io), ("dg", dg, (T, nv), io), ("dbeta", dbeta, (T, nv), io),
+             ("d_initial_state", d_initial_state, state, f32))
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -480,15 +527,10 @@ def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu
     if d_initial_state is None and (initial_state is not None if output_d_initial_state is None
                                     else output_d_initial_state):
         d_initial_state = torch.empty((n, nv, dk_, dv_), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = _workspace(lib().gdn_chunk_bwd_workspace(int(n), int(T), ctypes.byref(p)), "gdn_chunk_bwd", q.device)
-    rc = lib().gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(A_log), _ptr(dt_bias),
-                             _ptr(initial_state), _ptr(dout), _ptr(d_final_state), _ptr(cu_seqlens), int(n), int(T),
-                             _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(d_initial_state),
-                             _ptr(workspace), _bytes(workspace), ctypes.byref(p),
-                             _stream(stream))
-    if check and rc != GDN_OK:
-        raise GdnError(rc, "gdn_chunk_bwd")
+    workspace = _workspace(workspace, lib().gdn_chunk_bwd_workspace(int(n), int(T), ctypes.byref(p)), "gdn_chunk_bwd", q.device)
+    _run("gdn_chunk_bwd", dev, check, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(A_log), _ptr(dt_bias),
+         _ptr(initial_state), _ptr(dout), _ptr(d_final_state), _ptr(cu_seqlens), int(n), int(T), _ptr(dq), _ptr(dk), _ptr(dv),
+         _ptr(dg), _ptr(dbeta), _ptr(d_initial_state), _ptr(workspace), _bytes(workspace), ctypes.byref(p))
     return dq, dk, dv, dg, dbeta, d_initial_state
 
 
@@ -497,18 +539,32 @@ def _kept(x):
     return x if isinstance(x, tuple) else (x, None)
 
 
+def _kept_specs(name, x, scales, shape, io):
+    """What ``_checked`` has to see of a saved activation."""
+    import torch
+    if scales is None:
+        return ((name, x, shape, io),)
+    return ((name + " codes", x, shape, torch.float8_e4m3fn),
+            (name + " scales", scales, (*shape[:-1], shape[-1] // 32), torch.uint8))
+
+
 def _bytes(workspace):
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def _workspace(need, what, device):
+def _workspace(given, need, what, device):
+    """The caller's workspace, or one of ``need`` bytes."""
     import torch
     if need < 0:
         raise GdnError(need, what)
+    if given is not None:
+        _checked(what, device, ("workspace", given, given.shape, given.dtype))
+        return given
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
-def act_quantize(x, codes=None, scales=None, stream=None, check=True):
+@_on_stream
+def act_quantize(x, codes=None, scales=None, check=True):
     """Keep an activation in 8 bits (``gdn_act_quantize``): ``(codes, scales)``.
 
     x [..., D] (bf16 or fp32, CUDA, contiguous), D a multiple of 32.  codes [..., D]
@@ -519,31 +575,35 @@ def act_quantize(x, codes=None, scales=None, stream=None, check=True):
     import torch
     if x.shape[-1] % 32 != 0:
         raise GdnError(-2, "gdn_act_quantize")
+    shape, e4m3 = (*x.shape[:-1], x.shape[-1] // 32), torch.float8_e4m3fn
+    _checked("gdn_act_quantize", x.device, ("x", x, x.shape, torch.bfloat16 if x.dtype == torch.bfloat16 else torch.float32),
+             ("codes", codes, x.shape, e4m3), ("scales", scales, shape, torch.uint8))
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        codes = torch.empty(x.shape, dtype=e4m3, device=x.device)
     if scales is None:
-        scales = torch.empty((*x.shape[:-1], x.shape[-1] // 32), dtype=torch.uint8, device=x.device)
-    rc = lib().gdn_act_quantize(_ptr(x), _ptr(codes), _ptr(scales), int(x.numel()),
-                                DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32, _stream(stream))
-    if check and rc != GDN_OK:
-        raise GdnError(rc, "gdn_act_quantize")
+        scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    _run("gdn_act_quantize", x.device, check, _ptr(x), _ptr(codes), _ptr(scales), int(x.numel()),
+         DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32)
     return codes, scales
 
 
-def act_dequantize(codes, scales, dtype, out=None, stream=None, check=True):
+@_on_stream
+def act_dequantize(codes, scales, dtype, out=None, check=True):
     """The values that ``act_quantize``'s codes and scales stand for, in ``dtype`` (``gdn_act_dequantize``)."""
     import torch
+    if codes.shape[-1] % 32 != 0 or dtype not in (torch.bfloat16, torch.float32):
+        raise GdnError(-2, "gdn_act_dequantize")
+    _checked("gdn_act_dequantize", codes.device, ("codes", codes, codes.shape, torch.float8_e4m3fn),
+             ("scales", scales, (*codes.shape[:-1], codes.shape[-1] // 32), torch.uint8), ("out", out, codes.shape, dtype))
     if out is None:
         out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-    rc = lib().gdn_act_dequantize(_ptr(codes), _ptr(scales), _ptr(out), int(codes.numel()),
-                                  DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32, _stream(stream))
-    if check and rc != GDN_OK:
-        raise GdnError(rc, "gdn_act_dequantize")
+    _run("gdn_act_dequantize", codes.device, check, _ptr(codes), _ptr(scales), _ptr(out), int(codes.numel()),
+         DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32)
     return out
 
 
-def gated_rmsnorm_bwd(dy, o, z, weight, eps=1e-6, d_o=None, d_z=None, d_weight=None, workspace=None, stream=None,
-                      check=True):
+@_on_stream
+def gated_rmsnorm_bwd(dy, o, z, weight, eps=1e-6, d_o=None, d_z=None, d_weight=None, workspace=None, check=True):
     """Gradients of ``gated_rmsnorm`` (``gdn_gated_rmsnorm_bwd``): ``(do, dz, dweight)``.
 
     dy [..., D] (bf16 or fp32; D in {64, 128}).  o and z are the forward call's inputs
@@ -553,23 +613,23 @@ def gated_rmsnorm_bwd(dy, o, z, weight, eps=1e-6, d_o=None, d_z=None, d_weight=N
     import torch
     (o, os_), (z, zs) = _kept(o), _kept(z)
     dim, bf16 = dy.shape[-1], dy.dtype == torch.bfloat16
-    rows, io = int(dy.numel() // dim), DTYPE_BF16 if bf16 else DTYPE_F32
+    rows, io, f32 = int(dy.numel() // dim), DTYPE_BF16 if bf16 else DTYPE_F32, torch.float32
+    _checked("gdn_gated_rmsnorm_bwd", dy.device, ("dy", dy, dy.shape, torch.bfloat16 if bf16 else f32),
+             *_kept_specs("o", o, os_, dy.shape, dy.dtype), *_kept_specs("z", z, zs, dy.shape, dy.dtype), ("weight", weight, (dim,), f32),
+             ("d_o", d_o, dy.shape, dy.dtype), ("d_z", d_z, dy.shape, dy.dtype), ("d_weight", d_weight, (dim,), f32))
     d_o = torch.empty_like(dy) if d_o is None else d_o
     d_z = torch.empty_like(dy) if d_z is None else d_z
     d_weight = torch.empty(dim, dtype=torch.float32, device=dy.device) if d_weight is None else d_weight
-    if workspace is None:
-        workspace = _workspace(lib().gdn_gated_rmsnorm_bwd_workspace(rows, int(dim), io), "gdn_gated_rmsnorm_bwd", dy.device)
-    rc = lib().gdn_gated_rmsnorm_bwd(_ptr(dy), _ptr(o), _ptr(os_), _ptr(z), _ptr(zs), _ptr(weight), float(eps), _ptr(d_o),
-                                     _ptr(d_z), _ptr(d_weight), rows, int(dim), io, _ptr(workspace), _bytes(workspace),
-                                     _stream(stream))
-    if check and rc != GDN_OK:
-        raise GdnError(rc, "gdn_gated_rmsnorm_bwd")
+    workspace = _workspace(workspace, lib().gdn_gated_rmsnorm_bwd_workspace(rows, int(dim), io), "gdn_gated_rmsnorm_bwd", dy.device)
+    _run("gdn_gated_rmsnorm_bwd", dy.device, check, _ptr(dy), _ptr(o), _ptr(os_), _ptr(z), _ptr(zs), _ptr(weight),
+         float(eps), _ptr(d_o), _ptr(d_z), _ptr(d_weight), rows, int(dim), io, _ptr(workspace), _bytes(workspace))
     return d_o, d_z, d_weight
 
 
+@_on_stream
 def qkv_conv_bwd(dq, dk, dv, mixed_qkv, weight, bias=None, conv_state=None, cu_seqlens=None, num_seqs=None,
                  d_state_out=None, output_d_state=None, dx=None, d_weight=None, d_bias=None, d_state=None,
-                 workspace=None, stream=None, check=True):
+                 workspace=None, check=True):
     """Gradients of ``qkv_conv_fwd`` (``gdn_qkv_conv_bwd``): ``(dx, dweight, dbias, d_conv_state)``.
 
     dq, dk [T, Nqk, Dk], dv [T, Nv, Dv] (bf16 or fp32): the gradients of the call's q, k, v.
@@ -587,7 +647,12 @@ def qkv_conv_bwd(dq, dk, dv, mixed_qkv, weight, bias=None, conv_state=None, cu_s
     n = (cu_seqlens.numel() - 1) if cu_seqlens is not None else (num_seqs or 1)
     if C != 2 * nqk * dkk + nv * dvv:
         raise GdnError(-2, "gdn_qkv_conv_bwd")
-    dev = dq.device
+    dev, io, f32, state = dq.device, dq.dtype, torch.float32, (n, C, K)
+    _checked("gdn_qkv_conv_bwd", dev, ("dq", dq, (T, nqk, dkk), torch.bfloat16 if io == torch.bfloat16 else f32),
+             ("dk", dk, dq.shape, io), ("dv", dv, (T, nv, dvv), io), *_kept_specs("mixed_qkv", x, xs, x.shape, io),
+             ("weight", weight, (C, K), f32), ("bias", bias, (C,), f32), ("conv_state", conv_state, state, io),
+             ("cu_seqlens", cu_seqlens, (n + 1,), torch.int32), ("d_state_out", d_state_out, state, io), ("dx", dx, x.shape, io),
+             ("d_weight", d_weight, (C, K), f32), ("d_bias", d_bias, (C,), f32), ("d_state", d_state, state, io))
     dx = torch.empty((T, C), dtype=dq.dtype, device=dev) if dx is None else dx
     d_weight = torch.empty((C, K), dtype=torch.float32, device=dev) if d_weight is None else d_weight
     if d_bias is None and bias is not None:
@@ -595,19 +660,15 @@ def qkv_conv_bwd(dq, dk, dv, mixed_qkv, weight, bias=None, conv_state=None, cu_s
     if d_state is None and (conv_state is not None if output_d_state is None else output_d_state):
         d_state = torch.empty((n, C, K), dtype=dq.dtype, device=dev)
     p = make_params(nqk, nv, dkk, dvv, dq.dtype == torch.bfloat16)
-    if workspace is None:
-        workspace = _workspace(lib().gdn_qkv_conv_bwd_workspace(int(T), int(K), ctypes.byref(p)), "gdn_qkv_conv_bwd", dev)
-    rc = lib().gdn_qkv_conv_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(x), _ptr(xs), _ptr(weight), _ptr(bias),
-                                _ptr(conv_state), _ptr(d_state_out), _ptr(cu_seqlens), int(n), int(T), int(K), _ptr(dx),
-                                _ptr(d_weight), _ptr(d_bias), _ptr(d_state), _ptr(workspace), _bytes(workspace),
-                                ctypes.byref(p), _stream(stream))
-    if check and rc != GDN_OK:
-        raise GdnError(rc, "gdn_qkv_conv_bwd")
+    workspace = _workspace(workspace, lib().gdn_qkv_conv_bwd_workspace(int(T), int(K), ctypes.byref(p)), "gdn_qkv_conv_bwd", dev)
+    _run("gdn_qkv_conv_bwd", dev, check, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(x), _ptr(xs), _ptr(weight), _ptr(bias),
+         _ptr(conv_state), _ptr(d_state_out), _ptr(cu_seqlens), int(n), int(T), int(K), _ptr(dx), _ptr(d_weight), _ptr(d_bias),
+         _ptr(d_state), _ptr(workspace), _bytes(workspace), ctypes.byref(p))
     return dx, d_weight, d_bias, d_state
 
 
-def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt_bias=None, workspace=None, stream=None,
-             check=True):
+@_on_stream
+def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt_bias=None, workspace=None, check=True):
     """Gradients of the layer's gate (``gdn_gate_bwd``): ``(da, db, dA_log, ddt_bias)``.
 
     dg, dbeta [T, Nv] (bf16 or fp32, as ``chunk_bwd`` returns them); a, b [T, Nv] and
@@ -616,6 +677,10 @@ def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt
     """
     import torch
     T, nv = a.shape
+    io, f32 = dg.dtype, torch.float32
+    _checked("gdn_gate_bwd", dg.device, ("dg", dg, a.shape, torch.bfloat16 if io == torch.bfloat16 else f32), ("dbeta", dbeta, a.shape, io),
+             ("a", a, a.shape, f32), ("b", b, a.shape, f32), ("A_log", A_log, (nv,), f32), ("dt_bias", dt_bias, (nv,), f32),
+             ("da", da, a.shape, io), ("db", db, a.shape, io), ("dA_log", dA_log, (nv,), f32), ("ddt_bias", ddt_bias, (nv,), f32))
     da = torch.empty_like(dg) if da is None else da
     db = torch.empty_like(dg) if db is None else db
     if dA_log is None and ddt_bias is None:
@@ -623,12 +688,8 @@ def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt
     elif dA_log is None or ddt_bias is None:
         new = torch.empty(nv, dtype=torch.float32, device=dg.device)
         dA_log, ddt_bias = (new, ddt_bias) if dA_log is None else (dA_log, new)
-    if workspace is None:
-        workspace = _workspace(lib().gdn_gate_bwd_workspace(int(T), int(nv)), "gdn_gate_bwd", dg.device)
-    rc = lib().gdn_gate_bwd(_ptr(dg), _ptr(dbeta), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(da), _ptr(db),
-                            _ptr(dA_log), _ptr(ddt_bias), int(T), int(nv),
-                            DTYPE_BF16 if dg.dtype == torch.bfloat16 else DTYPE_F32, _ptr(workspace), _bytes(workspace),
-                            _stream(stream))
-    if check and rc != GDN_OK:
-        raise GdnError(rc, "gdn_gate_bwd")
+    workspace = _workspace(workspace, lib().gdn_gate_bwd_workspace(int(T), int(nv)), "gdn_gate_bwd", dg.device)
+    _run("gdn_gate_bwd", dg.device, check, _ptr(dg), _ptr(dbeta), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias),
+         _ptr(da), _ptr(db), _ptr(dA_log), _ptr(ddt_bias), int(T), int(nv), DTYPE_BF16 if io == torch.bfloat16 else DTYPE_F32,
+         _ptr(workspace), _bytes(workspace))
     return da, db, dA_log, ddt_bias

@@ -50,7 +50,7 @@ typedef enum {
     GDN_ERR_DEVICE = -6,         /* the current device is not a compute capability 10.0 GPU */
     GDN_ERR_DEVICE_TIMEOUT = -7, /* a bounded in-kernel wait expired (see gdn_device_status) */
     GDN_ERR_SEQLENS = -8,        /* cu_seqlens contents inconsistent (see gdn_device_status) */
-    GDN_ERR_GATE = -9            /* g > 0 or NaN reached the tensor-core kernel (see gdn_device_status) */
+    GDN_ERR_GATE = -9            /* a gate outside its range reached a tensor-core kernel (see gdn_device_status) */
 } gdn_status_t;
 
 typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1 } gdn_dtype_t;
@@ -397,8 +397,10 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
  * operands (each rounded by at most 2^-12 of its value, under powers of two shared by
  * tiles) with fp32 sums and states, and need g <= 0 and 0 <= beta <= 2: a gate outside
  * leaves the results undefined and is reported as GDN_ERR_GATE.  GDN_KERNEL_SIMT, fp32
- * io and calls without qk_l2norm use operands of about fp32's accuracy (pairs of TF32)
- * and take any finite g and beta; GDN_KERNEL_TC is rejected for the latter two.  The
+ * io and calls without qk_l2norm hold each operand as a pair of fp16 numbers under such
+ * a power of two: within 2^-22 of its value, or 2^-32 of the largest of its tile (64
+ * tokens of one head; for q, k and the states one row), if that is more.  They take any
+ * finite g and beta.  GDN_KERNEL_TC is rejected for the latter two kinds of call.  The
  * workspace size depends on that choice.
  *
  * No output may overlap an input, another output or the workspace.  Tokens that
@@ -517,7 +519,8 @@ int64_t gdn_gate_bwd_workspace(int64_t tokens, int32_t num_v_heads);
  * since the last call (in this order of precedence):
  *   GDN_ERR_DEVICE_TIMEOUT  a kernel gave up a bounded wait (its outputs are undefined)
  *   GDN_ERR_SEQLENS         a kernel met an inconsistent cu_seqlens (see gdn_chunk_fwd)
- *   GDN_ERR_GATE            the tensor-core chunk kernel met a gate g > 0 or NaN
+ *   GDN_ERR_GATE            the tensor-core chunk kernel, or gdn_chunk_bwd with fp16 operands, met a gate
+ *                           g > 0 or NaN (the latter also beta outside [0, 2])
  *   GDN_OK                  nothing,
  * or GDN_ERR_CUDA if the stream reported an error.  Reports of kernels still
  * running on other streams count towards the next call.  Calls from several
