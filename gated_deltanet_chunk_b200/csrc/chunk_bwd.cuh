@@ -157,9 +157,13 @@ __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int l
 // bytes whose 16-byte vectors are swapped by their row (vector v of row r at v ^ (r & 7)), which keeps ldmatrix free
 // of bank conflicts without padding.
 
-// Where element (r, col) of an image with rows of RB bytes stands, in bytes.
+// Layout RB > 0: rows of RB bytes; -RB > 0: panels of 64 columns, -RB rows of 128 bytes each, the 128-byte swizzle
+// of the tcgen05 operand descriptors (sm100_ptx.cuh).
+template <int RB> constexpr int kRowBytes = RB > 0 ? RB : 128;
+template <int RB> constexpr int kPanel = RB > 0 ? 128 : -RB * 128;  // from one 64 columns to the next
+// Where element (r, col) of an image stands, in bytes.
 template <int RB> __device__ __forceinline__ int image(int r, int col) {
-  return r * RB + ((((col >> 3) ^ (r & 7)) << 4) | ((col & 7) * 2));
+  return r * kRowBytes<RB> + (col >> 6) * kPanel<RB> + (((((col >> 3) & 7) ^ (r & 7)) << 4) | ((col & 7) * 2));
 }
 // Column d of a row of 32 stands at swap32(d): lane t's columns 8 b + 2 t, + 1 of the states' accumulators
 // (b = 0..3) are next to one another, so that they are stored as one vector.  Pairs stay pairs, and the swap is its
@@ -215,7 +219,8 @@ struct Lane {
 // kPair: the image is a pair hi, lo, in blocks of 16 rows, hi then lo (see chunk_bwd.cu); `row` is a multiple of 16.
 template <int RB, bool kPair = false>
 __device__ __forceinline__ uint32_t img_addr(uint32_t img, int row, int col, uint32_t r, uint32_t s) {
-  return img + (uint32_t)(row * RB * (kPair ? 2 : 1)) + r * RB + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) + (((uint32_t)col >> 6) << 7);
+  return img + (uint32_t)(row * kRowBytes<RB> * (kPair ? 2 : 1)) + r * kRowBytes<RB> + (((((uint32_t)col >> 3) & 7u) << 4) ^ s) +
+         ((uint32_t)col >> 6) * kPanel<RB>;
 }
 // By address, without a memory clobber: volatile statements and barriers keep their order, and images are written
 // and read by such statements only, or on two sides of a barrier.
@@ -243,7 +248,7 @@ template <int RB> __device__ __forceinline__ void img_b_t(uint32_t* r, uint32_t 
 }
 // Words of an image in shared memory: row r (r & 7 = g), columns col, col + 1
 template <int RB> __device__ __forceinline__ uint32_t img_word(uint32_t img, int r, int col, int g) {
-  return img + (uint32_t)(r * RB + ((((((col >> 3) & 7) ^ (g & 7)) << 4) | ((col & 7) * 2)) + ((col >> 6) << 7)));
+  return img + (uint32_t)(r * kRowBytes<RB> + ((((((col >> 3) & 7) ^ (g & 7)) << 4) | ((col & 7) * 2)) + (col >> 6) * kPanel<RB>));
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t p) {
   uint32_t v;

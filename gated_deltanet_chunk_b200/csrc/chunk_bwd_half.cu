@@ -38,14 +38,14 @@ constexpr int HP = C + 8;  // pitch of the prepare kernel's [..][64] fp16 tiles:
 // Workspace record of one (chunk slot, v-head), in bytes; images: see chunk_bwd.cuh.
 template <int DK, int DV>
 struct Rec {
-  static constexpr size_t kX = 0;                      // (P^T dO)^T fragments, then the image of dV'^T [DV][C]
+  static constexpr size_t kX = 0;                      // image of (P^T dO)^T [DV][C], columns by swap32; then of dV'^T
   static constexpr size_t kT = kX + 2 * C * DV;        // image of T 2^7 [C][C]
-  static constexpr size_t kV = kT + 2 * C * C;         // U^T fragments, then the image of V'^T [DV][C]
-  static constexpr size_t kS = kV + 2 * C * DV;        // image of S^T [DV][DK] before the chunk, columns by swap32
+  static constexpr size_t kV = kT + 2 * C * C;         // image of U^T [DV][C], columns by swap32; then of V'^T
+  static constexpr size_t kS = kV + 2 * C * DV;        // image of S^T [DV][DK] before the chunk, in panels, columns by swap32
   static constexpr size_t kO = kS + 2 * DK * DV;       // image of dO [C][DV]
-  static constexpr size_t kD = kO + 2 * C * DV;        // image of dS'^T [DV][DK] behind the chunk, columns by swap32
-  static constexpr size_t kW = kD + 2 * DK * DV;       // image of W 2^7 [C][DK]
-  static constexpr size_t kOq = kW + 2 * C * DK;       // (diag(qe) dO)^T fragments
+  static constexpr size_t kD = kO + 2 * C * DV;        // of dS'^T behind the chunk, alike
+  static constexpr size_t kW = kD + 2 * DK * DV;       // image of W 2^7 [C][DK], in panels, columns by swap32
+  static constexpr size_t kOq = kW + 2 * C * DK;       // image of diag(qe) dO [C][DV], in panels
   static constexpr size_t kF = kOq + 2 * C * DV;       // floats from here:
   static constexpr int fGc = 0;                        // [C] gcum
   static constexpr int fBeta = fGc + C;                // [C] beta
@@ -63,11 +63,9 @@ enum Scal { kScalU, kScalY, kScalO, kScalGl, kScalDo, kScalS, kScalD };
 // Workspace record of one (chunk slot, qk-head), in bytes.
 template <int DK>
 struct QkRec {
-  static constexpr size_t kK = 0;                 // image of K16 [C][DK]
-  static constexpr size_t kQ = kK + 2 * C * DK;   // of Q16
-  static constexpr size_t kKs = kQ + 2 * C * DK;  // of K16 with its columns by swap32
-  static constexpr size_t kQs = kKs + 2 * C * DK;
-  static constexpr size_t kF = kQs + 2 * C * DK;  // floats [4][C]: k_hat = kf K16, q_hat = qf Q16, and kf |k|, qf |q| inverted
+  static constexpr size_t kK = 0;                // image of K16 [C][DK], in panels, columns by swap32
+  static constexpr size_t kQ = kK + 2 * C * DK;  // of Q16
+  static constexpr size_t kF = kQ + 2 * C * DK;   // floats [4][C]: k_hat = kf K16, q_hat = qf Q16, and kf |k|, qf |q| inverted
   static constexpr size_t kBytes = kF + 16 * C;
 };
 
@@ -154,9 +152,17 @@ __device__ __forceinline__ void load_rows(const bf16* x, int64_t c0, int64_t end
     if (c0 + r < end) w[p] = *reinterpret_cast<const uint4*>(x + ((size_t)(c0 + r) * heads + head) * DK + 8 * (tid % L));
   }
 }
+// Four lanes' vectors of four words each: lane m gets word m of all
+__device__ __forceinline__ void transpose4(uint4& v, int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1), b = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
+  if (odd) { v.x = a; v.z = b; } else { v.y = a; v.w = b; }
+  const uint32_t c = __shfl_xor_sync(0xffffffffu, high ? v.x : v.z, 2), d = __shfl_xor_sync(0xffffffffu, high ? v.y : v.w, 2);
+  if (high) { v.x = c; v.y = d; } else { v.z = c; v.w = d; }
+}
 template <int DK>
-__device__ __forceinline__ void store_qk(const uint4 (&vec)[C * DK / 8 / kPrepThreads], __half* tile, uint8_t* plain,
-                                         uint8_t* swapped, float* f, float* wf, float* wn, int tid) {
+__device__ __forceinline__ void store_qk(const uint4 (&vec)[C * DK / 8 / kPrepThreads], __half* tile, uint8_t* img,
+                                         float* f, float* wf, float* wn, int tid) {
   constexpr int L = DK / 8, R = kPrepThreads / L;
   const int lr = tid % L;
 #pragma unroll
@@ -184,10 +190,8 @@ __device__ __forceinline__ void store_qk(const uint4 (&vec)[C * DK / 8 / kPrepTh
     h.z = pack2(v[2].x * s, v[2].y * s);
     h.w = pack2(v[3].x * s, v[3].y * s);
     *reinterpret_cast<uint4*>(tile + r * (DK + 8) + 8 * lr) = h;
-    *reinterpret_cast<uint4*>(plain + image<2 * DK>(r, 8 * lr)) = h;
-    const uint32_t pairs[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(swapped + image<2 * DK>(r, swap32(8 * lr + 2 * i))) = pairs[i];
+    transpose4(h, lr);
+    *reinterpret_cast<uint4*>(img + image<-C>(r, (8 * lr & ~31) + 8 * (lr & 3))) = h;
     if (lr == 0) {
       f[r] = inv / sqrtf(ss + kNormEps);
       wf[r] = f[r];
@@ -244,12 +248,18 @@ __device__ __forceinline__ void store_v(const uint4 (&w)[C * DV / 8 / kPrepThrea
   }
 }
 
-// A warp's accumulators of 16 rows and 64 columns, times f, as the fragments of A operands
-__device__ __forceinline__ void store_frags(uint4* dst, const float (&x)[8][4], float f) {
+// Row g (e = 0) or g + 8 (e = 2) of a warp's accumulators, 32 columns from x on, times f: this lane's 8 columns in the
+// order of swap32, where they are one vector
+__device__ __forceinline__ uint4 swapped32(const float (*x)[4], int e, float f) {
+  return make_uint4(pack2(x[0][e] * f, x[0][e + 1] * f), pack2(x[1][e] * f, x[1][e + 1] * f), pack2(x[2][e] * f, x[2][e + 1] * f),
+                    pack2(x[3][e] * f, x[3][e + 1] * f));
+}
+// Rows 16 u .. of an image [DV][C] from accumulators, times f, columns by swap32
+__device__ __forceinline__ void store_rows(uint8_t* img, int u, const float (&x)[8][4], float f, int g, int t) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    dst[32 * j] = make_uint4(pack2(x[2 * j][0] * f, x[2 * j][1] * f), pack2(x[2 * j][2] * f, x[2 * j][3] * f),
-                             pack2(x[2 * j + 1][0] * f, x[2 * j + 1][1] * f), pack2(x[2 * j + 1][2] * f, x[2 * j + 1][3] * f));
+  for (int j = 0; j < 8; j += 4)
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) *reinterpret_cast<uint4*>(img + image<2 * C>(16 * u + g + 4 * e, 8 * j + 8 * t)) = swapped32(x + j, e, f);
 }
 
 template <int DK, int DV>
@@ -282,8 +292,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
       prefetch_v<DV>(static_cast<const bf16*>(a.v), c0, end, a.nv, h, tid);
       prefetch_v<DV>(static_cast<const bf16*>(a.dout), c0, end, a.nv, h, tid);
     }
-    store_qk<DK>(kw, K, qrec + QR::kK, qrec + QR::kKs, kf, qfl, qfl + 2 * C, tid);
-    store_qk<DK>(qw, Q, qrec + QR::kQ, qrec + QR::kQs, qf, qfl + C, qfl + 3 * C, tid);
+    store_qk<DK>(kw, K, qrec + QR::kK, kf, qfl, qfl + 2 * C, tid);
+    store_qk<DK>(qw, Q, qrec + QR::kQ, qf, qfl + C, qfl + 3 * C, tid);
   }
   __syncthreads();
   // warp: rows 16 wr .., columns 32 wc .. of the [C][C] products; blocks above the diagonal are not formed
@@ -410,13 +420,21 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         }
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; j += 4)
 #pragma unroll
         for (int e = 0; e < 4; e += 2)
-          *reinterpret_cast<uint32_t*>(rec + R::kW + image<2 * DK>(r0 + 4 * e, n0 + 8 * j + 2 * t4)) =
-              pack2(x[j][e] * 0x1p-6f, x[j][e + 1] * 0x1p-6f);
+          *reinterpret_cast<uint4*>(rec + R::kW + image<-C>(r0 + 4 * e, n0 + 8 * j + 8 * t4)) = swapped32(x + j, e, 0x1p-6f);
     }
-    // U^T = V^T (T diag(b))^T and Y^T = dO^T P, 16 columns of Dv a unit, and the fragments of (diag(qe) dO)^T
+#pragma unroll
+    for (int p = 0; p < C * DV / 8 / kPrepThreads; ++p) {  // diag(qe) dO
+      const int r = (p * kPrepThreads + tid) / (DV / 8), c = 8 * (tid % (DV / 8));
+      uint4 w = *reinterpret_cast<const uint4*>(O + r * L::VP + c);
+      const __half2 f = __half2half2(qe[r]);
+      const uint32_t q = *reinterpret_cast<const uint32_t*>(&f);
+      w = make_uint4(mul2(w.x, q), mul2(w.y, q), mul2(w.z, q), mul2(w.w, q));
+      *reinterpret_cast<uint4*>(rec + R::kOq + image<-C>(r, c)) = w;
+    }
+    // U^T = V^T (T diag(b))^T and Y^T = dO^T P, 16 columns of Dv a unit
     for (int u = warp; u < DV / 16; u += kPrepThreads / 32) {
       float x[8][4] = {};
 #pragma unroll
@@ -431,11 +449,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
           mma_f16(x[2 * j + 1], af, b + 2);
         }
       }
-      store_frags(reinterpret_cast<uint4*>(rec + R::kV) + u * 128 + lane, x, 0x1p-7f);
+      store_rows(rec + R::kV, u, x, 0x1p-7f, g8, t4);
     }
     for (int u = kPrepThreads / 32 - 1 - warp; u < DV / 16; u += kPrepThreads / 32) {
       float x[8][4] = {};
-      uint4* dst = reinterpret_cast<uint4*>(rec + R::kOq) + u * 128 + lane;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t af[4];
@@ -447,36 +464,44 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
           mma_f16(x[2 * j], af, b);
           mma_f16(x[2 * j + 1], af, b + 2);
         }
-        const uint32_t lo = *reinterpret_cast<const uint32_t*>(qe + 16 * k + 2 * t4), hi = *reinterpret_cast<const uint32_t*>(qe + 16 * k + 8 + 2 * t4);
-        dst[32 * k] = make_uint4(mul2(af[0], lo), mul2(af[1], lo), mul2(af[2], hi), mul2(af[3], hi));
       }
-      store_frags(reinterpret_cast<uint4*>(rec + R::kX) + u * 128 + lane, x, 0x1p-8f);
+      store_rows(rec + R::kX, u, x, 0x1p-8f, g8, t4);
     }
   }
 }
 
 // ------------------------------------------------------------------ 2. states
-// One block per (sequence, v-head, direction), one warp per 16 Dv columns.  A chunk's tiles come in two chunks
-// ahead, by bulk copies.  The state's largest element is joined over the block (with the barrier that frees the
-// stage), so that its image has one factor; V' and dV' keep a factor for each row (column of Dv).
+// One block of 8 warps per (sequence, v-head, direction).  S^T (or dS^T) stays in registers in fp32, a row (a column of
+// Dv) in two threads of warps w and w + 4, whose TMEM lanes it shares; a chunk is two products on the tensor cores with
+// M = 128, N = 64 (Dv = 64 leaves half of the lanes unread):
+//   x^T = S^T W^T          then  S^T = e_last S^T + (V'^T diag(kw)) K                    forwards
+//   x^T = dS'^T K^T        then  dS^T = e_last dS'^T + (diag(qe) dO)^T Q - dV'^T W       backwards
+// Their A operands are what the gradients read as well (but for kw and qe), so they are written once to shared memory
+// and leave by bulk copies.  The tiles of a chunk come in two chunks ahead.  All columns of Dk are in the order of
+// swap32, which no product sees.  The state's image has one factor, joined over the block; V' and dV' keep one a row.
+
+constexpr int kStateThreads = 256;
 
 template <int DK, int DV>
-struct StateSmem {
-  static constexpr int kThreads = 2 * DV;
-  static constexpr size_t kTile = 2 * C * DK;
-  static constexpr size_t kStage = 3 * kTile + 4 * C;   // W, K16, Q16 (backwards), kw
-  static constexpr size_t kTop = 2 * kStage;            // fp32 [2][8] the warps' largest
-  static constexpr size_t kBar = kTop + 64;             // two barriers
-  static constexpr size_t kBytes = kBar + 16;
-  static_assert(kStage % 128 == 0 && kBytes <= 232448, "shared memory budget");
+struct StateSmem {  // from a 1024-byte boundary: tiles of the 128-byte swizzle
+  static constexpr uint32_t kTile = 2 * C * DK, kRows = 2 * C * DV;
+  static constexpr uint32_t oW = 0, oK = kTile, oU = 3 * kTile, oO = oU + kRows, oF = oO + kRows;  // a stage: W; K16, Q16; U or Y; Oq
+  static constexpr uint32_t kStage = oF + 1024;         // and kw [C], Scal [8]
+  static constexpr uint32_t kS = 2 * kStage;            // S^T, panels of 128 rows
+  static constexpr uint32_t kV = kS + 2 * 128 * DK;     // V'^T [128][C]
+  static constexpr uint32_t kTop = kV + 2 * 128 * C;    // fp32 [2][8] the warps' largest; [2][128] of the halves of a row of V'
+  static constexpr uint32_t kBar = kTop + 64 + 1024;    // four barriers
+  static constexpr uint32_t kTmem = kBar + 32;
+  static constexpr uint32_t kBytes = kTmem + 16 + 1024;
+  static constexpr uint32_t kKw = oO;                   // forwards: V'^T diag(kw) [128][C] where the first stage has no Oq
+  static_assert(kBytes <= 232448, "shared memory budget");
 };
 
-// Two 16 x 8 tiles of accumulators as an A fragment, rows g and g + 8 times f0 and f1
-__device__ __forceinline__ void pack_frag(const float* lo, const float* hi, float f0, float f1, uint32_t* f) {
-  f[0] = pack2(lo[0] * f0, lo[1] * f0);
-  f[1] = pack2(lo[2] * f1, lo[3] * f1);
-  f[2] = pack2(hi[0] * f0, hi[1] * f0);
-  f[3] = pack2(hi[2] * f1, hi[3] * f1);
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 pack8(const float* x, float f) {
+  return make_uint4(pack2(x[0] * f, x[1] * f), pack2(x[2] * f, x[3] * f), pack2(x[4] * f, x[5] * f), pack2(x[6] * f, x[7] * f));
 }
 
 template <int DK, int DV, bool kBackward>
@@ -484,205 +509,227 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
   using L = StateSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
-  constexpr int ND = DK / 8, RB = 2 * DK, NW = DV / 16;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int c = 16 * warp + g;  // this thread's columns of Dv: c and c + 8
+  constexpr int NS = DK / 2;                                     // columns of Dk of a thread
+  constexpr uint32_t kCols = kBackward && DK == 128 ? 512 : 256; // TMEM: x [64], y [DK], z [DK]
+  constexpr uint32_t tY = 64, tZ = 64 + DK;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
+  const int c = 32 * (warp & 3) + lane;                          // this thread's column of Dv
+  const bool active = 32 * (warp & 3) < DV;
   const int hq = h / (a.nv / a.nqk);
-  Lane ln(lane);
-  float* tops = reinterpret_cast<float*>(sm + L::kTop);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);
+  const uint32_t base = ptx::smem_u32(sm);
+  float *tops = reinterpret_cast<float*>(sm + L::kTop), *rtops = tops + 16;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);     // a stage's copies (two), x, y and z
   int64_t start, end;
   seq_bounds(a, n, start, end);
   const int64_t chunks = (end - start + C - 1) / C, slot0 = start / C + n;
+  if (chunks == 0 && !(kBackward && a.ds0)) return;
+  if (warp == 0) {
+    ptx::tmem_alloc(reinterpret_cast<uint32_t*>(sm + L::kTmem), kCols);
+    ptx::tmem_relinquish();
+  }
 
-  float s[ND][4];  // S^T or dS^T: rows c, c + 8, columns d = 8 j + 2 t, + 1
+  float s[NS];
   const float* init = kBackward ? a.ds_final : a.s0;
   const size_t state_off = ((size_t)n * a.nv + h) * (size_t)DK * DV;
 #pragma unroll
-  for (int j = 0; j < ND; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      s[j][e] = init ? init[state_off + (size_t)(8 * j + 2 * t + (e & 1)) * DV + c + 8 * (e >> 1)] : 0.f;
+  for (int j = 0; j < NS; ++j) s[j] = init && active ? init[state_off + (size_t)swap32(NS * half + j) * DV + c] : 0.f;
 
   auto slot_of = [&](int64_t i) { return slot0 + (kBackward ? chunks - 1 - i : i); };
   auto fetch = [&](int64_t i) {  // by one thread
     if (i >= chunks) return;
     uint8_t* st = sm + (i & 1) * L::kStage;
+    uint64_t* b = bar + (i & 1);
     const uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
-    const uint8_t* qrec = qk_at<DK, DV>(a, slot_of(i), hq);
     constexpr uint32_t tiles = (kBackward ? 2 : 1) * L::kTile;
-    ptx::mbar_arrive_expect_tx(bar + (i & 1), (uint32_t)(L::kTile + tiles + 4 * C));
-    bulk_copy(st, rec + R::kW, L::kTile, bar + (i & 1));
-    bulk_copy(st + L::kTile, qrec + QR::kK, tiles, bar + (i & 1));  // Q16 stands behind K16
-    bulk_copy(st + 3 * L::kTile, rec + R::kF + 4 * R::fKw, 4 * C, bar + (i & 1));
+    ptx::mbar_arrive_expect_tx(b, L::kTile + tiles + (kBackward ? 2 : 1) * L::kRows + 4 * C + 32);
+    bulk_copy(st + L::oW, rec + R::kW, L::kTile, b);
+    bulk_copy(st + L::oK, qk_at<DK, DV>(a, slot_of(i), hq) + QR::kK, tiles, b);  // Q16 stands behind K16
+    bulk_copy(st + L::oU, rec + (kBackward ? R::kX : R::kV), L::kRows, b);
+    if (kBackward) bulk_copy(st + L::oO, rec + R::kOq, L::kRows, b);
+    bulk_copy(st + L::oF, rec + R::kF + 4 * R::fKw, 4 * C, b);
+    bulk_copy(st + L::oF + 4 * C, rec + R::kF + 4 * R::fScal, 32, b);
   };
-  // the largest element of the state over the block; also the barrier behind which a chunk's stage is free
+  // the largest element of the state over the block; also the barrier behind which a chunk's tiles are free
   auto join_top = [&](int64_t i, bool ok) {
     float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < ND; ++j) top = fmaxf(fmaxf(top, fmaxf(fabsf(s[j][0]), fabsf(s[j][1]))), fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
+    for (int j = 0; j < NS; ++j) top = fmaxf(top, fabsf(s[j]));
     const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
     if (lane == 0) tops[8 * (i & 1) + warp] = __uint_as_float(w);
     return __syncthreads_or(!ok);
   };
   if (tid == 0) {
-    ptx::mbar_init(bar, 1);
-    ptx::mbar_init(bar + 1, 1);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(bar + i, 1);
     ptx::fence_mbar_init();
   }
+  ptx::tc_fence_before();
   __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + L::kTmem);
+  const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   if (tid == 0) {
     fetch(0);
     fetch(1);
   }
   join_top(1, true);
+  const uint32_t S = base + L::kS, V = base + L::kV;
+  // this thread's 16-byte vectors of a row of 128 bytes: v ^ (c & 7)
+  const uint32_t row = (uint32_t)c * 128, sw = (uint32_t)(c & 7);
+  bool quit = false;
   for (int64_t i = 0; i < chunks; ++i) {
     uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
     float* rf = reinterpret_cast<float*>(rec + R::kF);
-    uint4 uw[4], ow[4];  // U^T or Y^T as accumulators, and (diag(qe) dO)^T as A fragments
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uw[j] = reinterpret_cast<const uint4*>(rec + (kBackward ? R::kX : R::kV))[warp * 128 + 32 * j + lane];
-      if (kBackward) ow[j] = reinterpret_cast<const uint4*>(rec + R::kOq)[warp * 128 + 32 * j + lane];
-    }
-    const float us = rf[R::fScal + (kBackward ? kScalY : kScalU)], os = rf[R::fScal + kScalO], gl = rf[R::fScal + kScalGl];
-    // the state as this chunk meets it, in fp16: kept for the gradients, and the next product's operand
+    uint8_t* st = sm + (i & 1) * L::kStage;
+    const uint32_t W = base + (uint32_t)(i & 1) * L::kStage + L::oW, K = W + L::oK, Q = K + L::kTile, Oq = W + L::oO;
+    const float *kw = reinterpret_cast<const float*>(st + L::oF), *scal = kw + C;
     float top = 0.f, sfac, sinv;
 #pragma unroll
-    for (int j = 0; j < NW; ++j) top = fmaxf(top, tops[8 * ((i + 1) & 1) + j]);
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, tops[8 * ((i + 1) & 1) + j]);
     pow2_factor(top, sfac, sinv);
-    uint32_t sf[ND / 2][4];
+    if (active) {
 #pragma unroll
-    for (int j = 0; j < ND / 2; ++j) pack_frag(s[2 * j], s[2 * j + 1], sfac, sfac, sf[j]);
-    {
-      uint8_t* img = rec + (kBackward ? R::kD : R::kS);
-#pragma unroll
-      for (int j = 0; j < ND / 4; ++j) {  // 32 columns: each lane its 8 in one vector
-        *reinterpret_cast<uint4*>(img + image<RB>(c, 32 * j + 8 * t)) = make_uint4(sf[2 * j][0], sf[2 * j][2], sf[2 * j + 1][0], sf[2 * j + 1][2]);
-        *reinterpret_cast<uint4*>(img + image<RB>(c + 8, 32 * j + 8 * t)) = make_uint4(sf[2 * j][1], sf[2 * j][3], sf[2 * j + 1][1], sf[2 * j + 1][3]);
+      for (int v = 0; v < NS / 8; ++v) {
+        const uint32_t p = (uint32_t)(NS / 8 * half + v);  // vector of the row
+        *reinterpret_cast<uint4*>(sm + L::kS + (p >> 3) * (128 * 128) + row + (((p & 7) ^ sw) << 4)) = pack8(s + 8 * v, sfac);
       }
-      if (tid == 0) rf[R::fScal + (kBackward ? kScalD : kScalS)] = sinv;
     }
-    const bool ok = ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
-    const uint8_t* st = sm + (i & 1) * L::kStage;
-    const uint32_t W = ptx::smem_u32(st), K = W + (uint32_t)L::kTile, Q = K + (uint32_t)L::kTile;
-    const float* kw = reinterpret_cast<const float*>(st + 3 * L::kTile);
-    // x = S^T W^T (forwards) or dS'^T K^T (backwards), [16 x C]
-    float x[8][4] = {};
+    bool ok = ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      ptx::tc_fence_after();
+      const uint32_t b = kBackward ? K : W;
 #pragma unroll
-    for (int k = 0; k < ND / 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t b[4];
-        img_b<RB>(b, kBackward ? K : W, 16 * j, 16 * k, ln);
-        mma_f16(x[2 * j], sf[k], b);
-        mma_f16(x[2 * j + 1], sf[k], b + 2);
-      }
-    // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw)
-    float rtop[2] = {0.f, 0.f}, vfac[2], vinv[2];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint4 w = uw[j / 2];
-      const float2 u0 = unpack2(j & 1 ? w.z : w.x), u1 = unpack2(j & 1 ? w.w : w.y);
-      float2 f = make_float2(-0x1p-7f * sinv, -0x1p-7f * sinv);
+      for (int k = 0; k < DK / 16; ++k)
+        ptx::mma_bf16(tmem, ptx::sdesc_sw128(S + (k >> 2) * (128 * 128) + 32 * (k & 3), 16, 1024),
+                      ptx::sdesc_sw128(b + (k >> 2) * (128 * C) + 32 * (k & 3), 16, 1024), ptx::idesc_f16_f32(128, 64, false, false), k > 0);
+      ptx::mma_commit(bar + 2);
       if (kBackward) {
-        f = *reinterpret_cast<const float2*>(kw + 8 * j + 2 * t);
-        f.x *= sinv;
-        f.y *= sinv;
+#pragma unroll
+        for (int m = 0; m < DK / 64; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_bf16(tmem + tZ + 64 * m, ptx::sdesc_sw128(Oq + 2048 * k, 128 * C, 1024),
+                          ptx::sdesc_sw128(Q + m * (128 * C) + 2048 * k, 128 * C, 1024), ptx::idesc_f16_f32(128, 64, true, true), k > 0);
       }
-      x[j][0] = fmaf(x[j][0], f.x, us * u0.x);
-      x[j][1] = fmaf(x[j][1], f.y, us * u0.y);
-      x[j][2] = fmaf(x[j][2], f.x, us * u1.x);
-      x[j][3] = fmaf(x[j][3], f.y, us * u1.y);
-      rtop[0] = fmaxf(rtop[0], fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
-      rtop[1] = fmaxf(rtop[1], fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+    } else if (tid == 32) {
+#pragma unroll
+      for (int m = 0; m < DK / 64; ++m) bulk_store(rec + (kBackward ? R::kD : R::kS) + m * (128 * DV), S + m * (128 * 128), 128 * DV);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      rf[R::fScal + (kBackward ? kScalD : kScalS)] = sinv;
     }
+    const float us = scal[kBackward ? kScalY : kScalU], os = scal[kScalO], gl = scal[kScalGl];
+    // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw)
+    float x[32], vfac = 0.f, vinv = 0.f;
+    ok = ptx::mbar_wait_bounded(bar + 2, (uint32_t)(i & 1), kWaitLimitNs) && ok;
+    ptx::tc_fence_after();
+    if (active) {
+      ptx::tmem_ld32(tl + 32 * half, x);
+      uint4 u[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      rtop[e] = fmaxf(rtop[e], __shfl_xor_sync(0xffffffffu, rtop[e], 1));
-      rtop[e] = fmaxf(rtop[e], __shfl_xor_sync(0xffffffffu, rtop[e], 2));
-      pow2_factor(rtop[e], vfac[e], vinv[e]);
-    }
-    uint32_t vf[4][4];
+      for (int t = 0; t < 4; ++t) u[t] = *reinterpret_cast<const uint4*>(st + L::oU + row + (((uint32_t)(4 * half + t) ^ sw) << 4));
+      ptx::tmem_ld_wait();
+      float rtop = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) pack_frag(x[2 * j], x[2 * j + 1], vfac[0], vfac[1], vf[j]);
-    __syncwarp();  // the fragments of U or Y that these rows replace (the same 2 KB) are all read
-    {
-      uint8_t* img = rec + (kBackward ? R::kX : R::kV);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint32_t*>(img + image<2 * C>(c + 8 * (e & 1), 16 * j + 8 * (e >> 1) + 2 * t)) = vf[j][e];
-      if (t == 0) {
-        rf[(kBackward ? R::fDV : R::fV) + c] = vinv[0];
-        rf[(kBackward ? R::fDV : R::fV) + c + 8] = vinv[1];
+      for (int j = 0; j < 32; j += 2) {  // columns j, j + 1 of this half stand in vector (j / 2) % 4, word j / 8
+        const uint4& v = u[(j >> 1) & 3];
+        const float2 y = unpack2(j < 8 ? v.x : j < 16 ? v.y : j < 24 ? v.z : v.w);
+        float2 f = make_float2(-0x1p-7f * sinv, -0x1p-7f * sinv);
+        if (kBackward) {
+          f = *reinterpret_cast<const float2*>(kw + 32 * half + j);
+          f.x *= sinv;
+          f.y *= sinv;
+        }
+        x[j] = fmaf(x[j], f.x, us * y.x);
+        x[j + 1] = fmaf(x[j + 1], f.y, us * y.y);
+        rtop = fmaxf(rtop, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
       }
-    }
-    // forwards S^T = e_last S^T + (V' diag(kw))^T K, backwards dS^T = e_last dS'^T + (dO diag(qe))^T Q - dV'^T W
-    const float f0 = vinv[0] * (kBackward ? -0x1p-7f : 0x1p-7f), f1 = vinv[1] * (kBackward ? -0x1p-7f : 0x1p-7f);
-    if (!kBackward) {
+      rtops[128 * half + c] = rtop;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // warps w and w + 4
+      pow2_factor(fmaxf(rtop, rtops[128 * (half ^ 1) + c]), vfac, vinv);
+      if (half == 0) rf[(kBackward ? R::fDV : R::fV) + c] = vinv;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 lo = *reinterpret_cast<const float2*>(kw + 16 * j + 2 * t);
-        const float2 hi = *reinterpret_cast<const float2*>(kw + 16 * j + 8 + 2 * t);
-        const uint32_t l2 = pack2(lo.x * 0x1p7f, lo.y * 0x1p7f), h2 = pack2(hi.x * 0x1p7f, hi.y * 0x1p7f);
-        vf[j][0] = mul2(vf[j][0], l2);
-        vf[j][1] = mul2(vf[j][1], l2);
-        vf[j][2] = mul2(vf[j][2], h2);
-        vf[j][3] = mul2(vf[j][3], h2);
-      }
-    }
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t at = row + (((uint32_t)(4 * half + t) ^ sw) << 4);
+        *reinterpret_cast<uint4*>(sm + L::kV + at) = pack8(x + 8 * t, vfac);
+        if (!kBackward) {
 #pragma unroll
-    for (int m = 0; m < ND; m += 8) {  // 64 columns of Dk at a time
-      float y[8][4] = {}, z[8][4] = {};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t b[4];
-          img_b_t<RB>(b, kBackward ? W : K, 8 * m + 16 * j, 16 * k, ln);
-          mma_f16(y[2 * j], vf[k], b);
-          mma_f16(y[2 * j + 1], vf[k], b + 2);
-          if (kBackward) {
-            const uint32_t of[4] = {ow[k].x, ow[k].y, ow[k].z, ow[k].w};
-            img_b_t<RB>(b, Q, 8 * m + 16 * j, 16 * k, ln);
-            mma_f16(z[2 * j], of, b);
-            mma_f16(z[2 * j + 1], of, b + 2);
+          for (int e = 0; e < 8; e += 2) {
+            const float2 w = *reinterpret_cast<const float2*>(kw + 32 * half + 8 * t + e);
+            x[8 * t + e] *= w.x * 0x1p7f;  // kw 2^7 is at most 1
+            x[8 * t + e + 1] *= w.y * 0x1p7f;
           }
+          *reinterpret_cast<uint4*>(sm + L::kKw + at) = pack8(x + 8 * t, vfac);
         }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = gl * s[m + j][e];
-          if (kBackward) v = fmaf(os, z[j][e], v);
-          s[m + j][e] = fmaf(e < 2 ? f0 : f1, y[j][e], v);
-        }
+      }
     }
-    if (join_top(i, ok)) {  // a copy never came: report it, wait once more for what is in flight, and leave
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      ptx::tc_fence_after();
+      const uint32_t A = kBackward ? V : base + L::kKw, b = kBackward ? W : K;
+#pragma unroll
+      for (int m = 0; m < DK / 64; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ptx::mma_bf16(tmem + tY + 64 * m, ptx::sdesc_sw128(A + 32 * k, 16, 1024),
+                        ptx::sdesc_sw128(b + m * (128 * C) + 2048 * k, 128 * C, 1024), ptx::idesc_f16_f32(128, 64, false, true), k > 0);
+      ptx::mma_commit(bar + 3);
+    } else if (tid == 32) {
+      bulk_store(rec + (kBackward ? R::kX : R::kV), V, L::kRows);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    const float fy = vinv * (kBackward ? -0x1p-7f : 0x1p-7f);
+    ok = ptx::mbar_wait_bounded(bar + 3, (uint32_t)(i & 1), kWaitLimitNs) && ok;
+    ptx::tc_fence_after();
+    if (active) {
+#pragma unroll
+      for (int m = 0; m < NS; m += 32) {
+        float z[kBackward ? 32 : 1];
+        ptx::tmem_ld32(tl + tY + NS * half + m, x);
+        if constexpr (kBackward) ptx::tmem_ld32(tl + tZ + NS * half + m, z);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float v = gl * s[m + j];
+          if constexpr (kBackward) v = fmaf(os, z[j], v);
+          s[m + j] = fmaf(fy, x[j], v);
+        }
+      }
+    }
+    ptx::tc_fence_before();
+    if (tid == 32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // S and V may be written again
+    quit = join_top(i, ok);
+    if (quit) {  // a copy or a product never came: report it, wait once more for what is in flight, and leave
       if (tid == 0) {
         report_status(a.status, kStatusTimeout);
         ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
         if (i + 1 < chunks) ptx::mbar_wait_bounded(bar + ((i + 1) & 1), (uint32_t)(((i + 1) >> 1) & 1), kWaitLimitNs);
+        ptx::mbar_wait_bounded(bar + 2, (uint32_t)(i & 1), kWaitLimitNs);
+        ptx::mbar_wait_bounded(bar + 3, (uint32_t)(i & 1), kWaitLimitNs);
       }
-      return;
+      break;
     }
     if (tid == 0) fetch(i + 2);
   }
-  if (kBackward && a.ds0) {
+  if (kBackward && a.ds0 && active && !quit) {
 #pragma unroll
-    for (int j = 0; j < ND; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        a.ds0[state_off + (size_t)(8 * j + 2 * t + (e & 1)) * DV + c + 8 * (e >> 1)] = s[j][e];
+    for (int j = 0; j < NS; ++j) a.ds0[state_off + (size_t)swap32(NS * half + j) * DV + c] = s[j];
   }
+  if (tid == 32) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 0) ptx::tmem_dealloc(tmem, kCols);
 }
 
 // blockIdx.x: direction, y: v-head, z: sequence
 template <int DK, int DV>
-__global__ void __launch_bounds__(2 * DV) states_half_kernel(BwdArgs a) {
-  extern __shared__ __align__(128) uint8_t sm[];
+__global__ void __launch_bounds__(kStateThreads) states_half_kernel(BwdArgs a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
   if (blockIdx.x == 0)
     walk<DK, DV, true>(a, sm, blockIdx.z, blockIdx.y);
   else
@@ -714,7 +761,7 @@ struct GradSmem {
   static constexpr size_t kN = kDx + 2 * C * DV;              // N and B, images [C][C]
   static constexpr size_t kB = kN + 2 * C * C;
   static constexpr size_t kK = kB + 2 * C * C;                // two of: K16, Q16 (columns by swap32) and their floats
-  static constexpr size_t kKBytes = QkRec<DK>::kBytes - QkRec<DK>::kKs;
+  static constexpr size_t kKBytes = QkRec<DK>::kBytes;
   static constexpr size_t kF = kK + 2 * kKBytes;              // two of: the record's floats up to fKw
   static constexpr size_t kFBytes = 4 * R::fKw;
   static constexpr size_t kE = kF + 2 * kFBytes;              // fp32 [C] e
@@ -797,7 +844,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
   extern __shared__ __align__(128) uint8_t sm[];
   constexpr int NT = DK / 32;        // 8-column tiles of a warp's quarter of Dk
   constexpr int KV = DV / 16;        // steps over the columns of Dv
-  constexpr int RK = 2 * DK, RV = 2 * DV, RC = 2 * C;  // bytes of an image's rows
+  constexpr int RK = -C, RS = -DV, RV = 2 * DV, RC = 2 * C;  // layouts of K and Q, S and dS, dO, the rest
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Lane ln(lane);
   const bool first = warp < 8;       // warps 0-7, which keep dq
@@ -843,7 +890,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
   auto fetch_k = [&](int64_t w, uint32_t ni) {
     const uint8_t* qrec = qk_at<DK, DV>(a, w / a.nqk, (int)(w % a.nqk));
     ptx::mbar_arrive_expect_tx(bar + 3 + (ni & 1), (uint32_t)L::kKBytes);
-    bulk_copy(sm + L::kK + (ni & 1) * L::kKBytes, qrec + QR::kKs, L::kKBytes, bar + 3 + (ni & 1));
+    bulk_copy(sm + L::kK + (ni & 1) * L::kKBytes, qrec + QR::kK, L::kKBytes, bar + 3 + (ni & 1));
   };
   if (tid == 0) {
     for (int i = 0; i < 5; ++i) ptx::mbar_init(bar + i, 1);
@@ -966,8 +1013,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint32_t af[4], b[4];
-          img_a<RK>(af, S, cb, 16 * (k0 + k), ln);
-          img_b<RK>(b, D, cb, 16 * (k0 + k), ln);
+          img_a<RS>(af, S, cb, 16 * (k0 + k), ln);
+          img_b<RS>(b, D, cb, 16 * (k0 + k), ln);
           mma_f16(x[0], af, b);
           mma_f16(x[1], af, b + 2);
         }
@@ -979,7 +1026,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         float f[2][2], dot[2][2];
         {
           float x[2][NT][4] = {};
-          gemm32<NT, 0, KV, RV, false, RK>(x, O, m0, S, n0, ln);
+          gemm32<NT, 0, KV, RV, false, RS>(x, O, m0, S, n0, ln);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -1080,7 +1127,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         float f[2][2], dot[2][2];
         {
           float x[2][NT][4] = {};
-          gemm32<NT, 0, KV, RC, true, RK>(x, V, m0, D, n0, ln);
+          gemm32<NT, 0, KV, RC, true, RS>(x, V, m0, D, n0, ln);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -1108,7 +1155,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
           }
         {
           float x[2][NT][4] = {};
-          gemm32<NT, 0, KV, RC, true, RK>(x, Dx, m0, S, n0, ln);
+          gemm32<NT, 0, KV, RC, true, RS>(x, Dx, m0, S, n0, ln);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -1310,7 +1357,7 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = set_smem(states_half_kernel<DK, DV>, StateSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
-  states_half_kernel<DK, DV><<<dim3(2, a.nv, a.num_seqs), StateSmem<DK, DV>::kThreads, StateSmem<DK, DV>::kBytes, stream>>>(a);
+  states_half_kernel<DK, DV><<<dim3(2, a.nv, a.num_seqs), kStateThreads, StateSmem<DK, DV>::kBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.total_tokens == 0) return e;
   if ((e = set_smem(grads_half_kernel<DK, DV>, GradSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
   const int64_t items = (int64_t)slots * a.nqk;
@@ -1325,12 +1372,12 @@ int64_t chunk_bwd_half_workspace(int64_t total_tokens, int num_seqs, int nqk, in
   if (total_tokens == 0) return 0;
   const int64_t c = bwdh::C, slots = total_tokens / c + num_seqs;
   const int64_t rec = 2 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (3 * c + 8 + 2 * dv);
-  return slots * (nv * rec + nqk * (8 * c * dk + 16 * c) + (int64_t)sizeof(bwdh::SlotInfo));
+  return slots * (nv * rec + nqk * (4 * c * dk + 16 * c) + (int64_t)sizeof(bwdh::SlotInfo));
 }
 
 cudaError_t launch_chunk_bwd_half(const BwdArgs& a, int dk, int dv, cudaStream_t s) {
   static_assert(bwdh::Rec<128, 64>::kBytes == 2 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (3 * 64 + 8 + 2 * 64), "workspace size");
-  static_assert(bwdh::QkRec<128>::kBytes == 8 * 64 * 128 + 16 * 64, "workspace size");
+  static_assert(bwdh::QkRec<128>::kBytes == 4 * 64 * 128 + 16 * 64, "workspace size");
   if (dk == 64 && dv == 64) return bwdh::launch_one<64, 64>(a, s);
   if (dk == 64 && dv == 128) return bwdh::launch_one<64, 128>(a, s);
   if (dk == 128 && dv == 64) return bwdh::launch_one<128, 64>(a, s);
