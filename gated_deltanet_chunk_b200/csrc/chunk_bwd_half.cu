@@ -473,12 +473,15 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
 // ------------------------------------------------------------------ 2. states
 // One block of 8 warps per (sequence, v-head, direction).  S^T (or dS^T) stays in registers in fp32, a row (a column of
 // Dv) in two threads of warps w and w + 4, whose TMEM lanes it shares; a chunk is two products on the tensor cores with
-// M = 128, N = 64 (Dv = 64 leaves half of the lanes unread):
+// M = 128 (Dv = 64 leaves half of the lanes unread):
 //   x^T = S^T W^T          then  S^T = e_last S^T + (V'^T diag(kw)) K                    forwards
 //   x^T = dS'^T K^T        then  dS^T = e_last dS'^T + (diag(qe) dO)^T Q - dV'^T W       backwards
 // Their A operands are what the gradients read as well (but for kw and qe), so they are written once to shared memory
 // and leave by bulk copies.  The tiles of a chunk come in two chunks ahead.  All columns of Dk are in the order of
 // swap32, which no product sees.  The state's image has one factor, joined over the block; V' and dV' keep one a row.
+// A chunk waits for the one before it, and a thread issues an MMA every 90 to 130 cycles: so N is all of Dk, x is
+// two sums over half of Dk from two warps, and z = (diag(qe) dO)^T Q comes from a third (1.15 ms for 2 x 32768 tokens
+// and 32 heads of 128; 1.54 with one warp and N = 64, 1.51 with a ninth warp for all of them; 2.11 with warp MMAs).
 
 constexpr int kStateThreads = 256;
 
@@ -490,8 +493,8 @@ struct StateSmem {  // from a 1024-byte boundary: tiles of the 128-byte swizzle
   static constexpr uint32_t kS = 2 * kStage;            // S^T, panels of 128 rows
   static constexpr uint32_t kV = kS + 2 * 128 * DK;     // V'^T [128][C]
   static constexpr uint32_t kTop = kV + 2 * 128 * C;    // fp32 [2][8] the warps' largest; [2][128] of the halves of a row of V'
-  static constexpr uint32_t kBar = kTop + 64 + 1024;    // four barriers
-  static constexpr uint32_t kTmem = kBar + 32;
+  static constexpr uint32_t kBar = kTop + 64 + 1024;    // five barriers
+  static constexpr uint32_t kTmem = kBar + 48;
   static constexpr uint32_t kBytes = kTmem + 16 + 1024;
   static constexpr uint32_t kKw = oO;                   // forwards: V'^T diag(kw) [128][C] where the first stage has no Oq
   static_assert(kBytes <= 232448, "shared memory budget");
@@ -510,15 +513,15 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
   constexpr int NS = DK / 2;                                     // columns of Dk of a thread
-  constexpr uint32_t kCols = kBackward && DK == 128 ? 512 : 256; // TMEM: x [64], y [DK], z [DK]
-  constexpr uint32_t tY = 64, tZ = 64 + DK;
+  constexpr uint32_t kCols = kBackward && DK == 128 ? 512 : 256; // TMEM: x [2][64], y [DK], z [DK]
+  constexpr uint32_t tY = 128, tZ = 128 + DK;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
   const int c = 32 * (warp & 3) + lane;                          // this thread's column of Dv
   const bool active = 32 * (warp & 3) < DV;
   const int hq = h / (a.nv / a.nqk);
   const uint32_t base = ptx::smem_u32(sm);
   float *tops = reinterpret_cast<float*>(sm + L::kTop), *rtops = tops + 16;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);     // a stage's copies (two), x, y and z
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);     // a stage's copies (two), x, y, z
   int64_t start, end;
   seq_bounds(a, n, start, end);
   const int64_t chunks = (end - start + C - 1) / C, slot0 = start / C + n;
@@ -559,7 +562,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     return __syncthreads_or(!ok);
   };
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) ptx::mbar_init(bar + i, 1);
+    for (int i = 0; i < 5; ++i) ptx::mbar_init(bar + i, i == 2 ? 2 : 1);
     ptx::fence_mbar_init();
   }
   ptx::tc_fence_before();
@@ -597,22 +600,23 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0 || tid == 128) {
       ptx::tc_fence_after();
       const uint32_t b = kBackward ? K : W;
 #pragma unroll
-      for (int k = 0; k < DK / 16; ++k)
-        ptx::mma_bf16(tmem, ptx::sdesc_sw128(S + (k >> 2) * (128 * 128) + 32 * (k & 3), 16, 1024),
-                      ptx::sdesc_sw128(b + (k >> 2) * (128 * C) + 32 * (k & 3), 16, 1024), ptx::idesc_f16_f32(128, 64, false, false), k > 0);
-      ptx::mma_commit(bar + 2);
-      if (kBackward) {
-#pragma unroll
-        for (int m = 0; m < DK / 64; ++m)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_bf16(tmem + tZ + 64 * m, ptx::sdesc_sw128(Oq + 2048 * k, 128 * C, 1024),
-                          ptx::sdesc_sw128(Q + m * (128 * C) + 2048 * k, 128 * C, 1024), ptx::idesc_f16_f32(128, 64, true, true), k > 0);
+      for (int j = 0; j < DK / 32; ++j) {
+        const int k = DK / 32 * half + j;  // step of 16 columns of Dk
+        ptx::mma_bf16(tmem + 64 * half, ptx::sdesc_sw128(S + (k >> 2) * (128 * 128) + 32 * (k & 3), 16, 1024),
+                      ptx::sdesc_sw128(b + (k >> 2) * (128 * C) + 32 * (k & 3), 16, 1024), ptx::idesc_f16_f32(128, 64, false, false), j > 0);
       }
+      ptx::mma_commit(bar + 2);
+    } else if (kBackward && tid == 64) {
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        ptx::mma_bf16(tmem + tZ, ptx::sdesc_sw128(Oq + 2048 * k, 128 * C, 1024), ptx::sdesc_sw128(Q + 2048 * k, 128 * C, 1024),
+                      ptx::idesc_f16_f32(128, DK, true, true), k > 0);
+      ptx::mma_commit(bar + 4);
     } else if (tid == 32) {
 #pragma unroll
       for (int m = 0; m < DK / 64; ++m) bulk_store(rec + (kBackward ? R::kD : R::kS) + m * (128 * DV), S + m * (128 * 128), 128 * DV);
@@ -621,29 +625,29 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     }
     const float us = scal[kBackward ? kScalY : kScalU], os = scal[kScalO], gl = scal[kScalGl];
     // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw)
-    float x[32], vfac = 0.f, vinv = 0.f;
+    float x[32], w[32], vfac = 0.f, vinv = 0.f;
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>(kw + 32 * half + j);
+    if (active) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = *reinterpret_cast<const uint4*>(st + L::oU + row + (((uint32_t)(4 * half + t) ^ sw) << 4));
+    }
     ok = ptx::mbar_wait_bounded(bar + 2, (uint32_t)(i & 1), kWaitLimitNs) && ok;
     ptx::tc_fence_after();
     if (active) {
+      float y[32];
       ptx::tmem_ld32(tl + 32 * half, x);
-      uint4 u[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) u[t] = *reinterpret_cast<const uint4*>(st + L::oU + row + (((uint32_t)(4 * half + t) ^ sw) << 4));
+      ptx::tmem_ld32(tl + 64 + 32 * half, y);
       ptx::tmem_ld_wait();
       float rtop = 0.f;
+      const float fx = kBackward ? sinv : -0x1p-7f * sinv;
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {  // columns j, j + 1 of this half stand in vector (j / 2) % 4, word j / 8
+      for (int j = 0; j < 32; ++j) {  // columns j, j ^ 1 of this half stand in vector (j / 2) % 4, word j / 8
         const uint4& v = u[(j >> 1) & 3];
-        const float2 y = unpack2(j < 8 ? v.x : j < 16 ? v.y : j < 24 ? v.z : v.w);
-        float2 f = make_float2(-0x1p-7f * sinv, -0x1p-7f * sinv);
-        if (kBackward) {
-          f = *reinterpret_cast<const float2*>(kw + 32 * half + j);
-          f.x *= sinv;
-          f.y *= sinv;
-        }
-        x[j] = fmaf(x[j], f.x, us * y.x);
-        x[j + 1] = fmaf(x[j + 1], f.y, us * y.y);
-        rtop = fmaxf(rtop, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
+        const float2 u2 = unpack2(j < 8 ? v.x : j < 16 ? v.y : j < 24 ? v.z : v.w);
+        x[j] = fmaf(x[j] + y[j], kBackward ? fx * w[j] : fx, us * (j & 1 ? u2.y : u2.x));
+        rtop = fmaxf(rtop, fabsf(x[j]));
       }
       rtops[128 * half + c] = rtop;
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // warps w and w + 4
@@ -655,11 +659,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
         *reinterpret_cast<uint4*>(sm + L::kV + at) = pack8(x + 8 * t, vfac);
         if (!kBackward) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 w = *reinterpret_cast<const float2*>(kw + 32 * half + 8 * t + e);
-            x[8 * t + e] *= w.x * 0x1p7f;  // kw 2^7 is at most 1
-            x[8 * t + e + 1] *= w.y * 0x1p7f;
-          }
+          for (int e = 0; e < 8; ++e) x[8 * t + e] *= w[8 * t + e] * 0x1p7f;  // kw 2^7 is at most 1
           *reinterpret_cast<uint4*>(sm + L::kKw + at) = pack8(x + 8 * t, vfac);
         }
       }
@@ -671,15 +671,30 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       ptx::tc_fence_after();
       const uint32_t A = kBackward ? V : base + L::kKw, b = kBackward ? W : K;
 #pragma unroll
-      for (int m = 0; m < DK / 64; ++m)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          ptx::mma_bf16(tmem + tY + 64 * m, ptx::sdesc_sw128(A + 32 * k, 16, 1024),
-                        ptx::sdesc_sw128(b + m * (128 * C) + 2048 * k, 128 * C, 1024), ptx::idesc_f16_f32(128, 64, false, true), k > 0);
+      for (int k = 0; k < 4; ++k)
+        ptx::mma_bf16(tmem + tY, ptx::sdesc_sw128(A + 32 * k, 16, 1024), ptx::sdesc_sw128(b + 2048 * k, 128 * C, 1024),
+                      ptx::idesc_f16_f32(128, DK, false, true), k > 0);
       ptx::mma_commit(bar + 3);
     } else if (tid == 32) {
       bulk_store(rec + (kBackward ? R::kX : R::kV), V, L::kRows);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    // what does not need y, meanwhile
+    if constexpr (kBackward) {
+      ok = ptx::mbar_wait_bounded(bar + 4, (uint32_t)(i & 1), kWaitLimitNs) && ok;
+      ptx::tc_fence_after();
+      if (active) {
+#pragma unroll
+        for (int m = 0; m < NS; m += 32) {
+          ptx::tmem_ld32(tl + tZ + NS * half + m, x);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[m + j] = fmaf(os, x[j], gl * s[m + j]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) s[j] *= gl;
     }
     const float fy = vinv * (kBackward ? -0x1p-7f : 0x1p-7f);
     ok = ptx::mbar_wait_bounded(bar + 3, (uint32_t)(i & 1), kWaitLimitNs) && ok;
@@ -687,16 +702,10 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     if (active) {
 #pragma unroll
       for (int m = 0; m < NS; m += 32) {
-        float z[kBackward ? 32 : 1];
         ptx::tmem_ld32(tl + tY + NS * half + m, x);
-        if constexpr (kBackward) ptx::tmem_ld32(tl + tZ + NS * half + m, z);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float v = gl * s[m + j];
-          if constexpr (kBackward) v = fmaf(os, z[j], v);
-          s[m + j] = fmaf(fy, x[j], v);
-        }
+        for (int j = 0; j < 32; ++j) s[m + j] = fmaf(fy, x[j], s[m + j]);
       }
     }
     ptx::tc_fence_before();
@@ -709,6 +718,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
         if (i + 1 < chunks) ptx::mbar_wait_bounded(bar + ((i + 1) & 1), (uint32_t)(((i + 1) >> 1) & 1), kWaitLimitNs);
         ptx::mbar_wait_bounded(bar + 2, (uint32_t)(i & 1), kWaitLimitNs);
         ptx::mbar_wait_bounded(bar + 3, (uint32_t)(i & 1), kWaitLimitNs);
+        if (kBackward) ptx::mbar_wait_bounded(bar + 4, (uint32_t)(i & 1), kWaitLimitNs);
       }
       break;
     }
