@@ -584,16 +584,19 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
 }
 
 // ------------------------------------------------------------------ 2. states
-// One block per (sequence, v-head, direction, 64 columns of Dv), one warp per 16 columns.
+// One block per (sequence, v-head, direction, 64 columns of Dv).  Two warps, w and w + 4, share 16 columns of Dv, and
+// each keeps half of the columns of Dk: x is the sum of what both have, and each forms V' for itself.
 
-constexpr int kStateWarps = 4;
-constexpr int kStateThreads = 32 * kStateWarps;
+constexpr int kStateSlices = 4;
+constexpr int kStateThreads = 64 * kStateSlices;
 
 template <int DK>
 struct StateSmem {
   static constexpr size_t kTile = 4 * C * DK;            // a pair image: W, K16 and (backwards) Q16
   static constexpr size_t kStage = 3 * kTile + 4 * C;    // and kw
-  static constexpr size_t kBar = 2 * kStage;
+  static constexpr size_t kX = 2 * kStage;               // float4 [8 warps][8][32] a warp's part of x
+  static constexpr size_t kTop = kX + 8 * 4096;          // fp32 [8 warps][16] largest of its rows of the state
+  static constexpr size_t kBar = kTop + 512;
   static constexpr size_t kBytes = kBar + 16;
   static_assert(kStage % 128 == 0 && kBytes <= 232448, "shared memory budget");
 };
@@ -614,12 +617,12 @@ __device__ __forceinline__ void row_factors(float (&top)[2], float (&f)[2], floa
     pow2_factor(top[e], f[e], inv[e]);
   }
 }
-// x[8] (64 columns from n0) += (hi + lo) B[16 k .. + 15], B a pair image [n][k] (kT: [k][n])
-template <int RB, bool kT>
-__device__ __forceinline__ void mma_pairs(float (&x)[8][4], const uint32_t* hi, const uint32_t* lo, uint32_t img, int n0, int k,
+// x[NT] (8 NT columns from n0) += (hi + lo) B[16 k .. + 15], B a pair image [n][k] (kT: [k][n])
+template <int RB, bool kT, int NT>
+__device__ __forceinline__ void mma_pairs(float (&x)[NT][4], const uint32_t* hi, const uint32_t* lo, uint32_t img, int n0, int k,
                                           const Lane& ln) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < NT / 2; ++j) {
     uint32_t bh[4], bl[4];
     if (kT) pair_b_t<RB>(bh, bl, img, n0 + 16 * j, 16 * k, ln); else pair_b<RB>(bh, bl, img, n0 + 16 * j, 16 * k, ln);
     mma_pair(x[2 * j], hi, lo, bh, bl);
@@ -632,24 +635,28 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
   using L = StateSmem<DK>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
-  constexpr int ND = DK / 8, RB = 2 * DK, RC = 2 * C;
+  constexpr int ND = DK / 16, RB = 2 * DK, RC = 2 * C;  // ND: 8-column tiles of a warp's half of Dk
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int slice = col0 / 16 + warp, c = 16 * slice + g;  // this thread's columns of Dv: c and c + 8
+  const int half = warp >> 2, d0 = DK / 2 * half;
+  const int slice = col0 / 16 + (warp & 3), c = 16 * slice + g;  // this thread's columns of Dv: c and c + 8
   const int hq = h / (a.nv / a.nqk);
   Lane ln(lane);
+  float4* xs = reinterpret_cast<float4*>(sm + L::kX);
+  float* tops = reinterpret_cast<float*>(sm + L::kTop);
+  auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };  // warps w and w + 4
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);
   int64_t start, end;
   seq_bounds(a, n, start, end);
   const int64_t chunks = (end - start + C - 1) / C, slot0 = start / C + n;
 
-  float s[ND][4];  // S^T or dS^T: rows c, c + 8, columns d = 8 j + 2 t, + 1
+  float s[ND][4];  // S^T or dS^T: rows c, c + 8, columns d = d0 + 8 j + 2 t, + 1
   const float* init = kBackward ? a.ds_final : a.s0;
   const size_t state_off = ((size_t)n * a.nv + h) * (size_t)DK * DV;
 #pragma unroll
   for (int j = 0; j < ND; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      s[j][e] = init ? init[state_off + (size_t)(8 * j + 2 * t + (e & 1)) * DV + c + 8 * (e >> 1)] : 0.f;
+      s[j][e] = init ? init[state_off + (size_t)(d0 + 8 * j + 2 * t + (e & 1)) * DV + c + 8 * (e >> 1)] : 0.f;
 
   auto slot_of = [&](int64_t i) { return slot0 + (kBackward ? chunks - 1 - i : i); };
   auto fetch = [&](int64_t i) {  // by one thread
@@ -683,8 +690,16 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       top[0] = fmaxf(top[0], fmaxf(fabsf(s[j][0]), fabsf(s[j][1])));
       top[1] = fmaxf(top[1], fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
     }
-    row_factors(top, sf, sinv);
-    if (t == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+      if (t == 0) tops[16 * warp + 8 * e + g] = top[e];
+    }
+    pair_sync();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) pow2_factor(fmaxf(top[e], tops[16 * (warp ^ 4) + 8 * e + g]), sf[e], sinv[e]);
+    if (t == 0 && half == 0) {
       rf[(kBackward ? R::fD : R::fS) + c] = sinv[0];
       rf[(kBackward ? R::fD : R::fS) + c + 8] = sinv[1];
     }
@@ -692,6 +707,10 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     const uint8_t* st = sm + (i & 1) * L::kStage;
     const uint32_t W = ptx::smem_u32(st), K = W + (uint32_t)L::kTile, Q = K + (uint32_t)L::kTile;
     const float* kw = reinterpret_cast<const float*>(st + 3 * L::kTile);
+    const float4* uw = reinterpret_cast<const float4*>(rec + (kBackward ? R::kX : R::kV)) + slice * 256 + lane;
+    float4 u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = uw[32 * j];
     // x = S^T W^T (forwards) or dS'^T K^T (backwards), [16 x C]; the operand is also what the gradients read: two
     // steps of 16 columns are one vector a lane
     float x[8][4] = {};
@@ -702,21 +721,27 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         pair_frag(s[4 * k2 + 2 * m], s[4 * k2 + 2 * m + 1], sf[0], sf[1], hi[m], lo[m]);
-        mma_pairs<RB, false>(x, hi[m], lo[m], kBackward ? K : W, 0, 2 * k2 + m, ln);
+        mma_pairs<RB, false, 8>(x, hi[m], lo[m], kBackward ? K : W, 0, d0 / 16 + 2 * k2 + m, ln);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        uint8_t* dst = img + pair_at<RB>(c + 8 * e, 32 * k2 + 8 * t);
+        uint8_t* dst = img + pair_at<RB>(c + 8 * e, d0 + 32 * k2 + 8 * t);
         *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0][e], hi[0][2 + e], hi[1][e], hi[1][2 + e]);
         *reinterpret_cast<uint4*>(dst + 16 * RB) = make_uint4(lo[0][e], lo[0][2 + e], lo[1][e], lo[1][2 + e]);
       }
     }
-    // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw); stored over U^T, Y^T (this warp's 4 KB)
-    const float4* uw = reinterpret_cast<const float4*>(rec + (kBackward ? R::kX : R::kV)) + slice * 256 + lane;
-    float4 u[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = uw[32 * j];
-    __syncwarp();
+    for (int j = 0; j < 8; ++j) xs[256 * warp + 32 * j + lane] = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+    pair_sync();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 y = xs[256 * (warp ^ 4) + 32 * j + lane];
+      x[j][0] += y.x;
+      x[j][1] += y.y;
+      x[j][2] += y.z;
+      x[j][3] += y.w;
+    }
+    // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw); stored over U^T, Y^T (these warps' 4 KB, read by both)
     top[0] = top[1] = 0.f;
     float vf[2], vinv[2];
 #pragma unroll
@@ -731,7 +756,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       top[1] = fmaxf(top[1], fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
     }
     row_factors(top, vf, vinv);
-    if (t == 0) {
+    if (t == 0 && half == 0) {
       rf[(kBackward ? R::fDV : R::fV) + c] = vinv[0];
       rf[(kBackward ? R::fDV : R::fV) + c + 8] = vinv[1];
     }
@@ -740,6 +765,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       pair_frag(x[2 * k], x[2 * k + 1], vf[0], vf[1], vh[k], vl[k]);
+      if ((k >> 1) != half) continue;  // each warp stores half of the columns
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         uint8_t* dst = img + pair_at<RC>(c + 8 * (e & 1), 16 * k + 8 * (e >> 1) + 2 * t);
@@ -765,15 +791,14 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     }
     // forwards S^T = e_last S^T + (V' diag(kw))^T K, backwards dS^T = e_last dS'^T + (s diag(e) dO)^T Q - dV'^T W
     const float f0 = kBackward ? -vinv[0] * winv : vinv[0], f1 = kBackward ? -vinv[1] * winv : vinv[1];
+    {
+      float y[ND][4] = {};
 #pragma unroll
-    for (int m = 0; m < ND; m += 8) {  // 64 columns of Dk at a time
-      float y[8][4] = {};
+      for (int k = 0; k < 4; ++k) mma_pairs<RB, true, ND>(y, vh[k], vl[k], kBackward ? W : K, d0, k, ln);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mma_pairs<RB, true>(y, vh[k], vl[k], kBackward ? W : K, 8 * m, k, ln);
+      for (int j = 0; j < ND; ++j)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[m + j][e] = fmaf(e < 2 ? f0 : f1, y[j][e], gl * s[m + j][e]);
+        for (int e = 0; e < 4; ++e) s[j][e] = fmaf(e < 2 ? f0 : f1, y[j][e], gl * s[j][e]);
     }
     if (kBackward) {
       const uint4* ow = reinterpret_cast<const uint4*>(rec + R::kOq) + slice * 128 + lane;
@@ -784,16 +809,13 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
         vh[k][0] = h4.x; vh[k][1] = h4.y; vh[k][2] = h4.z; vh[k][3] = h4.w;
         vl[k][0] = l4.x; vl[k][1] = l4.y; vl[k][2] = l4.z; vl[k][3] = l4.w;
       }
+      float y[ND][4] = {};
 #pragma unroll
-      for (int m = 0; m < ND; m += 8) {
-        float y[8][4] = {};
+      for (int k = 0; k < 4; ++k) mma_pairs<RB, true, ND>(y, vh[k], vl[k], Q, d0, k, ln);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_pairs<RB, true>(y, vh[k], vl[k], Q, 8 * m, k, ln);
+      for (int j = 0; j < ND; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[m + j][e] = fmaf(e < 2 ? o0 : o1, y[j][e], s[m + j][e]);
-      }
+        for (int e = 0; e < 4; ++e) s[j][e] = fmaf(e < 2 ? o0 : o1, y[j][e], s[j][e]);
     }
     if (__syncthreads_or(!ok)) {  // a copy never came: report it, wait once more for what is in flight, and leave
       if (tid == 0) {
@@ -810,7 +832,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     for (int j = 0; j < ND; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        a.ds0[state_off + (size_t)(8 * j + 2 * t + (e & 1)) * DV + c + 8 * (e >> 1)] = s[j][e];
+        a.ds0[state_off + (size_t)(d0 + 8 * j + 2 * t + (e & 1)) * DV + c + 8 * (e >> 1)] = s[j][e];
   }
 }
 
@@ -818,7 +840,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 template <int DK, int DV>
 __global__ void __launch_bounds__(kStateThreads) states_kernel(BwdArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
-  const int col0 = 16 * kStateWarps * (blockIdx.x >> 1);
+  const int col0 = 16 * kStateSlices * (blockIdx.x >> 1);
   if (blockIdx.x & 1)
     walk<DK, DV, true>(a, sm, blockIdx.z, blockIdx.y, col0);
   else
@@ -1383,7 +1405,7 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = set_smem(states_kernel<DK, DV>, StateSmem<DK>::kBytes)) != cudaSuccess) return e;
-  states_kernel<DK, DV><<<dim3(2 * DV / (16 * kStateWarps), a.nv, a.num_seqs), kStateThreads, StateSmem<DK>::kBytes, stream>>>(a);
+  states_kernel<DK, DV><<<dim3(2 * DV / (16 * kStateSlices), a.nv, a.num_seqs), kStateThreads, StateSmem<DK>::kBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.total_tokens == 0) return e;
   if ((e = set_smem(grads_kernel<DK, DV, IO>, GradSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
   grads_kernel<DK, DV, IO><<<dim3(slots, a.nqk), kThreads, GradSmem<DK, DV>::kBytes, stream>>>(a);
