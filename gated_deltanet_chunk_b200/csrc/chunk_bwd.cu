@@ -630,6 +630,8 @@ __device__ __forceinline__ void mma_pairs(float (&x)[NT][4], const uint32_t* hi,
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <int DK, int DV, bool kBackward>
 __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h, int col0) {
   using L = StateSmem<DK>;
@@ -683,6 +685,16 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
     float* rf = reinterpret_cast<float*>(rec + R::kF);
     const float gl = rf[R::fScal + kScalGl], winv = rf[R::fScal + kScalW];
+    const float4* uw = reinterpret_cast<const float4*>(rec + (kBackward ? R::kX : R::kV)) + slice * 256 + lane;
+    float4 u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = uw[32 * j];
+    if (i + 1 < chunks) {  // the next chunk's U^T, or Y^T and half of Oq each, a line a lane
+      const uint8_t* nx = rec_at<DK, DV>(a, slot_of(i + 1), h);
+      if (half == 0) prefetch_l2(nx + (kBackward ? R::kX : R::kV) + 4096 * slice + 128 * lane);
+      if (half == 1 && lane < 8) prefetch_l2(nx + R::kF + min((size_t)(128 * lane), (size_t)(4 * R::kFloats - 4)));
+      if (kBackward && half == 1) prefetch_l2(nx + R::kOq + (lane >> 4) * (2 * C * DV) + 2048 * slice + 128 * (lane & 15));
+    }
     // the state as this chunk meets it
     float top[2] = {0.f, 0.f}, sf[2], sinv[2];
 #pragma unroll
@@ -707,10 +719,6 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     const uint8_t* st = sm + (i & 1) * L::kStage;
     const uint32_t W = ptx::smem_u32(st), K = W + (uint32_t)L::kTile, Q = K + (uint32_t)L::kTile;
     const float* kw = reinterpret_cast<const float*>(st + 3 * L::kTile);
-    const float4* uw = reinterpret_cast<const float4*>(rec + (kBackward ? R::kX : R::kV)) + slice * 256 + lane;
-    float4 u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = uw[32 * j];
     // x = S^T W^T (forwards) or dS'^T K^T (backwards), [16 x C]; the operand is also what the gradients read: two
     // steps of 16 columns are one vector a lane
     float x[8][4] = {};
@@ -850,9 +858,10 @@ __global__ void __launch_bounds__(kStateThreads) states_kernel(BwdArgs a) {
 // ------------------------------------------------------------------ 3. gradients
 // One block of 16 warps per (slot, qk-head), which takes its v-heads in turn, and of each 64 columns of Dv at a time:
 //   1. all warps: dX^T = dV'^T T; S^T, dS'^T and V'^T to one factor for all their rows
-//   2. warps 0-7: dO S^T, then dA and dP; warps 8-15: V' dS'^T, then dX S^T and dV; all: <S, dS'>
+//   2. warps 0-7: dO S^T; warps 8-15: V' dS'^T, then dX S^T and dV; warps 0-9: dA and dP, a 16 x 16 block of the
+//      triangle each; all: <S, dS'>
 // and after a v-head's last columns
-//   3. warps 0-7: N and B
+//   3. warps 0-9: N and B
 //   4. warps 0-7: N K, and keep dq; warps 8-15: N^T Q + (B + B^T) K, and keep dk
 
 template <int DK, int DV>
@@ -871,10 +880,10 @@ struct GradSmem {
   static constexpr size_t kF = kT + kHalf;                    // the record's floats up to fKw
   static constexpr size_t kFBytes = 4 * R::fKw;
   static constexpr size_t kRed = kF + kFBytes;                // fp32 [3][4][C] rows' dots by column block
-  static constexpr size_t kRedA = kRed + 48 * C;              // fp32 [6][C] row sums: through A and P (two halves: dgc, dbeta), dX V (two)
-  static constexpr size_t kCol = kRedA + 24 * C;              // fp32 [4][C] column sums by row block
-  static constexpr size_t kDot = kCol + 16 * C;               // fp32 [16] <S, dS'> by warp; [2][8] largest of N and B
-  static constexpr size_t kBar = kDot + 128;
+  static constexpr size_t kRedA = kRed + 48 * C;              // fp32 [10][C] row sums: through A and P by column block (dgc, dbeta), dX V (two)
+  static constexpr size_t kCol = kRedA + 40 * C;              // fp32 [4][C] column sums by row block
+  static constexpr size_t kDot = kCol + 16 * C;               // fp32 [16] <S, dS'> by warp; [2][16] largest of N and B
+  static constexpr size_t kBar = kDot + 192;
   static constexpr size_t kBytes = kBar + 16;
   static_assert(kS % 128 == 0 && kF % 16 == 0 && kFBytes % 16 == 0, "images and bulk copies");
   static_assert(kBytes <= 232448, "shared memory budget");
@@ -883,7 +892,7 @@ struct GradSmem {
 // x[2][NT] (32 rows from m0, 8 NT columns from n0) += A B over k in [16 K0, 16 K1); pair images A [m][k] (kAT: [k][m]), B [k][n]
 template <int NT, int K0, int K1, int RA, bool kAT, int RB>
 __device__ __forceinline__ void gemm32(float (&x)[2][NT][4], uint32_t A, int m0, uint32_t B, int n0, const Lane& l) {
-#pragma unroll 2
+#pragma unroll 1
   for (int k = K0; k < K1; ++k) {
     uint32_t ah[2][4], al[2][4];
 #pragma unroll
@@ -986,12 +995,15 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
   }
   // a warp's 32 rows and quarter of the columns of Dk for products with the state
   const int m0 = 32 * (w8 & 1), n0 = (DK / 4) * (w8 >> 1);
-  const bool above = w8 == 4 || w8 == 5;  // rows 0..31 and columns 32..63 of [C][C]: all above the diagonal, and never read
-  if (first && above) {
-    col[(w8 & 3) * C + 32 + lane] = 0.f;
-    if (lane < 16) reda[2 * C + 16 * (w8 & 3) + lane] = reda[3 * C + 16 * (w8 & 3) + lane] = 0.f;
+  // of [C][C], warps 0-9 have block (rb, cb) of the triangle; what they leave of the sums is zero
+  const bool tri = warp < 10;
+  const int rb = warp < 1 ? 0 : warp < 3 ? 1 : warp < 6 ? 2 : 3, cb = warp - rb * (rb + 1) / 2;
+  for (int i = tid; i < 4 * C; i += kThreads) {
+    const int q = i / C, r = i % C;      // column block or row block q, row or column r
+    if (r / 16 < q) reda[i] = reda[4 * C + i] = 0.f;
+    if (r / 16 > q) col[i] = 0.f;
   }
-  float dA[4][4], dP[4][4];              // warps 0-7: rows 16 (w8 & 3) .., columns 32 (w8 >> 2) .. of [C][C]
+  float dA[2][4], dP[2][4];
   float sum[2][NT][4] = {};              // qf dq_hat (warps 0-7) or kf dk_hat (warps 8-15), over the group's v-heads
   bool quit = false;
   uint32_t it = 0;
@@ -1095,30 +1107,6 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) put_row(f[m][e] * dot[m][e], red + (w8 >> 1) * C + m0 + 16 * m + 8 * e + ln.g, ln.t, head);
-        if (!above) {
-          const int wr = 16 * (w8 & 3), wc = 32 * (w8 >> 2);
-          if (head) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) dA[j][e] = dP[j][e] = 0.f;
-          }
-#pragma unroll 2
-          for (int k = 0; k < 4; ++k) {
-            uint32_t xh[4], xl[4], oh[4], ol[4];
-            pair_a_t<RC>(xh, xl, Dx, wr, 16 * k, ln);
-            pair_a<RC>(oh, ol, O, wr, 16 * k, ln);
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              uint32_t bh[4], bl[4];
-              pair_b_t<RC>(bh, bl, V, wc + 8 * j, 16 * k, ln);
-              mma_pair(dA[j], xh, xl, bh, bl);
-              mma_pair(dA[j + 1], xh, xl, bh + 2, bl + 2);
-              mma_pair(dP[j], oh, ol, bh, bl);
-              mma_pair(dP[j + 1], oh, ol, bh + 2, bl + 2);
-            }
-          }
-        }
       } else {
         float f[2][2], dot[2][2];
         {
@@ -1184,85 +1172,106 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
           }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) put_row(s_v[e], reda + (4 + (w8 >> 2)) * C + r0 + 8 * e, ln.t, head);
+        for (int e = 0; e < 2; ++e) put_row(s_v[e], reda + (8 + (w8 >> 2)) * C + r0 + 8 * e, ln.t, head);
+      }
+      if (tri) {
+        ln.again();
+        if (head) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dA[j][e] = dP[j][e] = 0.f;
+        }
+#pragma unroll 2
+        for (int k = 0; k < 4; ++k) {
+          uint32_t xh[4], xl[4], oh[4], ol[4], bh[4], bl[4];
+          pair_a_t<RC>(xh, xl, Dx, 16 * rb, 16 * k, ln);
+          pair_a<RC>(oh, ol, O, 16 * rb, 16 * k, ln);
+          pair_b_t<RC>(bh, bl, V, 16 * cb, 16 * k, ln);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            mma_pair(dA[j], xh, xl, bh + 2 * j, bl + 2 * j);
+            mma_pair(dP[j], oh, ol, bh + 2 * j, bl + 2 * j);
+          }
+        }
       }
       if (v0 + 64 < DV) continue;
       // ---- 3. what goes through A and P
       s_dot = warp_sum(s_dot);
       if (lane == 0) dots[warp] = s_dot * mS * mD;
       const float sP = oinv * mV, sA = mX * mV;
-      if (first) {
+      if (tri) {
         ln.again();
-        const int r0 = 16 * (w8 & 3) + ln.g, i0 = 32 * (w8 >> 2) + 2 * ln.t;
+        const int r0 = 16 * rb + ln.g, i0 = 16 * cb + 2 * ln.t;
         const float* bt = rf + R::fBeta;
         float s_gc[2] = {0.f, 0.f}, s_bt[2] = {0.f, 0.f}, top[2] = {0.f, 0.f};
-        if (!above) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int at = ((w8 & 3) * 8 + 4 * (w8 >> 2) + j) * 32 + lane;
-            const float4 kk4 = reinterpret_cast<const float4*>(qrec + QR::kKk)[at], qk4 = reinterpret_cast<const float4*>(qrec + QR::kQk)[at];
-            const float kk[4] = {kk4.x, kk4.y, kk4.z, kk4.w}, qk[4] = {qk4.x, qk4.y, qk4.z, qk4.w};
-            float cs[2] = {0.f, 0.f};
+        for (int j = 0; j < 2; ++j) {
+          const int at = (rb * 8 + 2 * cb + j) * 32 + lane;
+          const float4 kk4 = reinterpret_cast<const float4*>(qrec + QR::kKk)[at], qk4 = reinterpret_cast<const float4*>(qrec + QR::kQk)[at];
+          const float kk[4] = {kk4.x, kk4.y, kk4.z, kk4.w}, qk[4] = {qk4.x, qk4.y, qk4.z, qk4.w};
+          float cs[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = r0 + 8 * (e >> 1), i = i0 + 8 * j + (e & 1);
-              const float gamma = i <= r ? expf(gc[r] - gc[i]) : 0.f, strict = i < r ? gamma : 0.f;  // masked before exp
-              const float da = sA * dA[j][e], dp = a.scale * sP * dP[j][e];
-              const float fk = kf[r] * kf[i], fq = qf[r] * kf[i];
-              const float akd = da * (kk[e] * strict);
-              const float both = fmaf(-bt[r], akd, dp * strict * qk[e]);
-              s_bt[e >> 1] -= akd;
-              s_gc[e >> 1] += both;
-              cs[e & 1] += both;
-              dP[j][e] = dp * gamma * fq;             // N
-              dA[j][e] = -da * bt[r] * strict * fk;   // B
-              top[0] = fmaxf(top[0], fabsf(dP[j][e]));
-              top[1] = fmaxf(top[1], fabsf(dA[j][e]));
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], o);
-              if (ln.g == 0) col[(w8 & 3) * C + i0 + 8 * j + e] = cs[e];
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int r = r0 + 8 * (e >> 1), i = i0 + 8 * j + (e & 1);
+            const float gamma = i <= r ? expf(gc[r] - gc[i]) : 0.f, strict = i < r ? gamma : 0.f;  // masked before exp
+            const float da = sA * dA[j][e], dp = a.scale * sP * dP[j][e];
+            const float fk = kf[r] * kf[i], fq = qf[r] * kf[i];
+            const float akd = da * (kk[e] * strict);
+            const float both = fmaf(-bt[r], akd, dp * strict * qk[e]);
+            s_bt[e >> 1] -= akd;
+            s_gc[e >> 1] += both;
+            cs[e & 1] += both;
+            dP[j][e] = dp * gamma * fq;             // N
+            dA[j][e] = -da * bt[r] * strict * fk;   // B
+            top[0] = fmaxf(top[0], fabsf(dP[j][e]));
+            top[1] = fmaxf(top[1], fabsf(dA[j][e]));
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            put_row(s_gc[e], reda + (2 * (w8 >> 2)) * C + r0 + 8 * e, ln.t, true);
-            put_row(s_bt[e], reda + (2 * (w8 >> 2) + 1) * C + r0 + 8 * e, ln.t, true);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], o);
+            if (ln.g == 0) col[rb * C + i0 + 8 * j + e] = cs[e];
           }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          put_row(s_gc[e], reda + cb * C + r0 + 8 * e, ln.t, true);
+          put_row(s_bt[e], reda + (4 + cb) * C + r0 + 8 * e, ln.t, true);
           top[e] = warp_top(top[e]);
-          if (lane == 0) ntop[8 * e + w8] = top[e];
+          if (lane == 0) ntop[16 * e + warp] = top[e];
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");  // of warps 0-7, which alone read dV' and dO: N and B come over them
+        asm volatile("bar.sync 1, 320;" ::: "memory");  // of warps 0-9, which alone read dO: N and B come over dV' and dO
         float f[2], inv[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) pow2_factor(warp_top(ntop[8 * e + (lane & 7)]), f[e], inv[e]);
-        if (!above) {
+        for (int e = 0; e < 2; ++e) pow2_factor(warp_top(lane < 10 ? ntop[16 * e + lane] : 0.f), f[e], inv[e]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t hi, lo;
-              const uint32_t at = (uint32_t)pair_at<RC>(r0 + 8 * e, i0 + 8 * j);
-              pair2(dP[j][2 * e], dP[j][2 * e + 1], f[0], hi, lo);
-              sts32(N + at, hi);
-              sts32(N + at + 16 * RC, lo);
-              pair2(dA[j][2 * e], dA[j][2 * e + 1], f[1], hi, lo);
-              sts32(B + at, hi);
-              sts32(B + at + 16 * RC, lo);
+          for (int e = 0; e < 2; ++e) {
+            uint32_t hi, lo;
+            const uint32_t at = (uint32_t)pair_at<RC>(r0 + 8 * e, i0 + 8 * j);
+            pair2(dP[j][2 * e], dP[j][2 * e + 1], f[0], hi, lo);
+            sts32(N + at, hi);
+            sts32(N + at + 16 * RC, lo);
+            pair2(dA[j][2 * e], dA[j][2 * e + 1], f[1], hi, lo);
+            sts32(B + at, hi);
+            sts32(B + at + 16 * RC, lo);
+            if (cb == rb && (rb & 1) == 0) {  // the block on the right of it is read too, and above the diagonal
+              const uint32_t right = (uint32_t)pair_at<RC>(r0 + 8 * e, i0 + 8 * j + 16);
+              sts32(N + right, 0u);
+              sts32(N + right + 16 * RC, 0u);
+              sts32(B + right, 0u);
+              sts32(B + right + 16 * RC, 0u);
             }
-        }
+          }
       }
       __syncthreads();
       // ---- 4.
       ln.again();
       float sN, sB, unused;
-      pow2_factor(warp_top(ntop[lane & 7]), unused, sN);
-      pow2_factor(warp_top(ntop[8 + (lane & 7)]), unused, sB);
+      pow2_factor(warp_top(lane < 10 ? ntop[lane] : 0.f), unused, sN);
+      pow2_factor(warp_top(lane < 10 ? ntop[16 + lane] : 0.f), unused, sB);
       {
         float x[2][NT][4] = {};
         if (first) {
@@ -1303,16 +1312,15 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
       }
       if (warp == 0) {
         // dgc of rows 2 lane, 2 lane + 1; then the suffix sums
-        auto four = [&](int m, int r) { return (red[(4 * m) * C + r] + red[(4 * m + 1) * C + r]) + (red[(4 * m + 2) * C + r] + red[(4 * m + 3) * C + r]); };
+        auto four = [&](const float* x, int r) { return (x[r] + x[C + r]) + (x[2 * C + r] + x[3 * C + r]); };
         float d[2], th = 0.f, bsum[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = 2 * lane + e;
-          const float through = four(1, r), u = four(2, r);
-          const float cols = (col[r] + col[C + r]) + (col[2 * C + r] + col[3 * C + r]);
+          const float through = four(red + 4 * C, r), u = four(red + 8 * C, r);
           th += through;
-          d[e] = (reda[r] + reda[2 * C + r]) + four(0, r) + rf[R::fBeta + r] * u - through - cols;
-          bsum[e] = (reda[C + r] + reda[3 * C + r]) + (reda[4 * C + r] + reda[5 * C + r]) + u;
+          d[e] = four(reda, r) + four(red, r) + rf[R::fBeta + r] * u - through - four(col, r);
+          bsum[e] = four(reda + 4 * C, r) + (reda[8 * C + r] + reda[9 * C + r]) + u;
         }
         th = warp_sum(th);
         const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f);
