@@ -127,7 +127,7 @@ struct Rec {
   static constexpr int fGc = 0;                        // [C] gcum
   static constexpr int fBeta = fGc + C;                // [C] beta
   static constexpr int fScal = fBeta + C;              // [8] see Scal
-  static constexpr int fS = fScal + 8;                 // [DV] factor of every row of S^T
+  static constexpr int fS = fScal + 8;                 // [DV] factor of every row of S^T (one for 64 rows)
   static constexpr int fD = fS + DV;                   // [DV] of dS'^T
   static constexpr int fV = fD + DV;                   // [DV] of V'^T
   static constexpr int fDV = fV + DV;                  // [DV] of dV'^T
@@ -595,8 +595,8 @@ struct StateSmem {
   static constexpr size_t kTile = 4 * C * DK;            // a pair image: W, K16 and (backwards) Q16
   static constexpr size_t kStage = 3 * kTile + 4 * C;    // and kw
   static constexpr size_t kX = 2 * kStage;               // float4 [8 warps][8][32] a warp's part of x
-  static constexpr size_t kTop = kX + 8 * 4096;          // fp32 [8 warps][16] largest of its rows of the state
-  static constexpr size_t kBar = kTop + 512;
+  static constexpr size_t kTop = kX + 8 * 4096;          // fp32 [2][8] the warps' largest of the state
+  static constexpr size_t kBar = kTop + 64;
   static constexpr size_t kBytes = kBar + 16;
   static_assert(kStage % 128 == 0 && kBytes <= 232448, "shared memory budget");
 };
@@ -677,10 +677,20 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     ptx::fence_mbar_init();
   }
   __syncthreads();
+  // the largest element of the block's state; also the barrier behind which a chunk's stage is free
+  auto join_top = [&](int64_t i, bool ok) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < ND; ++j) m = fmaxf(fmaxf(m, fmaxf(fabsf(s[j][0]), fabsf(s[j][1]))), fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
+    m = warp_top(m);
+    if (lane == 0) tops[8 * (i & 1) + warp] = m;
+    return __syncthreads_or(!ok);
+  };
   if (tid == 0) {
     fetch(0);
     fetch(1);
   }
+  join_top(1, true);
   for (int64_t i = 0; i < chunks; ++i) {
     uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
     float* rf = reinterpret_cast<float*>(rec + R::kF);
@@ -696,25 +706,9 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       if (kBackward && half == 1) prefetch_l2(nx + R::kOq + (lane >> 4) * (2 * C * DV) + 2048 * slice + 128 * (lane & 15));
     }
     // the state as this chunk meets it
-    float top[2] = {0.f, 0.f}, sf[2], sinv[2];
-#pragma unroll
-    for (int j = 0; j < ND; ++j) {
-      top[0] = fmaxf(top[0], fmaxf(fabsf(s[j][0]), fabsf(s[j][1])));
-      top[1] = fmaxf(top[1], fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-      if (t == 0) tops[16 * warp + 8 * e + g] = top[e];
-    }
-    pair_sync();
-#pragma unroll
-    for (int e = 0; e < 2; ++e) pow2_factor(fmaxf(top[e], tops[16 * (warp ^ 4) + 8 * e + g]), sf[e], sinv[e]);
-    if (t == 0 && half == 0) {
-      rf[(kBackward ? R::fD : R::fS) + c] = sinv[0];
-      rf[(kBackward ? R::fD : R::fS) + c + 8] = sinv[1];
-    }
+    float top[2], sf, sinv;
+    pow2_factor(warp_top(tops[8 * ((i + 1) & 1) + (lane & 7)]), sf, sinv);
+    if (t == 0 && half == 0) rf[(kBackward ? R::fD : R::fS) + c] = rf[(kBackward ? R::fD : R::fS) + c + 8] = sinv;
     const bool ok = ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
     const uint8_t* st = sm + (i & 1) * L::kStage;
     const uint32_t W = ptx::smem_u32(st), K = W + (uint32_t)L::kTile, Q = K + (uint32_t)L::kTile;
@@ -728,7 +722,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       uint32_t hi[2][4], lo[2][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        pair_frag(s[4 * k2 + 2 * m], s[4 * k2 + 2 * m + 1], sf[0], sf[1], hi[m], lo[m]);
+        pair_frag(s[4 * k2 + 2 * m], s[4 * k2 + 2 * m + 1], sf, sf, hi[m], lo[m]);
         mma_pairs<RB, false, 8>(x, hi[m], lo[m], kBackward ? K : W, 0, d0 / 16 + 2 * k2 + m, ln);
       }
 #pragma unroll
@@ -756,10 +750,10 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     for (int j = 0; j < 8; ++j) {
       const float2 w = *reinterpret_cast<const float2*>(kw + 8 * j + 2 * t);
       const float2 f = kBackward ? w : make_float2(-winv, -winv);
-      x[j][0] = fmaf(x[j][0] * sinv[0], f.x, u[j].x);
-      x[j][1] = fmaf(x[j][1] * sinv[0], f.y, u[j].y);
-      x[j][2] = fmaf(x[j][2] * sinv[1], f.x, u[j].z);
-      x[j][3] = fmaf(x[j][3] * sinv[1], f.y, u[j].w);
+      x[j][0] = fmaf(x[j][0] * sinv, f.x, u[j].x);
+      x[j][1] = fmaf(x[j][1] * sinv, f.y, u[j].y);
+      x[j][2] = fmaf(x[j][2] * sinv, f.x, u[j].z);
+      x[j][3] = fmaf(x[j][3] * sinv, f.y, u[j].w);
       top[0] = fmaxf(top[0], fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
       top[1] = fmaxf(top[1], fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
     }
@@ -825,7 +819,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = fmaf(e < 2 ? o0 : o1, y[j][e], s[j][e]);
     }
-    if (__syncthreads_or(!ok)) {  // a copy never came: report it, wait once more for what is in flight, and leave
+    if (join_top(i, ok)) {  // a copy never came: report it, wait once more for what is in flight, and leave
       if (tid == 0) {
         report_status(a.status, kStatusTimeout);
         ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
@@ -857,8 +851,8 @@ __global__ void __launch_bounds__(kStateThreads) states_kernel(BwdArgs a) {
 
 // ------------------------------------------------------------------ 3. gradients
 // One block of 16 warps per (slot, qk-head), which takes its v-heads in turn, and of each 64 columns of Dv at a time:
-//   1. all warps: dX^T = dV'^T T; S^T, dS'^T and V'^T to one factor for all their rows
-//   2. warps 0-7: dO S^T; warps 8-15: V' dS'^T, then dX S^T and dV; warps 0-9: dA and dP, a 16 x 16 block of the
+//   1. all warps: dX^T = dV'^T T; V'^T to one factor for all its rows
+//   2. warps 0-7: dO S^T and dV; warps 8-15: V' dS'^T, then dX S^T; warps 0-9: dA and dP, a 16 x 16 block of the
 //      triangle each; all: <S, dS'>
 // and after a v-head's last columns
 //   3. warps 0-9: N and B
@@ -1028,20 +1022,17 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
       const bool ok = ptx::mbar_wait_bounded(bar, it & 1, kWaitLimitNs);
       ln.again();
       // ---- 1.
-      float mS, mD, mV, mX;
+      const float mS = rf[R::fS + v0], mD = rf[R::fD + v0];
+      float mV, mX;
       {
         auto top = [&](const float* f) {
           float m = 0.f;
           for (int i = lane; i < DV; i += 32) m = fmaxf(m, f[i]);
           return warp_top(m);
         };
-        mS = top(rf + R::fS);
-        mD = top(rf + R::fD);
         mV = top(rf + R::fV);
         mX = top(rf + R::fDV);
       }
-      rescale<RK>(sm + L::kS, rf + R::fS + v0, mS, tid);
-      rescale<RK>(sm + L::kD, rf + R::fD + v0, mD, tid);
       rescale<RC>(sm + L::kV, rf + R::fV + v0, mV, tid);
       {
         const int cb = 16 * (warp & 3), ib = 16 * (warp >> 2);
@@ -1086,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
           mma_pair(x[0], ah, al, bh, bl);
           mma_pair(x[1], ah, al, bh + 2, bl + 2);
         }
-        s_dot += (2 * ln.t == ln.g ? x[0][0] + x[1][2] : 0.f) + (2 * ln.t + 1 == ln.g ? x[0][1] + x[1][3] : 0.f);
+        s_dot = fmaf(mS * mD, (2 * ln.t == ln.g ? x[0][0] + x[1][2] : 0.f) + (2 * ln.t + 1 == ln.g ? x[0][1] + x[1][3] : 0.f), s_dot);
       }
       const float* gc = rf + R::fGc;
       if (first) {
@@ -1107,6 +1098,36 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) put_row(f[m][e] * dot[m][e], red + (w8 >> 1) * C + m0 + 16 * m + 8 * e + ln.g, ln.t, head);
+        ln.again();
+        // dV = diag(b) dX and its part of dbeta: 16 rows, 32 columns a warp
+        const int r0 = 16 * (w8 & 3) + ln.g, k0 = 2 * (w8 >> 2);
+        float s_v[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t hi[4], lo[4];
+          pair_a_t<RC>(hi, lo, Dx, 16 * (w8 & 3), 16 * (k0 + k), ln);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = r0 + 8 * (e & 1), c = v0 + 16 * (k0 + k) + 8 * (e >> 1) + 2 * ln.t;
+            if (r >= rows) continue;
+            float2 d = both2(hi[e], lo[e]);
+            d.x *= mX;
+            d.y *= mX;
+            const size_t at = ((size_t)(c0 + r) * a.nv + h) * DV + c;
+            const float b = rf[R::fBeta + r];
+            if constexpr (sizeof(IO) == 4) {
+              const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(a.v) + at);
+              s_v[e & 1] = fmaf(d.x, v.x, fmaf(d.y, v.y, s_v[e & 1]));
+              *reinterpret_cast<float2*>(static_cast<float*>(a.dv_out) + at) = make_float2(b * d.x, b * d.y);
+            } else {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.v) + at);
+              s_v[e & 1] = fmaf(d.x, __uint_as_float(v << 16), fmaf(d.y, __uint_as_float(v & 0xffff0000u), s_v[e & 1]));
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dv_out) + at) = ptx::pack_bf16x2(b * d.x, b * d.y);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) put_row(s_v[e], reda + (8 + (w8 >> 2)) * C + r0 + 8 * e, ln.t, head);
       } else {
         float f[2][2], dot[2][2];
         {
@@ -1144,35 +1165,6 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) put_row(u[m][e] * dot[m][e], red + (8 + (w8 >> 1)) * C + m0 + 16 * m + 8 * e + ln.g, ln.t, head);
-        // dV = diag(b) dX and its part of dbeta: 16 rows, 32 columns a warp
-        const int r0 = 16 * (w8 & 3) + ln.g, k0 = 2 * (w8 >> 2);
-        float s_v[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t hi[4], lo[4];
-          pair_a_t<RC>(hi, lo, Dx, 16 * (w8 & 3), 16 * (k0 + k), ln);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = r0 + 8 * (e & 1), c = v0 + 16 * (k0 + k) + 8 * (e >> 1) + 2 * ln.t;
-            if (r >= rows) continue;
-            float2 d = both2(hi[e], lo[e]);
-            d.x *= mX;
-            d.y *= mX;
-            const size_t at = ((size_t)(c0 + r) * a.nv + h) * DV + c;
-            const float b = rf[R::fBeta + r];
-            if constexpr (sizeof(IO) == 4) {
-              const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(a.v) + at);
-              s_v[e & 1] = fmaf(d.x, v.x, fmaf(d.y, v.y, s_v[e & 1]));
-              *reinterpret_cast<float2*>(static_cast<float*>(a.dv_out) + at) = make_float2(b * d.x, b * d.y);
-            } else {
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.v) + at);
-              s_v[e & 1] = fmaf(d.x, __uint_as_float(v << 16), fmaf(d.y, __uint_as_float(v & 0xffff0000u), s_v[e & 1]));
-              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dv_out) + at) = ptx::pack_bf16x2(b * d.x, b * d.y);
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) put_row(s_v[e], reda + (8 + (w8 >> 2)) * C + r0 + 8 * e, ln.t, head);
       }
       if (tri) {
         ln.again();
@@ -1198,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
       if (v0 + 64 < DV) continue;
       // ---- 3. what goes through A and P
       s_dot = warp_sum(s_dot);
-      if (lane == 0) dots[warp] = s_dot * mS * mD;
+      if (lane == 0) dots[warp] = s_dot;
       const float sP = oinv * mV, sA = mX * mV;
       if (tri) {
         ln.again();
