@@ -50,15 +50,14 @@ struct Rec {
   static constexpr int fGc = 0;                        // [C] gcum
   static constexpr int fBeta = fGc + C;                // [C] beta
   static constexpr int fScal = fBeta + C;              // [8] see Scal
-  static constexpr int fV = fScal + 8;                 // [DV] factor of every row of V'^T
-  static constexpr int fDV = fV + DV;                  // [DV] of dV'^T
+  static constexpr int fDV = fScal + 8;                // [DV] factor of every row of dV'^T
   static constexpr int fKw = fDV + DV;                 // [C] l_r / |k_r| in units of K16
   static constexpr int kFloats = fKw + C;
   static constexpr size_t kBytes = kF + 4 * kFloats;
   static_assert(kBytes % 16 == 0 && fScal % 4 == 0 && fKw % 4 == 0, "16-byte copies");
 };
-// factors of U, Y, diag(qe) dO, dO, S and dS', and e_last
-enum Scal { kScalU, kScalY, kScalO, kScalGl, kScalDo, kScalS, kScalD };
+// factors of U, Y, diag(qe) dO, dO, S, dS' and V', and e_last
+enum Scal { kScalU, kScalY, kScalO, kScalGl, kScalDo, kScalS, kScalD, kScalV };
 
 // Workspace record of one (chunk slot, qk-head), in bytes.
 template <int DK>
@@ -478,7 +477,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
 //   x^T = dS'^T K^T        then  dS^T = e_last dS'^T + (diag(qe) dO)^T Q - dV'^T W       backwards
 // Their A operands are what the gradients read as well (but for kw and qe), so they are written once to shared memory
 // and leave by bulk copies.  The tiles of a chunk come in two chunks ahead.  All columns of Dk are in the order of
-// swap32, which no product sees.  The state's image has one factor, joined over the block; V' and dV' keep one a row.
+// swap32, which no product sees.  The state's image has one factor, joined over the
+// block, and so has the image of V', which is written while the second product runs; the products' own V' diag(kw) and
+// dV' keep one a row.
 // A chunk waits for the one before it, and a thread issues an MMA every 90 to 130 cycles: so N is all of Dk, x is
 // two sums over half of Dk from two warps, and z = (diag(qe) dO)^T Q comes from a third (1.15 ms for 2 x 32768 tokens
 // and 32 heads of 128; 1.54 with one warp and N = 64, 1.51 with a ninth warp for all of them; 2.11 with warp MMAs).
@@ -492,8 +493,8 @@ struct StateSmem {  // from a 1024-byte boundary: tiles of the 128-byte swizzle
   static constexpr uint32_t kStage = oF + 1024;         // and kw [C], Scal [8]
   static constexpr uint32_t kS = 2 * kStage;            // S^T, panels of 128 rows
   static constexpr uint32_t kV = kS + 2 * 128 * DK;     // V'^T [128][C]
-  static constexpr uint32_t kTop = kV + 2 * 128 * C;    // fp32 [2][8] the warps' largest; [2][128] of the halves of a row of V'
-  static constexpr uint32_t kBar = kTop + 64 + 1024;    // five barriers
+  static constexpr uint32_t kTop = kV + 2 * 128 * C;    // fp32 [2][8], [8] the warps' largest of the state and V'; [2][128] of a row's halves
+  static constexpr uint32_t kBar = kTop + 96 + 1024;    // five barriers
   static constexpr uint32_t kTmem = kBar + 48;
   static constexpr uint32_t kBytes = kTmem + 16 + 1024;
   static constexpr uint32_t kKw = oO;                   // forwards: V'^T diag(kw) [128][C] where the first stage has no Oq
@@ -520,7 +521,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
   const bool active = 32 * (warp & 3) < DV;
   const int hq = h / (a.nv / a.nqk);
   const uint32_t base = ptx::smem_u32(sm);
-  float *tops = reinterpret_cast<float*>(sm + L::kTop), *rtops = tops + 16;
+  float *tops = reinterpret_cast<float*>(sm + L::kTop), *vtops = tops + 16, *rtops = tops + 24;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);     // a stage's copies (two), x, y, z
   int64_t start, end;
   seq_bounds(a, n, start, end);
@@ -652,20 +653,24 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       rtops[128 * half + c] = rtop;
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // warps w and w + 4
       pow2_factor(fmaxf(rtop, rtops[128 * (half ^ 1) + c]), vfac, vinv);
-      if (half == 0) rf[(kBackward ? R::fDV : R::fV) + c] = vinv;
+      if constexpr (kBackward) {
+        if (half == 0) rf[R::fDV + c] = vinv;
+      } else {
+        rtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rtop)));
+        if (lane == 0) vtops[warp] = rtop;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t at = row + (((uint32_t)(4 * half + t) ^ sw) << 4);
-        *reinterpret_cast<uint4*>(sm + L::kV + at) = pack8(x + 8 * t, vfac);
-        if (!kBackward) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[8 * t + e] *= w[8 * t + e] * 0x1p7f;  // kw 2^7 is at most 1
-          *reinterpret_cast<uint4*>(sm + L::kKw + at) = pack8(x + 8 * t, vfac);
-        }
+        for (int j = 0; j < 32; ++j) w[j] = x[j] * (w[j] * 0x1p7f);  // kw 2^7 is at most 1
       }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        *reinterpret_cast<uint4*>(sm + (kBackward ? L::kV : L::kKw) + row + (((uint32_t)(4 * half + t) ^ sw) << 4)) =
+            pack8((kBackward ? x : w) + 8 * t, vfac);
+    } else if (!kBackward && lane == 0) {
+      vtops[warp] = 0.f;
     }
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
+    if (!kBackward && tid == 32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last chunk's V has left
     __syncthreads();
     if (tid == 0) {
       ptx::tc_fence_after();
@@ -675,8 +680,8 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
         ptx::mma_bf16(tmem + tY, ptx::sdesc_sw128(A + 32 * k, 16, 1024), ptx::sdesc_sw128(b + 2048 * k, 128 * C, 1024),
                       ptx::idesc_f16_f32(128, DK, false, true), k > 0);
       ptx::mma_commit(bar + 3);
-    } else if (tid == 32) {
-      bulk_store(rec + (kBackward ? R::kX : R::kV), V, L::kRows);
+    } else if (kBackward && tid == 32) {
+      bulk_store(rec + R::kX, V, L::kRows);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     // what does not need y, meanwhile
@@ -693,6 +698,17 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
         }
       }
     } else {
+      float vtop = 0.f, f, inv;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vtop = fmaxf(vtop, vtops[j]);
+      pow2_factor(vtop, f, inv);
+      if (tid == 32) rf[R::fScal + kScalV] = inv;
+      if (active) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          *reinterpret_cast<uint4*>(sm + L::kV + row + (((uint32_t)(4 * half + t) ^ sw) << 4)) = pack8(x + 8 * t, f);
+      }
+      ptx::fence_proxy_async_smem();
 #pragma unroll
       for (int j = 0; j < NS; ++j) s[j] *= gl;
     }
@@ -709,8 +725,12 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       }
     }
     ptx::tc_fence_before();
-    if (tid == 32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // S and V may be written again
+    if (tid == 32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // S (and dV') may be written again
     quit = join_top(i, ok);
+    if (!kBackward && tid == 32) {
+      bulk_store(rec + R::kV, V, L::kRows);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
     if (quit) {  // a copy or a product never came: report it, wait once more for what is in flight, and leave
       if (tid == 0) {
         report_status(a.status, kStatusTimeout);
@@ -749,7 +769,7 @@ __global__ void __launch_bounds__(kStateThreads) states_half_kernel(BwdArgs a) {
 // ------------------------------------------------------------------ 3. gradients
 // One block of 16 warps per SM takes (slot, qk-head) items, and their v-heads in turn.  The tiles of the next
 // v-head (of the next item, after an item's last one) are fetched by bulk copies as soon as this one's are used:
-//   1. all warps: dX^T = dV'^T T; V'^T to one factor for all its rows
+//   1. all warps: dX^T = dV'^T T
 //   2. warps 0-7: dO S^T, then dA and dP; warps 8-15: V' dS'^T, then dX S^T; all: <S, dS'>
 //   3. warps 0-7: N and B; warps 8-15: dV
 //   4. warps 0-7: N K, and keep dq; warps 8-15: N^T Q + (B + B^T) K, and keep dk
@@ -969,17 +989,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
       // ---- 1.
       ln.again();
       ok &= ptx::mbar_wait_bounded(bar, nh & 1, kWaitLimitNs);
-      ok &= ptx::mbar_wait_bounded(bar + 1, nh & 1, kWaitLimitNs);
-      const float mV = top_factor(rf + R::fV, DV, lane), mX = top_factor(rf + R::fDV, DV, lane);
-#pragma unroll
-      for (int x = 0; x < DV * C / 8 / kGradThreads; ++x) {
-        const int v = x * kGradThreads + tid;
-        const float f = __fdividef(rf[R::fV + v / (C / 8)], mV);
-        const uint32_t f2 = pack2(f, f);
-        uint4* at = reinterpret_cast<uint4*>(sm + L::kV) + v;
-        const uint4 p = *at;
-        *at = make_uint4(mul2(p.x, f2), mul2(p.y, f2), mul2(p.z, f2), mul2(p.w, f2));
-      }
+      const float mV = rf[R::fScal + kScalV], mX = top_factor(rf + R::fDV, DV, lane);
       if (tid < C) eg[tid] = expf(rf[R::fGc + tid]);
       {  // times 2^7 for T and 2^-7: 16 columns of Dv by 16 or 32 tokens (T's zeros above the diagonal included)
         constexpr int NB = DV / 64;  // blocks of 16 tokens
@@ -1014,6 +1024,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
         fetch_x(last ? next : item, last ? (int)(next % a.nqk) * group : h + 1, nh + 1);
       // ---- 2.
       ln.again();
+      ok &= ptx::mbar_wait_bounded(bar + 1, nh & 1, kWaitLimitNs);
       ok &= ptx::mbar_wait_bounded(bar + 2, nh & 1, kWaitLimitNs);
       const float mS = rf[R::fScal + kScalS], mD = rf[R::fScal + kScalD], oinv = rf[R::fScal + kScalDo];
       {  // <S, dS'>: the diagonal of S^T dS', 16 columns of Dv and a share of Dk a warp
@@ -1381,12 +1392,12 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
 int64_t chunk_bwd_half_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv) {
   if (total_tokens == 0) return 0;
   const int64_t c = bwdh::C, slots = total_tokens / c + num_seqs;
-  const int64_t rec = 2 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (3 * c + 8 + 2 * dv);
+  const int64_t rec = 2 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (3 * c + 8 + dv);
   return slots * (nv * rec + nqk * (4 * c * dk + 16 * c) + (int64_t)sizeof(bwdh::SlotInfo));
 }
 
 cudaError_t launch_chunk_bwd_half(const BwdArgs& a, int dk, int dv, cudaStream_t s) {
-  static_assert(bwdh::Rec<128, 64>::kBytes == 2 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (3 * 64 + 8 + 2 * 64), "workspace size");
+  static_assert(bwdh::Rec<128, 64>::kBytes == 2 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (3 * 64 + 8 + 64), "workspace size");
   static_assert(bwdh::QkRec<128>::kBytes == 4 * 64 * 128 + 16 * 64, "workspace size");
   if (dk == 64 && dv == 64) return bwdh::launch_one<64, 64>(a, s);
   if (dk == 64 && dv == 128) return bwdh::launch_one<64, 128>(a, s);

@@ -399,7 +399,7 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
  * leaves the results undefined and is reported as GDN_ERR_GATE.  GDN_KERNEL_SIMT, fp32
  * io and calls without qk_l2norm hold each operand as a pair of fp16 numbers under such
  * a power of two: within 2^-22 of its value, or 2^-32 of the largest of its tile (64
- * tokens of one head; for q, k and the states one row), if that is more.  They take any
+ * tokens of one head, 64 columns of a state; one row of q and k), if that is more.  They take any
  * finite g and beta.  GDN_KERNEL_TC is rejected for the latter two kinds of call.  The
  * workspace size depends on that choice.
  *
