@@ -17,7 +17,8 @@ LIB = os.path.join(PKG, "libgdn.so")
 
 SOURCES = ["gdn_abi.cu", "chunk_simt.cu", "chunk_tc.cu", "decode_step.cu", "gated_rmsnorm.cu", "causal_conv.cu",
            "chunk_bwd.cu", "chunk_bwd_half.cu", "act8.cu", "gated_rmsnorm_bwd.cu", "causal_conv_bwd.cu", "gate_bwd.cu"]
-HEADERS = ["act8.cuh", "chunk_bwd.cuh", "f32x2.cuh", "gdn_common.cuh", "gdn_launch.h", "gdn_silu.cuh", "sm100_ptx.cuh"]
+HEADERS = ["act8.cuh", "chunk_bwd.cuh", "f32x2.cuh", "gdn_common.cuh", "gdn_launch.h", "gdn_silu.cuh", "sm100_ptx.cuh",
+           "train_common.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -6,7 +6,7 @@
 // once (3.03 bytes per bf16 value each way).  All of a thread's loads are issued
 // before any is used.
 #include "act8.cuh"
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 #include "gdn_launch.h"
 
 namespace gdn {

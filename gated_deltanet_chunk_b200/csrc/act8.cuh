@@ -10,7 +10,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 
 namespace gdn {
 namespace act8 {

@@ -25,7 +25,7 @@
 
 #include "act8.cuh"
 #include "f32x2.cuh"
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 #include "gdn_launch.h"
 #include "sm100_ptx.cuh"
 

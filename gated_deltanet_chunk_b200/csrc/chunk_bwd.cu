@@ -52,7 +52,7 @@
 // relative against 64 bits; now 3.1e-7).  Only the inverse's 16 x 16 blocks split TF32.
 
 #include "chunk_bwd.cuh"
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 #include "gdn_launch.h"
 #include "sm100_ptx.cuh"
 

@@ -5,7 +5,7 @@
 
 #include <cuda_fp16.h>
 
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 #include "sm100_ptx.cuh"
 
 namespace gdn {

@@ -23,7 +23,7 @@
 #include <type_traits>
 
 #include "chunk_bwd.cuh"
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 #include "gdn_launch.h"
 #include "sm100_ptx.cuh"
 
@@ -608,7 +608,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       for (int j = 0; j < DK / 32; ++j) {
         const int k = DK / 32 * half + j;  // step of 16 columns of Dk
         ptx::mma_bf16(tmem + 64 * half, ptx::sdesc_sw128(S + (k >> 2) * (128 * 128) + 32 * (k & 3), 16, 1024),
-                      ptx::sdesc_sw128(b + (k >> 2) * (128 * C) + 32 * (k & 3), 16, 1024), ptx::idesc_f16_f32(128, 64, false, false), j > 0);
+                      ptx::sdesc_sw128(b + (k >> 2) * (128 * C) + 32 * (k & 3), 16, 1024), idesc_f16_f32(128, 64, false, false), j > 0);
       }
       ptx::mma_commit(bar + 2);
     } else if (kBackward && tid == 64) {
@@ -616,7 +616,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         ptx::mma_bf16(tmem + tZ, ptx::sdesc_sw128(Oq + 2048 * k, 128 * C, 1024), ptx::sdesc_sw128(Q + 2048 * k, 128 * C, 1024),
-                      ptx::idesc_f16_f32(128, DK, true, true), k > 0);
+                      idesc_f16_f32(128, DK, true, true), k > 0);
       ptx::mma_commit(bar + 4);
     } else if (tid == 32) {
 #pragma unroll
@@ -678,7 +678,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         ptx::mma_bf16(tmem + tY, ptx::sdesc_sw128(A + 32 * k, 16, 1024), ptx::sdesc_sw128(b + 2048 * k, 128 * C, 1024),
-                      ptx::idesc_f16_f32(128, DK, false, true), k > 0);
+                      idesc_f16_f32(128, DK, false, true), k > 0);
       ptx::mma_commit(bar + 3);
     } else if (kBackward && tid == 32) {
       bulk_store(rec + R::kX, V, L::kRows);

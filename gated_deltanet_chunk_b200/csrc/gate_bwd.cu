@@ -9,7 +9,7 @@
 // second kernel, in a fixed order.  da is summed in fp32, before its rounding.
 // Bound by HBM where there is enough of it: 65,536 tokens x 32 heads, 34 MB, move
 // in @T0@; a few thousand tokens are one block's, and one launch.
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 #include "gdn_launch.h"
 
 namespace gdn {

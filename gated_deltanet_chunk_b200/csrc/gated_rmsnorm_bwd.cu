@@ -12,7 +12,7 @@
 // second kernel joins the blocks, in a fixed order.
 #include "act8.cuh"
 #include "f32x2.cuh"
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 #include "gdn_launch.h"
 
 namespace gdn {

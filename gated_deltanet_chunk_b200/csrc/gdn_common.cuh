@@ -94,90 +94,6 @@ struct ConvArgs {
   void* v;                   // [T or N, nv, dv]
 };
 
-// Arguments of the gradients of the chunked forward (gdn_chunk_bwd).
-struct BwdArgs {
-  const void* q;             // [T, Nqk, Dk]
-  const void* k;             // [T, Nqk, Dk]
-  const void* v;             // [T, Nv, Dv]
-  const float* g;            // [T, Nv]: g, or the raw projection a when A_log != nullptr
-  const float* beta;         // [T, Nv]: beta, or the raw projection b when A_log != nullptr
-  const float* A_log;        // [Nv] or nullptr (g and beta given)
-  const float* dt_bias;      // [Nv] (used with A_log)
-  const void* dout;          // [T, Nv, Dv]
-  const float* s0;           // [N, Nv, Dk, Dv] or nullptr
-  const float* ds_final;     // [N, Nv, Dk, Dv] or nullptr
-  const int32_t* cu;         // [N + 1] or nullptr (equal lengths)
-  void* dq;                  // [T, Nqk, Dk] outputs
-  void* dk;
-  void* dv_out;              // [T, Nv, Dv]
-  void* dg;                  // [T, Nv] in the io dtype
-  void* dbeta;               // [T, Nv] in the io dtype
-  float* ds0;                // [N, Nv, Dk, Dv] or nullptr
-  float* ws;                 // workspace (chunk_bwd_workspace bytes)
-  int32_t uniform_len;       // sequence length when cu == nullptr
-  int32_t num_seqs;
-  int64_t total_tokens;
-  unsigned int* status;      // device status word (kStatus* bits)
-  int32_t nqk, nv;
-  int32_t qk_l2norm;
-  float scale;
-};
-
-// Arguments of the gradients of the gated RMSNorm (gdn_gated_rmsnorm_bwd).
-struct NormBwdArgs {
-  const void* dy;            // [rows, dim] io dtype
-  const void* o;             // [rows, dim] io dtype, or e4m3 codes
-  const uint8_t* o_scales;   // [rows, dim / 32] when o holds codes, or nullptr
-  const void* z;             // as o
-  const uint8_t* z_scales;
-  const float* w;            // [dim]
-  float eps;
-  void* d_o;                 // [rows, dim] io dtype
-  void* d_z;
-  float* dw;                 // [dim]
-  int64_t rows;
-};
-
-// Arguments of the gradients of the gate (gdn_gate_bwd).
-struct GateBwdArgs {
-  const void* dg;            // [tokens, nv] io dtype
-  const void* dbeta;
-  const float* a;            // [tokens, nv]
-  const float* b;
-  const float* A_log;        // [nv]
-  const float* dt_bias;
-  void* da;                  // [tokens, nv] io dtype
-  void* db;
-  float* dA_log;             // [nv]
-  float* ddt_bias;
-  int64_t tokens;
-  int32_t nv;
-};
-
-// Arguments of the gradients of the causal conv1d + SiLU (gdn_qkv_conv_bwd).
-struct ConvBwdArgs {
-  const void* dq;            // [T, nqk, dk] io dtype
-  const void* dk_;
-  const void* dv_;           // [T, nv, dv]
-  const void* x;             // [T, channels] io dtype, or e4m3 codes
-  const uint8_t* x_scales;   // [T, channels / 32] when x holds codes, or nullptr
-  const float* weight;       // [channels, ksize]
-  const float* bias;         // [channels] or nullptr
-  const void* state_in;      // [N, channels, ksize] io dtype or nullptr (zeros)
-  const void* dstate_out;    // [N, channels, ksize] io dtype or nullptr
-  const int32_t* cu;         // [N + 1] or nullptr (equal lengths)
-  void* dx;                  // [T, channels] io dtype
-  float* dw;                 // [channels, ksize]
-  float* db;                 // [channels] or nullptr
-  void* dstate_in;           // [N, channels, ksize] io dtype or nullptr
-  int32_t uniform_len;       // sequence length when cu == nullptr
-  int32_t num_seqs;
-  int64_t total_tokens;
-  int32_t channels, ksize;   // channels = 2 nqk dk + nv dv
-  int32_t nqk, nv, dk, dv;
-  unsigned int* status;      // device status word (kStatus* bits)
-};
-
 template <typename T> __device__ __forceinline__ float to_f32(T x);
 template <> __device__ __forceinline__ float to_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) {
@@ -252,23 +168,18 @@ __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __ex
 // cumulative lengths).  A violation that this sequence sees (its own bounds out
 // of order or out of range, or a wrong first / last entry) is reported through
 // the status word, and the clamped bounds keep every access inside the tensors.
-// seq_bounds_quiet clamps without reporting, for kernels that look bounds up
-// again after another kernel of the same call has reported.
-template <class Args>
-__device__ __forceinline__ bool seq_bounds_quiet(const Args& a, int n, int64_t& start, int64_t& end) {
-  if (!a.cu) {
-    start = (int64_t)n * a.uniform_len;
-    end = start + a.uniform_len;
-    return true;
-  }
-  const int64_t s = a.cu[n], e = a.cu[n + 1], T = a.total_tokens;
-  start = s < 0 ? 0 : (s > T ? T : s);
-  end = e < start ? start : (e > T ? T : e);
-  return !(s < 0 || e < s || e > T || (n == 0 && s != 0) || (n == a.num_seqs - 1 && e != T));
-}
 template <class Args>
 __device__ __forceinline__ void seq_bounds(const Args& a, int n, int64_t& start, int64_t& end) {
-  if (!seq_bounds_quiet(a, n, start, end)) report_status(a.status, kStatusSeqlens);
+  if (a.cu) {
+    const int64_t s = a.cu[n], e = a.cu[n + 1], T = a.total_tokens;
+    const bool bad = s < 0 || e < s || e > T || (n == 0 && s != 0) || (n == a.num_seqs - 1 && e != T);
+    start = s < 0 ? 0 : (s > T ? T : s);
+    end = e < start ? start : (e > T ? T : e);
+    if (bad) report_status(a.status, kStatusSeqlens);
+  } else {
+    start = (int64_t)n * a.uniform_len;
+    end = start + a.uniform_len;
+  }
 }
 
 }  // namespace gdn

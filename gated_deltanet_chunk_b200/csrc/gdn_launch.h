@@ -3,7 +3,7 @@
 
 #include <cuda_runtime.h>
 
-#include "gdn_common.cuh"
+#include "train_common.cuh"
 
 namespace gdn {
 

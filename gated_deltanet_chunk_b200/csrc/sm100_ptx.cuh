@@ -282,11 +282,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// The same with fp16 A/B (the MMA instruction is the same).
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
-  return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
-}
-
 // ------------------------------------------------------------------ swizzled rows
 // Byte offset of 16-byte chunk c of row r inside a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t sw128_off(int r, int c) {
