@@ -446,8 +446,9 @@ def qkv_conv_update(mixed_qkv, weight, conv_state, nqk, nv, dk, dv, bias=None, s
 def _checked(what, device, *specs):
     """Raise ``GdnError`` (GDN_ERR_SHAPE) unless every (name, tensor, shape, dtype) given is a contiguous tensor of that
     shape and type on ``device``: gradients often come as views, expanded or in another type."""
+    at = -1 if device.index is None else device.index
     for name, t, shape, dtype in specs:
-        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device):
+        if t is not None and (t.dtype is not dtype or t.get_device() != at or not t.is_contiguous() or t.shape != shape):
             raise GdnError(-2, "%s (%s is not a contiguous %s tensor of shape %s on %s)"
                            % (what, name, str(dtype).replace("torch.", ""), tuple(shape), device))
 
@@ -683,11 +684,8 @@ def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt
              ("da", da, a.shape, io), ("db", db, a.shape, io), ("dA_log", dA_log, (nv,), f32), ("ddt_bias", ddt_bias, (nv,), f32))
     da = torch.empty_like(dg) if da is None else da
     db = torch.empty_like(dg) if db is None else db
-    if dA_log is None and ddt_bias is None:
-        dA_log, ddt_bias = torch.empty((2, nv), dtype=torch.float32, device=dg.device).unbind(0)
-    elif dA_log is None or ddt_bias is None:
-        new = torch.empty(nv, dtype=torch.float32, device=dg.device)
-        dA_log, ddt_bias = (new, ddt_bias) if dA_log is None else (dA_log, new)
+    dA_log = torch.empty_like(A_log) if dA_log is None else dA_log
+    ddt_bias = torch.empty_like(dt_bias) if ddt_bias is None else ddt_bias
     workspace = _workspace(workspace, lib().gdn_gate_bwd_workspace(int(T), int(nv)), "gdn_gate_bwd", dg.device)
     _run("gdn_gate_bwd", dg.device, check, _ptr(dg), _ptr(dbeta), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias),
          _ptr(da), _ptr(db), _ptr(dA_log), _ptr(ddt_bias), int(T), int(nv), DTYPE_BF16 if io == torch.bfloat16 else DTYPE_F32,

@@ -4,7 +4,12 @@
 // two neighbouring lanes, the codes move as 16-byte vectors, and a warp's 16 scale
 // bytes are contiguous.  Bound by HBM: a value is read once and its code written
 // once (3.03 bytes per bf16 value each way).  All of a thread's loads are issued
-// before any is used.
+// before any is used.  To quantize took as much issue time as traffic while every
+// value was looked at for infinities (363 us for 537 million bf16 values), so a
+// group's largest magnitude is found on the bits, two bf16 at a time, where
+// infinities and NaN are the largest: only a group that has one, or that reaches
+// fp32's last binade, takes the path that looks at each value: 239 us, and 238 to
+// read back, 1.63 GB each way, which is the rate of a plain copy.
 #include "act8.cuh"
 #include "train_common.cuh"
 #include "gdn_launch.h"
@@ -26,6 +31,17 @@ template <> struct Words<float> {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
   }
+  // The bits of the largest magnitude
+  __device__ static uint32_t top(const uint32_t* w) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t = max(t, w[i] & 0x7fffffffu);
+    return t;
+  }
+  // Values 2 i and 2 i + 1 times f
+  __device__ static float2 scaled(const uint32_t* w, int i, float f) {
+    return make_float2(__uint_as_float(w[2 * i]) * f, __uint_as_float(w[2 * i + 1]) * f);
+  }
 };
 template <> struct Words<__nv_bfloat16> {
   static constexpr int N = 8;
@@ -43,6 +59,17 @@ template <> struct Words<__nv_bfloat16> {
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
+  __device__ static uint32_t top(const uint32_t* w) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
+    return max(t & 0xffff0000u, t << 16);
+  }
+  // f is a power of two, and what falls below bf16's normal numbers is zero in e4m3: the product is exact in bf16
+  __device__ static float2 scaled(const uint32_t* w, int i, float f) {
+    const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(w + i), __float2bfloat162_rn(f));
+    return __bfloat1622float2(h);
+  }
 };
 
 // `n16` = values / 16 (even: whole groups).
@@ -59,32 +86,42 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const IO* __restrict
     const uint4 u = __ldcs(reinterpret_cast<const uint4*>(x + i * kPer) + j);
     w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
   }
-  float v[kPer], top = 0.f;
-  Words<IO>::unpack(w, v);
+  uint32_t top = Words<IO>::top(w), s, c[4];
+  top = max(top, __shfl_xor_sync(both, top, 1));
+  if (top < 0x7f000000u) {  // below 2^127
+    s = scale_byte(__uint_as_float(top));
+    const float f = inv_factor(s);
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const float m = fabsf(v[j]);
-    if (m < INFINITY) top = fmaxf(top, m); else v[j] = NAN;  // what is not finite reads back as NaN
-  }
-  top = fmaxf(top, __shfl_xor_sync(both, top, 1));
-  const uint32_t s = scale_byte(top);
-  const float f = inv_factor(s);
-  // 2^128 would be beyond fp32: the last binade is cut to what can be read back
-  const float lim = s >= 247u ? 240.f : 448.f;
-  uint32_t c[4];
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(Words<IO>::scaled(w, 2 * j, f), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(Words<IO>::scaled(w, 2 * j + 1, f), __NV_SATFINITE, __NV_E4M3);
+      c[j] = lo | (hi << 16);
+    }
+  } else {
+    float v[kPer], most = 0.f;
+    Words<IO>::unpack(w, v);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t p[2];
+    for (int j = 0; j < kPer; ++j) {
+      const float m = fabsf(v[j]);
+      if (m < INFINITY) most = fmaxf(most, m); else v[j] = NAN;  // what is not finite reads back as NaN
+    }
+    most = fmaxf(most, __shfl_xor_sync(both, most, 1));
+    s = scale_byte(most);
+    const float f = inv_factor(s);
+    // 2^128 would be beyond fp32: the last binade is cut to what can be read back
+    const float lim = s >= 247u ? 240.f : 448.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float2 y = make_float2(v[4 * j + 2 * k] * f, v[4 * j + 2 * k + 1] * f);
-      if (lim < 448.f) {
+    for (int j = 0; j < 4; ++j) {
+      uint32_t p[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float2 y = make_float2(v[4 * j + 2 * k] * f, v[4 * j + 2 * k + 1] * f);
         y.x = y.x > lim ? lim : (y.x < -lim ? -lim : y.x);  // a NaN stays one
         y.y = y.y > lim ? lim : (y.y < -lim ? -lim : y.y);
+        p[k] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
       }
-      p[k] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+      c[j] = p[0] | (p[1] << 16);
     }
-    c[j] = p[0] | (p[1] << 16);
   }
   __stcs(reinterpret_cast<uint4*>(codes) + i, make_uint4(c[0], c[1], c[2], c[3]));
   if ((threadIdx.x & 1) == 0) scales[i >> 1] = (uint8_t)s;

@@ -38,7 +38,7 @@ constexpr int kMinRun = 32;    // tokens of a run at least
 
 template <typename IO> struct Io;
 template <> struct Io<float> { static constexpr int E = 4, kPerSm = 8; };          // channels of a thread, blocks per SM
-template <> struct Io<__nv_bfloat16> { static constexpr int E = 8, kPerSm = 6; };
+template <> struct Io<__nv_bfloat16> { static constexpr int E = 8, kPerSm = 4; };
 
 struct Shape {
   int tiles;    // channel blocks
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
 #pragma unroll
-  for (int u = 0; u + 1 < kDepth; ++u) fetch(u);
+  for (int u = 0; u + 2 < kDepth; ++u) fetch(u);
 
   F2 w[K][P], b[P], dw[K][P], db[P], win[HA][P], pend[HA][P];
   const F2 zero = f2(0.f, 0.f);
@@ -239,16 +239,18 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
   auto scale_of = [&](int i) { return k8 ? (uint32_t)sbuf[threadIdx.x / 32][i & 31][(threadIdx.x & 31) * E / act8::kGroup] : 127u; };
   // Token i: its share of dw and dbias, of the pending gradients, and dx of token i - H.  kInside: the token is
   // this run's and its sequence's, and so is token i - H, which d_conv_state_out does not add to.
-  auto row = [&](int i, uint32_t scale, auto inside) {
-    constexpr bool kInside = decltype(inside)::value;
-    fetch((i + kDepth - 1) % kDepth);
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
-    F2 g[P], v[P], last[P];
+  auto load = [&](int i, uint32_t scale, F2* g, F2* v) {
     unpack<IO>(&ring_y[i % kDepth][threadIdx.x * 16], g);
     if constexpr (k8)
       decode<E>(&ring_x[i % kDepth][threadIdx.x * kX], act8::factor(scale), v);
     else
       unpack<IO>(&ring_x[i % kDepth][threadIdx.x * kX], v);
+  };
+  // two rows are in flight less than the ring holds: what comes in next replaces rows that are done with
+  auto arrived = [&]() { asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 2) : "memory"); };
+  auto row = [&](int i, F2* g, F2* v, auto inside) {
+    constexpr bool kInside = decltype(inside)::value;
+    F2 last[P];
     if (!kInside && (i < lo || i >= stop)) {  // of no sequence (inconsistent cu_seqlens, already reported)
 #pragma unroll
       for (int e = 0; e < P; ++e) g[e] = zero;
@@ -296,7 +298,16 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
     for (const int to = min(hi - 4, add - 4 + H); i >= lo + H && i <= to; i += 4) {
       if ((i & 31) == 0) scales(i);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) row(i + u, scale_of(i + u), std::true_type{});
+      for (int u = 0; u < 4; u += 2) {  // two rows' loads and slopes side by side: 16 of a thread's own are 53 % of the issue slots
+        F2 g[2][P], v[2][P];
+        fetch((i + u + kDepth - 2) % kDepth);
+        fetch((i + u + kDepth - 1) % kDepth);
+        arrived();
+        load(i + u, scale_of(i + u), g[0], v[0]);
+        load(i + u + 1, scale_of(i + u + 1), g[1], v[1]);
+        row(i + u, g[0], v[0], std::true_type{});
+        row(i + u + 1, g[1], v[1], std::true_type{});
+      }
     }
     if (i < rows && (i & 31) == 0) scales(i);
 #pragma unroll 1
@@ -321,7 +332,11 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
             pend[j][e] = zero;
           }
       }
-      row(i, scale_of(i), std::false_type{});
+      F2 g[P], v[P];
+      fetch((i + kDepth - 2) % kDepth);
+      arrived();
+      load(i, scale_of(i), g, v);
+      row(i, g, v, std::false_type{});
     }
     if (i == rows) {
 #pragma unroll

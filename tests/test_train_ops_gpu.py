@@ -262,3 +262,25 @@ def test_the_layer_and_back(gdn, io, bits8):
     want = torch.autograd.grad(G.conv(*leaves, None, lens)[0], leaves, torch.cat([y.cpu().flatten(1) for y in (dq, dk, dv)], 1).double())
     for name, g, e, ty in zip(("dx", "dw", "dbias"), (dx, dw, dbias), want, (io, torch.float32, torch.float32)):
         G.assert_close(g, e, ty, name)
+
+
+# ---------------------------------------------------------------- 8 bits, every bf16 number
+
+def test_quantize_every_bf16_number(gdn):
+    """All 65,536 bit patterns, 32 neighbours a group: subnormal groups, the last binade, infinities and NaN."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(2048, 32)
+    x64 = x.double()
+    fin = torch.isfinite(x64)
+    top = torch.where(fin, x64.abs(), 0.0).amax(1, keepdim=True)
+    m, ex = torch.frexp(top)                                   # top = m 2^ex, m in [1/2, 1): 448 = 7/8 2^9
+    e = torch.where(top > 0, ex - 9 + (m > 0.875).int(), torch.tensor(-126)).clamp(min=-126)
+    lim = torch.where(e >= 120, 240.0, 448.0)
+    y = torch.where(fin, x64, 0.0) * torch.exp2(-e.double())
+    step = torch.exp2(torch.frexp(y)[1].clamp(min=-5).double() - 4)   # three bits behind the first, 2^-9 at least
+    want = torch.minimum(torch.maximum(torch.round(y / step) * step, -lim), lim) * torch.exp2(e.double())
+    codes, scales = gdn.act_quantize(x.cuda())
+    assert torch.equal(scales.cpu().int() - 127, e.int())
+    got = read_back(codes, scales)
+    assert torch.isnan(got[~fin]).all() and torch.equal(got[fin], want[fin])
+    codes32, scales32 = gdn.act_quantize(x.float().cuda())
+    assert torch.equal(scales32, scales) and torch.equal(codes32.view(torch.uint8)[fin.cuda()], codes.view(torch.uint8)[fin.cuda()])
