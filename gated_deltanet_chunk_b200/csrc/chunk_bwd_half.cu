@@ -1,8 +1,8 @@
 // chunk_bwd_half.cu -- gradients of the chunked gated delta rule for bf16 tensors.
 //
 // The mathematics, the notation and the three kernels are those of chunk_bwd.cu.
-// Here every product is one warp MMA in fp16 (mma.sync.m16n8k16, fp32
-// accumulation): an operand is an fp16 number (11 significant bits) times a power
+// Here every product is one MMA in fp16 with fp32 accumulation (mma.sync.m16n8k16;
+// tcgen05 in the states kernel, where the next chunk waits for it): an operand is an fp16 number (11 significant bits) times a power
 // of two that its tile, row or column shares, chosen so that the largest
 // magnitude is in [2^7, 2^8) or bounded by it.  So
 //   - q, k, v and dout, which have 8 significant bits, are exact,
@@ -18,6 +18,16 @@
 // and normalised q, k; the prepare kernel checks the gates, and other calls take
 // chunk_bwd.cu): decays are at most 1, |T| <= 2 (row r of T is beta_r k_r^T times
 // a product of contractions, times k_i), |W| <= 2, |q_r . k_i| <= 1.
+//
+// Measured for 2 x 32768 tokens, 16 / 32 heads of 128, as prepare + states + gradients:
+// 1.50 + 1.16 + 2.49 ms (0.38 + 0.28 + 0.66 ms for 15,868 packed tokens).  What they read
+// and write, the tiles that they pass on included, is 5.1 + 6.5 + 6.1 GB, 2.7 ms at the
+// copy bandwidth: states is near it (86 %), prepare at half of it (a block's loads, its
+// inverse and its stores wait for one another, and two blocks per SM is what shared
+// memory holds), gradients at 37 % (17,000 cycles a v-head, of which the MMAs are
+// 6,000: the element-wise parts between them and two barriers are the rest).  Passing
+// tiles on in fp16 costs bytes but no second walk over the chunk; forming T, U and W
+// again in the gradients would cost more than the 1.3 GB it saves.
 #include <cuda_fp16.h>
 
 #include <type_traits>

@@ -9,7 +9,9 @@
 // dz written once.  The layout is that of gated_rmsnorm.cu: a row spans the lanes of
 // a group, and a thread's columns are the same in every row, so its part of dw
 // stays in registers until the block's groups are joined in shared memory; a
-// second kernel joins the blocks, in a fixed order.
+// second kernel joins the blocks, in a fixed order.  Measured: 16,384 tokens x 8 heads of
+// 128 in fp32, 0.34 GB, 55 us and 4 for the second kernel (87 % of the copy
+// bandwidth); 65,536 x 32 in bf16 from 8 bits, 2.16 GB, 366 and 4 us (89 %).
 #include "act8.cuh"
 #include "f32x2.cuh"
 #include "train_common.cuh"
@@ -19,8 +21,9 @@ namespace gdn {
 namespace rmsbwd {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;               // rows of a lane group in flight
-constexpr int kPerSm = 3;               // blocks per SM
+// 65,536 tokens x 32 heads of 128, o and z in 8 bits: 366 us; with 1 row in flight 413, with 2 or 4 blocks 412 and 496
+constexpr int kUnroll = 2;                // rows of a lane group in flight
+constexpr int kPerSm = 3;                 // blocks per SM
 constexpr int kMaxBlocks = 148 * kPerSm;  // one wave
 
 template <typename IO> struct Vec;  // 16 bytes of IO
