@@ -574,17 +574,18 @@ def act_quantize(x, codes=None, scales=None, check=True):
     Values that are not finite read back as NaN and do not touch their group's scale.
     """
     import torch
-    if x.shape[-1] % 32 != 0:
+    shape, device, bf16 = x.shape, x.device, x.dtype is torch.bfloat16
+    if shape[-1] % 32 != 0:
         raise GdnError(-2, "gdn_act_quantize")
-    shape, e4m3 = (*x.shape[:-1], x.shape[-1] // 32), torch.float8_e4m3fn
-    _checked("gdn_act_quantize", x.device, ("x", x, x.shape, torch.bfloat16 if x.dtype == torch.bfloat16 else torch.float32),
-             ("codes", codes, x.shape, e4m3), ("scales", scales, shape, torch.uint8))
+    groups = (*shape[:-1], shape[-1] // 32)
+    _checked("gdn_act_quantize", device, ("x", x, shape, torch.bfloat16 if bf16 else torch.float32),
+             ("codes", codes, shape, torch.float8_e4m3fn), ("scales", scales, groups, torch.uint8))
     if codes is None:
-        codes = torch.empty(x.shape, dtype=e4m3, device=x.device)
+        codes = torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
-    _run("gdn_act_quantize", x.device, check, _ptr(x), _ptr(codes), _ptr(scales), int(x.numel()),
-         DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32)
+        scales = torch.empty(groups, dtype=torch.uint8, device=device)
+    _run("gdn_act_quantize", device, check, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), x.numel(),
+         DTYPE_BF16 if bf16 else DTYPE_F32)
     return codes, scales
 
 
@@ -592,14 +593,15 @@ def act_quantize(x, codes=None, scales=None, check=True):
 def act_dequantize(codes, scales, dtype, out=None, check=True):
     """The values that ``act_quantize``'s codes and scales stand for, in ``dtype`` (``gdn_act_dequantize``)."""
     import torch
-    if codes.shape[-1] % 32 != 0 or dtype not in (torch.bfloat16, torch.float32):
+    shape, device, bf16 = codes.shape, codes.device, dtype is torch.bfloat16
+    if shape[-1] % 32 != 0 or not (bf16 or dtype is torch.float32):
         raise GdnError(-2, "gdn_act_dequantize")
-    _checked("gdn_act_dequantize", codes.device, ("codes", codes, codes.shape, torch.float8_e4m3fn),
-             ("scales", scales, (*codes.shape[:-1], codes.shape[-1] // 32), torch.uint8), ("out", out, codes.shape, dtype))
+    _checked("gdn_act_dequantize", device, ("codes", codes, shape, torch.float8_e4m3fn),
+             ("scales", scales, (*shape[:-1], shape[-1] // 32), torch.uint8), ("out", out, shape, dtype))
     if out is None:
-        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-    _run("gdn_act_dequantize", codes.device, check, _ptr(codes), _ptr(scales), _ptr(out), int(codes.numel()),
-         DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32)
+        out = torch.empty(shape, dtype=dtype, device=device)
+    _run("gdn_act_dequantize", device, check, codes.data_ptr(), _ptr(scales), out.data_ptr(), codes.numel(),
+         DTYPE_BF16 if bf16 else DTYPE_F32)
     return out
 
 
@@ -677,17 +679,17 @@ def gate_bwd(dg, dbeta, a, b, A_log, dt_bias, da=None, db=None, dA_log=None, ddt
     dA_log and ddt_bias [Nv] are fp32.
     """
     import torch
-    T, nv = a.shape
-    io, f32 = dg.dtype, torch.float32
-    _checked("gdn_gate_bwd", dg.device, ("dg", dg, a.shape, torch.bfloat16 if io == torch.bfloat16 else f32), ("dbeta", dbeta, a.shape, io),
-             ("a", a, a.shape, f32), ("b", b, a.shape, f32), ("A_log", A_log, (nv,), f32), ("dt_bias", dt_bias, (nv,), f32),
-             ("da", da, a.shape, io), ("db", db, a.shape, io), ("dA_log", dA_log, (nv,), f32), ("ddt_bias", ddt_bias, (nv,), f32))
+    shape, device, bf16, io, f32 = a.shape, dg.device, dg.dtype is torch.bfloat16, dg.dtype, torch.float32
+    T, nv = shape
+    head = (nv,)
+    _checked("gdn_gate_bwd", device, ("dg", dg, shape, torch.bfloat16 if bf16 else f32), ("dbeta", dbeta, shape, io), ("a", a, shape, f32),
+             ("b", b, shape, f32), ("A_log", A_log, head, f32), ("dt_bias", dt_bias, head, f32), ("da", da, shape, io), ("db", db, shape, io),
+             ("dA_log", dA_log, head, f32), ("ddt_bias", ddt_bias, head, f32))
     da = torch.empty_like(dg) if da is None else da
     db = torch.empty_like(dg) if db is None else db
     dA_log = torch.empty_like(A_log) if dA_log is None else dA_log
     ddt_bias = torch.empty_like(dt_bias) if ddt_bias is None else ddt_bias
-    workspace = _workspace(workspace, lib().gdn_gate_bwd_workspace(int(T), int(nv)), "gdn_gate_bwd", dg.device)
-    _run("gdn_gate_bwd", dg.device, check, _ptr(dg), _ptr(dbeta), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias),
-         _ptr(da), _ptr(db), _ptr(dA_log), _ptr(ddt_bias), int(T), int(nv), DTYPE_BF16 if io == torch.bfloat16 else DTYPE_F32,
-         _ptr(workspace), _bytes(workspace))
+    workspace = _workspace(workspace, lib().gdn_gate_bwd_workspace(T, nv), "gdn_gate_bwd", device)
+    _run("gdn_gate_bwd", device, check, _ptr(dg), _ptr(dbeta), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(da), _ptr(db),
+         _ptr(dA_log), _ptr(ddt_bias), T, nv, DTYPE_BF16 if bf16 else DTYPE_F32, _ptr(workspace), _bytes(workspace))
     return da, db, dA_log, ddt_bias
