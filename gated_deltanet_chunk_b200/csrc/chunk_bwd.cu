@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
   constexpr int RK = 2 * DK, RV = 2 * DV, RC = 2 * C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Lane ln(lane);
-  const int hq = blockIdx.y, group = a.nv / a.nqk;
-  const int64_t slot = blockIdx.x;
+  const int hq = blockIdx.x, group = a.nv / a.nqk;
+  const int64_t slot = grid_slot();
+  if (slot >= a.total_tokens / C + a.num_seqs) return;
   int64_t c0, end;
   if (!chunk_at(a, slot, c0, end)) return;
   const uint32_t base = ptx::smem_u32(sm);
@@ -975,8 +976,9 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
   Lane ln(lane);
   const bool first = warp < 8;       // warps 0-7, which keep dq
   const int w8 = warp & 7;
-  const int hq = blockIdx.y, group = a.nv / a.nqk, h0 = hq * group;
-  const int64_t slot = blockIdx.x;
+  const int hq = blockIdx.x, group = a.nv / a.nqk, h0 = hq * group;
+  const int64_t slot = grid_slot();
+  if (slot >= a.total_tokens / C + a.num_seqs) return;
   int64_t c0, end;
   if (!chunk_at(a, slot, c0, end)) return;
   const int rows = (int)min((int64_t)C, end - c0);
@@ -1407,14 +1409,14 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
   cudaError_t e;
   if (a.total_tokens > 0) {
     if ((e = set_smem(prepare_kernel<DK, DV, IO>, PrepSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
-    prepare_kernel<DK, DV, IO><<<dim3(slots, a.nqk), kThreads, PrepSmem<DK, DV>::kBytes, stream>>>(a);
+    prepare_kernel<DK, DV, IO><<<slot_grid(slots, a.nqk), kThreads, PrepSmem<DK, DV>::kBytes, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = set_smem(states_kernel<DK, DV>, StateSmem<DK>::kBytes)) != cudaSuccess) return e;
   states_kernel<DK, DV><<<dim3(2 * DV / (16 * kStateSlices), a.nv, a.num_seqs), kStateThreads, StateSmem<DK>::kBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.total_tokens == 0) return e;
   if ((e = set_smem(grads_kernel<DK, DV, IO>, GradSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
-  grads_kernel<DK, DV, IO><<<dim3(slots, a.nqk), kThreads, GradSmem<DK, DV>::kBytes, stream>>>(a);
+  grads_kernel<DK, DV, IO><<<slot_grid(slots, a.nqk), kThreads, GradSmem<DK, DV>::kBytes, stream>>>(a);
   return cudaGetLastError();
 }
 

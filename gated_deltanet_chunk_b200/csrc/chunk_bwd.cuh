@@ -17,25 +17,37 @@ constexpr int TP = C + 4;       // pitch of fp32 [C][C] tiles
 // Chunks are numbered by slots: chunk c of sequence n has slot cu[n] / C + n + c.
 // Slots of different sequences never meet (cu[n] / C + ceil(len / C) <= cu[n + 1] / C + 1),
 // and there are at most T / C + N of them.
-template <class Args>
-__device__ __forceinline__ int64_t first_slot(const Args& a, int n) {
-  int64_t s, e;
-  seq_bounds_quiet(a, n, s, e);
-  return s / C + n;
-}
-
-// The chunk at a slot: its sequence's end and its first token; false where the slot is empty.
+// The chunk at a slot: its sequence's end and its first token; false where the slot is empty.  By whole warps: 32
+// sequences are looked at together, so that a block waits for two or three loads and not for log2 of the sequences.
 template <class Args>
 __device__ __forceinline__ bool chunk_at(const Args& a, int64_t slot, int64_t& c0, int64_t& end) {
-  int lo = 0, hi = a.num_seqs - 1;
-  while (lo < hi) {  // the last sequence whose first slot is not beyond `slot`
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_slot(a, mid) <= slot) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, count = a.num_seqs;  // the last sequence of [lo, lo + count) whose first slot is not beyond `slot`
+  int64_t s, e;
+  while (true) {
+    const int step = (count + 31) / 32, n = lo + lane * step;
+    const bool in = lane * step < count;
+    s = e = 0;
+    if (in) seq_bounds_quiet(a, n, s, e);
+    const unsigned int before = __ballot_sync(0xffffffffu, in && s / C + n <= slot);
+    const int last = before ? 31 - __clz(before) : 0;
+    lo += last * step;
+    if (step == 1) {
+      s = __shfl_sync(0xffffffffu, s, last);
+      e = __shfl_sync(0xffffffffu, e, last);
+      break;
+    }
+    count = min(step, count - last * step);
   }
-  int64_t start;
-  seq_bounds_quiet(a, lo, start, end);
-  c0 = start + (slot - (start / C + lo)) * C;
-  return c0 >= start && c0 < end;
+  end = e;
+  c0 = s + (slot - (s / C + lo)) * C;
+  return c0 >= s && c0 < end;
+}
+
+// Slots and qk-heads of a grid whose blocks of one chunk follow one another, so that they share DRAM pages
+__device__ __forceinline__ int64_t grid_slot() { return (int64_t)blockIdx.z * 65535 + blockIdx.y; }
+static inline dim3 slot_grid(int64_t slots, int nqk) {
+  return dim3((unsigned int)nqk, (unsigned int)(slots < 65535 ? slots : 65535), (unsigned int)((slots + 65534) / 65535));
 }
 
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {

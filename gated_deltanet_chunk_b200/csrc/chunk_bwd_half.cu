@@ -278,8 +278,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   using QR = QkRec<DK>;
   extern __shared__ __align__(128) uint8_t sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
-  const int hq = blockIdx.y, group = a.nv / a.nqk;
-  const int64_t slot = blockIdx.x;
+  const int hq = blockIdx.x, group = a.nv / a.nqk;
+  const int64_t slot = grid_slot();
+  if (slot >= a.total_tokens / C + a.num_seqs) return;
   int64_t c0, end;
   const bool any = bwd::chunk_at(a, slot, c0, end);
   if (hq == 0 && tid == 0) *slot_info<DK, DV>(a, slot) = SlotInfo{c0, any ? (int32_t)min((int64_t)C, end - c0) : 0, 0};
@@ -1384,7 +1385,7 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
   cudaError_t e;
   if (a.total_tokens > 0) {
     if ((e = set_smem(prepare_half_kernel<DK, DV>, PrepSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
-    prepare_half_kernel<DK, DV><<<dim3(slots, a.nqk), kPrepThreads, PrepSmem<DK, DV>::kBytes, stream>>>(a);
+    prepare_half_kernel<DK, DV><<<slot_grid(slots, a.nqk), kPrepThreads, PrepSmem<DK, DV>::kBytes, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = set_smem(states_half_kernel<DK, DV>, StateSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
