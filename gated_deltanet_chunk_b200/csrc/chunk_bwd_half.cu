@@ -172,40 +172,58 @@ __device__ __forceinline__ void transpose4(uint4& v, int lane) {
 template <int DK>
 __device__ __forceinline__ void store_qk(const uint4 (&vec)[C * DK / 8 / kPrepThreads], __half* tile, uint8_t* img,
                                          float* f, float* wf, float* wn, int tid) {
-  constexpr int L = DK / 8, R = kPrepThreads / L;
+  constexpr int L = DK / 8, R = kPrepThreads / L, N = C / R;
   const int lr = tid % L;
+  float ss[N], top[N], s[N], inv[N];
 #pragma unroll
-  for (int p = 0; p < C / R; ++p) {
-    const int r = p * R + tid / L;
+  for (int p = 0; p < N; ++p) {
     const uint32_t u[4] = {vec[p].x, vec[p].y, vec[p].z, vec[p].w};
-    float2 v[4];
-    float ss = 0.f, top = 0.f;
+    ss[p] = top[p] = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i] = bf2(u[i]);
-      ss = fmaf(v[i].x, v[i].x, fmaf(v[i].y, v[i].y, ss));
-      top = fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+      const float2 v = bf2(u[i]);
+      ss[p] = fmaf(v.x, v.x, fmaf(v.y, v.y, ss[p]));
+      top[p] = fmaxf(top[p], fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+  }
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+      ss[p] += __shfl_xor_sync(0xffffffffu, ss[p], o);
+      top[p] = fmaxf(top[p], __shfl_xor_sync(0xffffffffu, top[p], o));
     }
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) {
-      ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    float s, inv;
-    pow2_factor(fmaxf(top, 0x1p-10f), s, inv);
+  for (int p = 0; p < N; ++p) {
+    const int r = p * R + tid / L;
+    const uint32_t u[4] = {vec[p].x, vec[p].y, vec[p].z, vec[p].w};
+    pow2_factor(fmaxf(top[p], 0x1p-10f), s[p], inv[p]);
     uint4 h;
-    h.x = pack2(v[0].x * s, v[0].y * s);
-    h.y = pack2(v[1].x * s, v[1].y * s);
-    h.z = pack2(v[2].x * s, v[2].y * s);
-    h.w = pack2(v[3].x * s, v[3].y * s);
+    uint32_t* w = &h.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = bf2(u[i]);
+      w[i] = pack2(v.x * s[p], v.y * s[p]);
+    }
     *reinterpret_cast<uint4*>(tile + r * (DK + 8) + 8 * lr) = h;
     transpose4(h, lr);
     *reinterpret_cast<uint4*>(img + image<-C>(r, (8 * lr & ~31) + 8 * (lr & 3))) = h;
-    if (lr == 0) {
-      f[r] = inv / sqrtf(ss + kNormEps);
-      wf[r] = f[r];
-      wn[r] = s;
-    }
+  }
+  static_assert(N <= L, "a lane for every row");
+  if (lr < N) {  // lane p has row p's factors: one square root and division for all
+    float q = ss[0], a = s[0], b = inv[0];
+#pragma unroll
+    for (int p = 1; p < N; ++p)
+      if (lr == p) {
+        q = ss[p];
+        a = s[p];
+        b = inv[p];
+      }
+    const int r = lr * R + tid / L;
+    b /= sqrtf(q + kNormEps);
+    f[r] = b;
+    wf[r] = b;
+    wn[r] = a;
   }
 }
 
