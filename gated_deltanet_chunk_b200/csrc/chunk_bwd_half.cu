@@ -238,24 +238,26 @@ __device__ __forceinline__ void prefetch_v(const bf16* x, int64_t c0, int64_t en
 
 // [C x DV] of v or dout for this thread: NV vectors of 8, vector i at row i R + tid / L
 template <int DV>
-__device__ __forceinline__ void load_v(const bf16* x, int64_t c0, int64_t end, int nv, int h, uint4 (&w)[C * DV / 8 / kPrepThreads],
-                                       float& top, int tid) {
+__device__ __forceinline__ void load_v(const bf16* x, int64_t c0, int64_t end, int nv, int h, uint4 (&w)[C * DV / 8 / kPrepThreads], int tid) {
   constexpr int L = DV / 8, R = kPrepThreads / L;
-  top = 0.f;
 #pragma unroll
   for (int p = 0; p < C / R; ++p) {
     const int r = p * R + tid / L;
     w[p] = make_uint4(0u, 0u, 0u, 0u);
     if (c0 + r < end) w[p] = *reinterpret_cast<const uint4*>(x + ((size_t)(c0 + r) * nv + h) * DV + 8 * (tid % L));
+  }
+}
+// The largest magnitude of a warp's vectors (a NaN does not count)
+template <int N>
+__device__ __forceinline__ float top_v(const uint4 (&w)[N]) {
+  __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
     const uint32_t u[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = bf2(u[i]);
-      top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-    }
+    for (int i = 0; i < 4; ++i) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(u + i)));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(__bfloat162float(__hmax(top.x, top.y)))));
 }
 template <int DV>
 __device__ __forceinline__ void store_v(const uint4 (&w)[C * DV / 8 / kPrepThreads], float s, __half* tile, uint8_t* img, int tid) {
@@ -352,13 +354,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
       }
   }
 
+  uint4 vw[C * DV / 8 / kPrepThreads], ow[C * DV / 8 / kPrepThreads];  // of the next v-head, while this one's U and Y are formed
+  load_v<DV>(static_cast<const bf16*>(a.v), c0, end, a.nv, hq * group, vw, tid);
+  load_v<DV>(static_cast<const bf16*>(a.dout), c0, end, a.nv, hq * group, ow, tid);
   for (int h = hq * group; h < (hq + 1) * group; ++h) {
     uint8_t* rec = rec_at<DK, DV>(a, slot, h);
     float* rf = reinterpret_cast<float*>(rec + R::kF);
-    uint4 vw[C * DV / 8 / kPrepThreads], ow[C * DV / 8 / kPrepThreads];
-    float vtop, otop;
-    load_v<DV>(static_cast<const bf16*>(a.v), c0, end, a.nv, h, vw, vtop, tid);
-    load_v<DV>(static_cast<const bf16*>(a.dout), c0, end, a.nv, h, ow, otop, tid);
+    float vtop = top_v(vw), otop = top_v(ow);
     float gv = 0.f, bv = 0.f;
     if (tid < C && c0 + tid < end) {
       load_gate(a, (size_t)(c0 + tid) * a.nv + h, h, gv, bv);
@@ -387,15 +389,31 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     store_v<DV>(vw, vs, V, nullptr, tid);
     store_v<DV>(ow, os, O, rec + R::kO, tid);
     __syncthreads();
-    if (tid < C) {
-      const float e = expf(gc[tid]);
+    float p[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int r = r0 + 4 * e, i = wc + 8 * j + 2 * t4;
+        const float2 gi = *reinterpret_cast<const float2*>(gc + i);
+        const float g0 = i <= r ? ptx::ex2_approx(1.44269504f * (gc[r] - gi.x)) : 0.f;  // masked before exp
+        const float g1 = i + 1 <= r ? ptx::ex2_approx(1.44269504f * (gc[r] - gi.y)) : 0.f;
+        *reinterpret_cast<float2*>(A + r * TP + i) =
+            make_float2(i < r ? -bt[r] * (kk[j][e] * g0) : 0.f, i + 1 < r ? -bt[r] * (kk[j][e + 1] * g1) : 0.f);
+        p[j][e] = qk[j][e] * g0 * 0x1p8f;
+        p[j][e + 1] = qk[j][e + 1] * g1 * 0x1p8f;
+      }
+    __syncthreads();
+    if (tid >= 128 && tid < 128 + C) {  // while warps 0-3 substitute
+      const int i = tid - 128;
+      const float e = expf(gc[i]);
       // 2^7 kf <= 1 (kf is at most 2^-7: the largest element of a row is at most its norm)
-      wf[tid] = bt[tid] * e * kf[tid] * 0x1p13f;
-      qe[tid] = __float2half_rn(e * qf[tid] * 0x1p7f);
-      rf[R::fGc + tid] = gc[tid];
-      rf[R::fBeta + tid] = bt[tid];
-      rf[R::fKw + tid] = expf(gc[C - 1] - gc[tid]) * kf[tid];
-      if (tid == C - 1) {
+      wf[i] = bt[i] * e * kf[i] * 0x1p13f;
+      qe[i] = __float2half_rn(e * qf[i] * 0x1p7f);
+      rf[R::fGc + i] = gc[i];
+      rf[R::fBeta + i] = bt[i];
+      rf[R::fKw + i] = expf(gc[C - 1] - gc[i]) * kf[i];
+      if (i == C - 1) {
         rf[R::fScal + kScalU] = 2.f * vinv;
         rf[R::fScal + kScalY] = a.scale * oinv;
         rf[R::fScal + kScalO] = a.scale * oinv * 0x1p-7f;
@@ -403,17 +421,6 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         rf[R::fScal + kScalDo] = oinv;
       }
     }
-    float p[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = r0 + 8 * (e >> 1), i = wc + 8 * j + 2 * t4 + (e & 1);
-        const float gamma = i <= r ? ptx::ex2_approx(1.44269504f * (gc[r] - gc[i])) : 0.f;  // masked before exp
-        A[r * TP + i] = i < r ? -bt[r] * (kk[j][e] * gamma) : 0.f;
-        p[j][e] = qk[j][e] * gamma * 0x1p8f;
-      }
-    __syncthreads();
     bwd::invert_chunk<false>(A, Y, warp, lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -461,6 +468,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
       const uint32_t q = *reinterpret_cast<const uint32_t*>(&f);
       w = make_uint4(mul2(w.x, q), mul2(w.y, q), mul2(w.z, q), mul2(w.w, q));
       *reinterpret_cast<uint4*>(rec + R::kOq + image<-C>(r, c)) = w;
+    }
+    if (h + 1 < (hq + 1) * group) {
+      load_v<DV>(static_cast<const bf16*>(a.v), c0, end, a.nv, h + 1, vw, tid);
+      load_v<DV>(static_cast<const bf16*>(a.dout), c0, end, a.nv, h + 1, ow, tid);
     }
     // U^T = V^T (T diag(b))^T and Y^T = dO^T P, 16 columns of Dv a unit
     for (int u = warp; u < DV / 16; u += kPrepThreads / 32) {
