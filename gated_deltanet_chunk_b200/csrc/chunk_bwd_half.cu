@@ -832,8 +832,8 @@ struct GradSmem {
   static constexpr size_t kB = kN + 2 * C * C;
   static constexpr size_t kK = kB + 2 * C * C;                // two of: K16, Q16 (columns by swap32) and their floats
   static constexpr size_t kKBytes = QkRec<DK>::kBytes;
-  static constexpr size_t kF = kK + 2 * kKBytes;              // two of: the record's floats up to fKw
-  static constexpr size_t kFBytes = 4 * R::fKw;
+  static constexpr size_t kF = kK + 2 * kKBytes;              // two of: the record's floats
+  static constexpr size_t kFBytes = 4 * R::kFloats;
   static constexpr size_t kE = kF + 2 * kFBytes;              // fp32 [C] e
   static constexpr size_t kRed = kE + 4 * C;                  // fp32 [3][4][C] rows' dots by column block
   static constexpr size_t kRedA = kRed + 48 * C;              // fp32 [6][C] row sums: through A and P (two halves: dgc, dbeta), dX V (two)
@@ -856,7 +856,7 @@ __device__ __forceinline__ float top_factor(const float* f, int n, int lane) {
 // A: an image [m][k], or [k][m]; B: an image [k][n].
 template <int NT, int K0, int K1, int RA, bool kAT, int RBB>
 __device__ __forceinline__ void gemm32(float (&x)[2][NT][4], uint32_t A, int m0, uint32_t B, int n0, const Lane& l) {
-#pragma unroll
+#pragma unroll 2
   for (int k = K0; k < K1; ++k) {
     uint32_t a0[4], a1[4];
     if (kAT) {
@@ -1194,7 +1194,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = m0 + 16 * m + 8 * e + ln.g;
-              f[m][e] = expf(rf[R::fGc + C - 1] - rf[R::fGc + r]) * kf[r] * mV * mD;
+              f[m][e] = rf[R::fKw + r] * mV * mD;
             }
           take<NT, RK>(x, K, m0, n0, f, sum, dot, ln);
         }
