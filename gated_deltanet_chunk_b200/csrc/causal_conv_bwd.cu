@@ -139,6 +139,7 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, int64_t t
 
 template <typename IO, int K, bool k8>
 __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(ConvBwdArgs a, Shape sh, float* part) {
+  let_next_begin();
   constexpr int E = Io<IO>::E, P = E / 2;
   constexpr int kX = k8 ? E : 16;          // bytes of a row of x
   constexpr int kDepth = 8;
@@ -360,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
 }
 
 // dw[c, i] and dbias[c] from the runs' parts [run][K + 1][channels]: 32 columns by 8 shares of the runs
-__global__ void __launch_bounds__(256) conv_weight_kernel(const float* __restrict__ part, int runs, int channels, int K, float* dw, float* db) {
+__global__ void __launch_bounds__(256) conv_weight_kernel(const float* part, int runs, int channels, int K, float* dw, float* db) {
+  let_next_begin();
+  wait_for_previous();
   __shared__ float sum[8][32];
   const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, i = blockIdx.y;
@@ -381,6 +384,7 @@ __global__ void __launch_bounds__(256) conv_weight_kernel(const float* __restric
 // sequence is shorter than K.
 template <typename IO, int K, bool k8>
 __global__ void __launch_bounds__(kStateThreads) conv_state_bwd_kernel(ConvBwdArgs a) {
+  wait_for_previous();
   const int64_t idx = (int64_t)blockIdx.x * kStateThreads + threadIdx.x;
   if (idx >= (int64_t)a.num_seqs * a.channels) return;
   const int n = (int)(idx / a.channels), c = (int)(idx % a.channels);
@@ -422,11 +426,10 @@ static cudaError_t launch_k(const ConvBwdArgs& a, float* part, cudaStream_t s) {
     conv_bwd_kernel<IO, K, k8><<<dim3(sh.tiles, sh.blocks), kThreads, 0, s>>>(a, sh, part);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  conv_weight_kernel<<<dim3((a.channels + 31) / 32, K + 1), 256, 0, s>>>(part, sh.blocks, a.channels, K, a.dw, a.db);
-  if ((e = cudaGetLastError()) != cudaSuccess || !a.dstate_in) return e;
+  e = launch_next(conv_weight_kernel, dim3((a.channels + 31) / 32, K + 1), 256, 0, s, part, sh.blocks, a.channels, K, a.dw, a.db);
+  if (e != cudaSuccess || !a.dstate_in) return e;
   const int64_t threads = (int64_t)a.num_seqs * a.channels;
-  conv_state_bwd_kernel<IO, K, k8><<<(unsigned int)((threads + kStateThreads - 1) / kStateThreads), kStateThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_next(conv_state_bwd_kernel<IO, K, k8>, (unsigned int)((threads + kStateThreads - 1) / kStateThreads), kStateThreads, 0, s, a);
 }
 template <typename IO, int K>
 static cudaError_t launch_io(const ConvBwdArgs& a, float* part, cudaStream_t s) {

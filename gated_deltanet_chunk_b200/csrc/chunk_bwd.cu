@@ -293,6 +293,7 @@ __device__ __forceinline__ void store_qk(const float (&v)[C * DK / 8 / kThreads]
 
 template <int DK, int DV, typename IO>
 __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
+  let_next_begin();
   using L = PrepSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
@@ -848,6 +849,8 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 // blockIdx.x: direction and 64-column slice, y: v-head, z: sequence
 template <int DK, int DV>
 __global__ void __launch_bounds__(kStateThreads) states_kernel(BwdArgs a) {
+  let_next_begin();
+  wait_for_previous();
   extern __shared__ __align__(128) uint8_t sm[];
   const int col0 = 16 * kStateSlices * (blockIdx.x >> 1);
   if (blockIdx.x & 1)
@@ -966,6 +969,7 @@ __device__ __forceinline__ void rescale(uint8_t* img, const float* f, float top,
 
 template <int DK, int DV, typename IO>
 __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
+  wait_for_previous();
   using L = GradSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
@@ -1413,11 +1417,10 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = set_smem(states_kernel<DK, DV>, StateSmem<DK>::kBytes)) != cudaSuccess) return e;
-  states_kernel<DK, DV><<<dim3(2 * DV / (16 * kStateSlices), a.nv, a.num_seqs), kStateThreads, StateSmem<DK>::kBytes, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.total_tokens == 0) return e;
+  e = launch_next(states_kernel<DK, DV>, dim3(2 * DV / (16 * kStateSlices), a.nv, a.num_seqs), kStateThreads, StateSmem<DK>::kBytes, stream, a);
+  if (e != cudaSuccess || a.total_tokens == 0) return e;
   if ((e = set_smem(grads_kernel<DK, DV, IO>, GradSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
-  grads_kernel<DK, DV, IO><<<slot_grid(slots, a.nqk), kThreads, GradSmem<DK, DV>::kBytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_next(grads_kernel<DK, DV, IO>, slot_grid(slots, a.nqk), kThreads, GradSmem<DK, DV>::kBytes, stream, a);
 }
 
 template <int DK, int DV>

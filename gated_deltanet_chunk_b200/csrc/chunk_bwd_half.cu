@@ -293,6 +293,7 @@ __device__ __forceinline__ void store_rows(uint8_t* img, int u, const float (&x)
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a) {
+  let_next_begin();
   using L = PrepSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
@@ -798,6 +799,8 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
 // blockIdx.x: direction, y: v-head, z: sequence
 template <int DK, int DV>
 __global__ void __launch_bounds__(kStateThreads) states_half_kernel(BwdArgs a) {
+  let_next_begin();
+  wait_for_previous();
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);
   if (blockIdx.x == 0)
@@ -908,6 +911,7 @@ __device__ __forceinline__ void put_row(float v, float* dst, int t) {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) {
+  wait_for_previous();
   using L = GradSmem<DK, DV>;
   using R = Rec<DK, DV>;
   using QR = QkRec<DK>;
@@ -1418,13 +1422,12 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = set_smem(states_half_kernel<DK, DV>, StateSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
-  states_half_kernel<DK, DV><<<dim3(2, a.nv, a.num_seqs), kStateThreads, StateSmem<DK, DV>::kBytes, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.total_tokens == 0) return e;
+  e = launch_next(states_half_kernel<DK, DV>, dim3(2, a.nv, a.num_seqs), kStateThreads, StateSmem<DK, DV>::kBytes, stream, a);
+  if (e != cudaSuccess || a.total_tokens == 0) return e;
   if ((e = set_smem(grads_half_kernel<DK, DV>, GradSmem<DK, DV>::kBytes)) != cudaSuccess) return e;
   const int64_t items = (int64_t)slots * a.nqk;
   const unsigned int grid = (unsigned int)(items < kSms ? items : kSms);
-  grads_half_kernel<DK, DV><<<grid, kGradThreads, GradSmem<DK, DV>::kBytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_next(grads_half_kernel<DK, DV>, grid, kGradThreads, GradSmem<DK, DV>::kBytes, stream, a);
 }
 
 }  // namespace bwdh

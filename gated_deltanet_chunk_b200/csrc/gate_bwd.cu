@@ -67,6 +67,7 @@ template <typename IO, int V> __device__ __forceinline__ void store(IO* p, const
 
 template <typename IO, int V>
 __global__ void __launch_bounds__(kThreads) gate_bwd_kernel(GateBwdArgs p, Shape s, float* part) {
+  let_next_begin();
   __shared__ float sum[2][V][kThreads];
   const int tid = threadIdx.x, cl = tid % s.cols, rl = tid / s.cols;
   const int h = (blockIdx.x * s.cols + cl) * V;
@@ -144,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) gate_bwd_kernel(GateBwdArgs p, Shape
 }
 
 // One block per column of part [blocks][cols]: out[c] = its sum.
-__global__ void __launch_bounds__(128) column_sums_kernel(const float* __restrict__ part, int blocks, int nv, float* dA, float* ddt) {
+__global__ void __launch_bounds__(128) column_sums_kernel(const float* part, int blocks, int nv, float* dA, float* ddt) {
+  wait_for_previous();
   __shared__ float sum[4];
   const int c = blockIdx.x;
   float s = 0.f;
@@ -166,8 +168,7 @@ static cudaError_t launch(const GateBwdArgs& p, float* part, cudaStream_t stream
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || s.blocks == 1) return e;
   }
-  column_sums_kernel<<<2 * p.nv, 128, 0, stream>>>(part, s.blocks, p.nv, p.dA_log, p.ddt_bias);
-  return cudaGetLastError();
+  return launch_next(column_sums_kernel, 2 * p.nv, 128, 0, stream, part, s.blocks, p.nv, p.dA_log, p.ddt_bias);
 }
 
 }  // namespace gatebwd

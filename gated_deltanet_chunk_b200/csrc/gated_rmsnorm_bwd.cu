@@ -90,6 +90,7 @@ struct Kept {
 
 template <typename IO, int DIM, bool kO8, bool kZ8>
 __global__ void __launch_bounds__(kThreads, kPerSm) gated_rmsnorm_bwd_kernel(NormBwdArgs p, float* part) {
+  let_next_begin();
   constexpr int E = Vec<IO>::N, L = DIM / E, G = kThreads / L;
   __shared__ float sum[G][DIM];
   const int lr = threadIdx.x % L, grp = threadIdx.x / L;
@@ -189,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) gated_rmsnorm_bwd_kernel(Nor
 }
 
 // out[c] = sum over blocks of part[block][c]; one warp a column
-__global__ void __launch_bounds__(kThreads) weight_sums_kernel(const float* __restrict__ part, int blocks, int dim, float* out) {
+__global__ void __launch_bounds__(kThreads) weight_sums_kernel(const float* part, int blocks, int dim, float* out) {
+  wait_for_previous();
   const int c = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
   float s = 0.f;
   for (int b = lane; b < blocks; b += 32) s += part[(size_t)b * dim + c];
@@ -218,8 +220,7 @@ static cudaError_t launch(const NormBwdArgs& p, float* part, cudaStream_t s) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  weight_sums_kernel<<<DIM / (kThreads / 32), kThreads, 0, s>>>(part, blocks, DIM, p.dw);
-  return cudaGetLastError();
+  return launch_next(weight_sums_kernel, DIM / (kThreads / 32), kThreads, 0, s, part, blocks, DIM, p.dw);
 }
 
 }  // namespace rmsbwd

@@ -1,6 +1,8 @@
 // train_common.cuh -- arguments of the training kernels, and what they share beyond gdn_common.cuh.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include "gdn_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -102,6 +104,26 @@ __device__ __forceinline__ void seq_bounds_quiet(const Args& a, int n, int64_t& 
   const int64_t s = a.cu[n], e = a.cu[n + 1], T = a.total_tokens;
   start = s < 0 ? 0 : (s > T ? T : s);
   end = e < start ? start : (e > T ? T : e);
+}
+
+// A call's kernels follow one another closely: each lets the next one be launched as soon as all its blocks have begun
+// (let_next_begin), and that one's blocks wait for its end before they do anything (wait_for_previous).  Launched by
+// launch_next; only the first kernel of a call is launched as usual, behind everything before it on the stream.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+static inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
 // Instruction descriptor of a tcgen05 MMA of kind::f16 with fp16 A/B and fp32 D (the type fields of the bf16 one are 1).
