@@ -20,9 +20,9 @@
 // a product of contractions, times k_i), |W| <= 2, |q_r . k_i| <= 1.
 //
 // Measured for 2 x 32768 tokens, 16 / 32 heads of 128, as prepare + states + gradients:
-// 1.50 + 1.16 + 2.49 ms (0.38 + 0.28 + 0.66 ms for 15,928 packed tokens).  What they read
+// 1.37 + 1.17 + 2.48 ms (0.35 + 0.28 + 0.65 ms for 15,928 packed tokens).  What they read
 // and write, the tiles that they pass on included, is 5.1 + 6.5 + 6.1 GB, 2.7 ms at the
-// copy bandwidth: states is near it (86 %), prepare at half of it (a block's loads, its
+// copy bandwidth: states is near it (85 %), prepare at 57 % (a block's loads, its
 // inverse and its stores wait for one another, and two blocks per SM is what shared
 // memory holds), gradients at 37 % (17,000 cycles a v-head, of which the MMAs are
 // 6,000: the element-wise parts between them and two barriers are the rest).  Passing
