@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
   let_next_begin();
   constexpr int E = Io<IO>::E, P = E / 2;
   constexpr int kX = k8 ? E : 16;          // bytes of a row of x
-  constexpr int kDepth = 8;
+  constexpr int kDepth = 8;                // rows of the ring; 4 or 16: within 2 %
   constexpr int H = K - 1;                 // inputs before the token
   constexpr int HA = H > 0 ? H : 1;
   __shared__ __align__(16) uint8_t ring_y[kDepth][kThreads * 16];

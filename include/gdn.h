@@ -418,7 +418,12 @@ int gdn_chunk_bwd(const void *q, const void *k, const void *v,
                   float *d_initial_state, void *workspace, int64_t workspace_bytes,
                   const gdn_params_t *p, void *cuda_stream);
 
-/* Bytes of workspace that gdn_chunk_bwd needs, or a negative gdn_status_t.  Host only. */
+/*
+ * Bytes of workspace that gdn_chunk_bwd needs, or a negative gdn_status_t.  Host only.
+ * About (total_tokens / 64 + num_seqs) * Nv records of 157 KB with fp16 operands and
+ * 315 KB otherwise at Dk = Dv = 128 (67 and 133 KB at 64): many sequences much shorter
+ * than 64 tokens take a record each.
+ */
 int64_t gdn_chunk_bwd_workspace(int32_t num_seqs, int64_t total_tokens, const gdn_params_t *p);
 
 /*
