@@ -277,13 +277,11 @@ __device__ __forceinline__ void store_qk(const float (&v)[C * DK / 8 / kThreads]
     *reinterpret_cast<uint4*>(tile + at + 16 * RB) = lo;
     *reinterpret_cast<uint4*>(plain + at) = hi;
     *reinterpret_cast<uint4*>(plain + at + 16 * RB) = lo;
-    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int w = pair_at<RB>(r, swap32(8 * lr + 2 * i));
-      *reinterpret_cast<uint32_t*>(swapped + w) = h[i];
-      *reinterpret_cast<uint32_t*>(swapped + w + 16 * RB) = l[i];
-    }
+    transpose4(hi, lr);
+    transpose4(lo, lr);
+    const int w = pair_at<RB>(r, (8 * lr & ~31) + 8 * (lr & 3));
+    *reinterpret_cast<uint4*>(swapped + w) = hi;
+    *reinterpret_cast<uint4*>(swapped + w + 16 * RB) = lo;
     if (lr == 0) {
       f[r] = wf[r] = inv;
       wn[r] = norm[p] * s;
@@ -319,6 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
     float kv[N][8], qv[N][8], kn[N], qn[N];
     load_qk<DK, IO>(static_cast<const IO*>(a.k), c0, end, a.nqk, hq, l2, kv, kn, rows, tid);
     load_qk<DK, IO>(static_cast<const IO*>(a.q), c0, end, a.nqk, hq, l2, qv, qn, rows + C, tid);
+    constexpr int LN = DV * sizeof(IO) / 128;  // v and dout of the group come into L2 meanwhile, a line of 128 bytes a thread
+    const int pr = tid % (C * LN) / LN;
+    if (tid < 2 * C * LN && c0 + pr < end) {
+      const IO* x = static_cast<const IO*>(tid < C * LN ? a.v : a.dout) + ((size_t)(c0 + pr) * a.nv + hq * group) * DV + tid % LN * (128 / sizeof(IO));
+      for (int h = 0; h < group; ++h) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (size_t)h * DV));
+    }
     __syncthreads();
     store_qk<DK>(kv, kn, l2, rows, sm + L::kK, qrec + QR::kK, qrec + QR::kKs, kf, qfl, qfl + 2 * C, tid);
     store_qk<DK>(qv, qn, l2, rows + C, sm + L::kQ, qrec + QR::kQ, qrec + QR::kQs, qf, qfl + C, qfl + 3 * C, tid);

@@ -182,6 +182,15 @@ template <int RB> __device__ __forceinline__ int image(int r, int col) {
 // own inverse.
 __device__ __forceinline__ int swap32(int d) { return (d & ~31) | (((d >> 1) & 3) << 3) | (((d >> 3) & 3) << 1) | (d & 1); }
 
+// Four lanes' vectors of four words each: lane m gets word m of all
+__device__ __forceinline__ void transpose4(uint4& v, int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1), b = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
+  if (odd) { v.x = a; v.z = b; } else { v.y = a; v.w = b; }
+  const uint32_t c = __shfl_xor_sync(0xffffffffu, high ? v.x : v.z, 2), d = __shfl_xor_sync(0xffffffffu, high ? v.y : v.w, 2);
+  if (high) { v.x = c; v.y = d; } else { v.z = c; v.w = d; }
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);

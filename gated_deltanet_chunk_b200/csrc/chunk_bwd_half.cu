@@ -161,14 +161,6 @@ __device__ __forceinline__ void load_rows(const bf16* x, int64_t c0, int64_t end
     if (c0 + r < end) w[p] = *reinterpret_cast<const uint4*>(x + ((size_t)(c0 + r) * heads + head) * DK + 8 * (tid % L));
   }
 }
-// Four lanes' vectors of four words each: lane m gets word m of all
-__device__ __forceinline__ void transpose4(uint4& v, int lane) {
-  const bool odd = lane & 1, high = lane & 2;
-  const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1), b = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
-  if (odd) { v.x = a; v.z = b; } else { v.y = a; v.w = b; }
-  const uint32_t c = __shfl_xor_sync(0xffffffffu, high ? v.x : v.z, 2), d = __shfl_xor_sync(0xffffffffu, high ? v.y : v.w, 2);
-  if (high) { v.x = c; v.y = d; } else { v.z = c; v.w = d; }
-}
 template <int DK>
 __device__ __forceinline__ void store_qk(const uint4 (&vec)[C * DK / 8 / kPrepThreads], __half* tile, uint8_t* img,
                                          float* f, float* wf, float* wn, int tid) {
