@@ -47,7 +47,7 @@
 // images that one bulk copy brings into shared memory.  An MMA of fp16 takes twice the
 // terms of one of TF32, and ldmatrix feeds it; with pairs of TF32 split as they were
 // loaded the three kernels took 0.56, 2.26 and 1.25 ms for 4 x 4096 tokens, 4 / 8 heads
-// of 128, against 0.28, 0.46 and 0.46 now (1 x 256 tokens, one head of 64: 16, 18 and
+// of 128, against 0.26, 0.46 and 0.46 now (1 x 256 tokens, one head of 64: 16, 18 and
 // 14 us).  Partial sums of one MMA step (16 terms) are added in fp32: the MMA itself
 // truncates, and over long sums that showed (3.8e-6 relative against 64 bits; now
 // 3.1e-7).  Only the inverse's 16 x 16 blocks split TF32.
@@ -411,18 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
       *reinterpret_cast<uint4*>(rec + R::kO + at + 16 * 128) = lo;
     }
     __syncthreads();
-    if (tid < C) {
-      const float e = expf(gc[tid]);
-      wf[tid] = bt[tid] * e * kf[tid];
-      qe[tid] = a.scale * e * qf[tid];
-      rf[R::fGc + tid] = gc[tid];
-      rf[R::fBeta + tid] = bt[tid];
-      rf[R::fKw + tid] = expf(gc[C - 1] - gc[tid]) * kf[tid];
-      if (tid == C - 1) {
-        rf[R::fScal + kScalGl] = e;
-        rf[R::fScal + kScalDo] = oinv;
-      }
-    }
     float p[2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -434,6 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
         p[j][e] = i <= r ? a.scale * qk[j][e] * gamma : 0.f;
       }
     __syncthreads();
+    if (tid >= 128 && tid < 128 + C) {  // while warps 0-3 substitute
+      const int i = tid - 128;
+      const float e = expf(gc[i]);
+      wf[i] = bt[i] * e * kf[i];
+      qe[i] = a.scale * e * qf[i];
+      rf[R::fGc + i] = gc[i];
+      rf[R::fBeta + i] = bt[i];
+      rf[R::fKw + i] = expf(gc[C - 1] - gc[i]) * kf[i];
+      if (i == C - 1) {
+        rf[R::fScal + kScalGl] = e;
+        rf[R::fScal + kScalDo] = oinv;
+      }
+    }
     invert_chunk<true>(A, Y, warp, lane);
     {  // pairs of T, T diag(b) and P, each under one factor
       float2 t[2][2], tb[2][2];
