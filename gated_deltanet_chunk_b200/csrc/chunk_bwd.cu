@@ -32,12 +32,13 @@
 // Only S -> S' and dS' -> dS are sequential, and both are separable in the Dv
 // columns.  So three kernels run one after another:
 //   1. prepare (every chunk and v-head at once): T, U, W, Y = P^T dO.
-//   2. states: one warp per 16 Dv columns walks its sequence, forwards for S
-//      and V', backwards for dS' and dV'.  The state slice stays in the warp's
-//      registers as S^T [16 x Dk] MMA accumulators, whose layout is that of
-//      the next product's A operand, so a chunk is two (or three) chained
-//      products without a shared-memory round trip.  The two directions need
-//      nothing of each other and run in the same launch.
+//   2. states: two warps per 16 Dv columns walk their sequence, forwards for S
+//      and V', backwards for dS' and dV'.  The state slice stays in their
+//      registers as S^T [16 x Dk] MMA accumulators, half of Dk each, whose layout
+//      is that of the next product's A operand, so a chunk is two (or three)
+//      chained products, and all that goes through shared memory is one sum of
+//      what both have.  The two directions need nothing of each other and run in
+//      the same launch.
 //   3. gradients (every chunk and qk-head at once): the rest.  One block takes
 //      all the v-heads that share a qk-head, one after another, so dq and dk
 //      are summed in registers, in a fixed order.

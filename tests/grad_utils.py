@@ -70,10 +70,10 @@ def conv(x, w, b, state, lens):
 def assert_close(got, want, io, what, floor=0.0):
     """Every element within the rounding of its type and the arithmetic of the path.
 
-    fp32: operands are split into TF32 pairs, each product within 2^-22 of its value, and sums run over at
+    fp32: operands are pairs hi + lo, each product within 2^-22 of its value, and sums run over at
     most 128 terms in fp32 (2^-24 sqrt(128) < 2^-20); a gradient passes through at most about 16 such
     products, so 16 * 2^-20 = 2^-16 of the largest element bounds it.  bf16: the same plus one rounding of
-    the output, half a step = 2^-8 of the element, and operands that may be held to TF32's 2^-12 in place of
+    the output, half a step = 2^-8 of the element, and operands that may be held to fp16's 2^-12 in place of
     pairs: through 4 of them, 2^-10 of the largest element.
     """
     got, want = got.detach().cpu().double(), want.detach().cpu().double()
