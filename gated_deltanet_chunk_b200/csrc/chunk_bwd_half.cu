@@ -117,10 +117,6 @@ template <int P> __device__ __forceinline__ void frag_b_t(uint32_t* r, const __h
   ldsm_t(r, tile + (k0 + (lane & 15)) * P + n0 + 8 * (lane >> 4));
 }
 
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ float2 bf2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
@@ -141,9 +137,9 @@ struct PrepSmem {
   static constexpr size_t kA = kO + 2 * C * VP;                         // fp32 [C][TP] A, then T
   static constexpr size_t kY = kA + 4 * C * TP;                         // fp32 [C / 2][TP] scratch of the inverse
   static constexpr size_t kF = kY + 2 * C * TP;                         // fp32 [C] each: gc, beta, kf, qf, T's column factors of W
-  static constexpr size_t kQe = kF + 20 * C;                            // fp16 [C] e qf 2^7 (at most 1)
-  static constexpr size_t kTop = kQe + 2 * C;                           // fp32 [2][8] largest |v|, |dO| by warp
-  static constexpr size_t kBytes = kTop + 64;
+  static constexpr size_t kQe = kF + 20 * C;                            // fp32 [C] e qf
+  static constexpr size_t kTop = kQe + 4 * C;                           // fp32 [3][8] largest |v|, |dO|, |diag(qe) dO| by warp
+  static constexpr size_t kBytes = kTop + 96;
   static_assert(kBytes <= 113 * 1024, "two blocks per SM");
 };
 
@@ -239,17 +235,16 @@ __device__ __forceinline__ void load_v(const bf16* x, int64_t c0, int64_t end, i
     if (c0 + r < end) w[p] = *reinterpret_cast<const uint4*>(x + ((size_t)(c0 + r) * nv + h) * DV + 8 * (tid % L));
   }
 }
-// The largest magnitude of a warp's vectors (a NaN does not count)
-template <int N>
-__device__ __forceinline__ float top_v(const uint4 (&w)[N]) {
-  __nv_bfloat162 top = __float2bfloat162_rn(0.f);
-#pragma unroll
-  for (int p = 0; p < N; ++p) {
-    const uint32_t u[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(u + i)));
-  }
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(__bfloat162float(__hmax(top.x, top.y)))));
+// The largest magnitudes of a vector's even and odd elements (a NaN does not count), and over a warp or its shares in `t`
+__device__ __forceinline__ __nv_bfloat162 top_v(const uint4& w) {
+  const __nv_bfloat162* u = reinterpret_cast<const __nv_bfloat162*>(&w);
+  return __hmax2(__hmax2(__habs2(u[0]), __habs2(u[1])), __hmax2(__habs2(u[2]), __habs2(u[3])));
+}
+__device__ __forceinline__ float top_f(__nv_bfloat162 x) { return fmaxf(__bfloat162float(x.x), __bfloat162float(x.y)); }
+__device__ __forceinline__ float warp_top(float x) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x))); }
+__device__ __forceinline__ float top8(const float* t) {
+  const float4 a = *reinterpret_cast<const float4*>(t), b = *reinterpret_cast<const float4*>(t + 4);
+  return fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
 }
 template <int DV>
 __device__ __forceinline__ void store_v(const uint4 (&w)[C * DV / 8 / kPrepThreads], float s, __half* tile, uint8_t* img, int tid) {
@@ -302,7 +297,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   __half *TB = Q, *P = Q + C * HP, *V = reinterpret_cast<__half*>(sm + L::kV), *O = reinterpret_cast<__half*>(sm + L::kO);
   float *A = reinterpret_cast<float*>(sm + L::kA), *Y = reinterpret_cast<float*>(sm + L::kY);
   float *gc = reinterpret_cast<float*>(sm + L::kF), *bt = gc + C, *kf = bt + C, *qf = kf + C, *wf = qf + C;
-  __half* qe = reinterpret_cast<__half*>(sm + L::kQe);
+  float* qe = reinterpret_cast<float*>(sm + L::kQe);
   float* tops = reinterpret_cast<float*>(sm + L::kTop);
   uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
   float* qfl = reinterpret_cast<float*>(qrec + QR::kF);
@@ -353,7 +348,15 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   for (int h = hq * group; h < (hq + 1) * group; ++h) {
     uint8_t* rec = rec_at<DK, DV>(a, slot, h);
     float* rf = reinterpret_cast<float*>(rec + R::kF);
-    float vtop = top_v(vw), otop = top_v(ow);
+    constexpr int NV = C * DV / 8 / kPrepThreads;
+    __nv_bfloat162 vt = __float2bfloat162_rn(0.f), orow[NV], ot = vt;  // orow: of this thread's part of a row of dO
+#pragma unroll
+    for (int p = 0; p < NV; ++p) {
+      vt = __hmax2(vt, top_v(vw[p]));
+      orow[p] = top_v(ow[p]);
+      ot = __hmax2(ot, orow[p]);
+    }
+    float vtop = warp_top(top_f(vt)), otop = warp_top(top_f(ot));
     float gv = 0.f, bv = 0.f;
     if (tid < C && c0 + tid < end) {
       load_gate(a, (size_t)(c0 + tid) * a.nv + h, h, gv, bv);
@@ -370,12 +373,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     }
     __syncthreads();
     if (warp == 0) bwd::cumsum_chunk(gc, lane);
-    vtop = otop = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      vtop = fmaxf(vtop, tops[i]);
-      otop = fmaxf(otop, tops[8 + i]);
-    }
+    vtop = top8(tops);
+    otop = top8(tops + 8);
     float vs, vinv, os, oinv;
     pow2_factor(vtop, vs, vinv);
     pow2_factor(otop, os, oinv);
@@ -402,14 +401,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
       const float e = expf(gc[i]);
       // 2^7 kf <= 1 (kf is at most 2^-7: the largest element of a row is at most its norm)
       wf[i] = bt[i] * e * kf[i] * 0x1p13f;
-      qe[i] = __float2half_rn(e * qf[i] * 0x1p7f);
+      qe[i] = e * qf[i];
       rf[R::fGc + i] = gc[i];
       rf[R::fBeta + i] = bt[i];
       rf[R::fKw + i] = expf(gc[C - 1] - gc[i]) * kf[i];
       if (i == C - 1) {
         rf[R::fScal + kScalU] = 2.f * vinv;
         rf[R::fScal + kScalY] = a.scale * oinv;
-        rf[R::fScal + kScalO] = a.scale * oinv * 0x1p-7f;
         rf[R::fScal + kScalGl] = e;
         rf[R::fScal + kScalDo] = oinv;
       }
@@ -425,6 +423,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         *reinterpret_cast<uint32_t*>(TB + r * HP + i) = pack2(t.x * bt[i] * 0x1p6f, t.y * bt[i + 1] * 0x1p6f);
         *reinterpret_cast<uint32_t*>(rec + R::kT + image<2 * C>(r, i)) = pack2(t.x * 0x1p7f, t.y * 0x1p7f);
       }
+    float qtop = 0.f;
+#pragma unroll
+    for (int p = 0; p < NV; ++p) qtop = fmaxf(qtop, top_f(orow[p]) * qe[(p * kPrepThreads + tid) / (DV / 8)]);
+    qtop = warp_top(qtop);
+    if (lane == 0) tops[16 + warp] = qtop;
     __syncthreads();
     {  // W 2^7 = (T diag(b e kf) 2^13) K16 2^-6: this warp's 16 rows, one half of the columns
       constexpr int NT = DK / 16;
@@ -453,14 +456,25 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         for (int e = 0; e < 4; e += 2)
           *reinterpret_cast<uint4*>(rec + R::kW + image<-C>(r0 + 4 * e, n0 + 8 * j + 8 * t4)) = swapped32(x + j, e, 0x1p-6f);
     }
+    {  // diag(qe) dO: fp32 products, rounded once, under a factor that follows the largest of them.  e spans any number of
+       // binades over a chunk and between chunks, so a factor that did not would lose the digits of dS behind a strong gate
+      float f, inv;
+      pow2_factor(top8(tops + 16), f, inv);
+      if (tid == 0) rf[R::fScal + kScalO] = a.scale * inv;
 #pragma unroll
-    for (int p = 0; p < C * DV / 8 / kPrepThreads; ++p) {  // diag(qe) dO
-      const int r = (p * kPrepThreads + tid) / (DV / 8), c = 8 * (tid % (DV / 8));
-      uint4 w = *reinterpret_cast<const uint4*>(O + r * L::VP + c);
-      const __half2 f = __half2half2(qe[r]);
-      const uint32_t q = *reinterpret_cast<const uint32_t*>(&f);
-      w = make_uint4(mul2(w.x, q), mul2(w.y, q), mul2(w.z, q), mul2(w.w, q));
-      *reinterpret_cast<uint4*>(rec + R::kOq + image<-C>(r, c)) = w;
+      for (int p = 0; p < NV; ++p) {
+        const int r = (p * kPrepThreads + tid) / (DV / 8), c = 8 * (tid % (DV / 8));
+        uint4 w = *reinterpret_cast<const uint4*>(O + r * L::VP + c);
+        uint32_t* u = &w.x;
+        // dO16 oinv is dO.  A row that is not zero in dO16 (at least 2^-24) has a factor of at most 2^32
+        const float q = fminf(qe[r] * f * oinv, 0x1p100f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 o = unpack2(u[i]);
+          u[i] = pack2(o.x * q, o.y * q);
+        }
+        *reinterpret_cast<uint4*>(rec + R::kOq + image<-C>(r, c)) = w;
+      }
     }
     if (h + 1 < (hq + 1) * group) {
       load_v<DV>(static_cast<const bf16*>(a.v), c0, end, a.nv, h + 1, vw, tid);

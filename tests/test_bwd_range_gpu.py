@@ -1,0 +1,61 @@
+"""Gradients of the chunked forward on a B200 where factors of a chunk lie many binades apart: strong gates, tokens without a
+value or a gradient, small or large beta, keys that repeat.  Every head is held to its own largest element, against 64-bit
+autograd of the token recurrence.
+
+Tolerances.  bf16 tensors: a path from the inputs to a gradient takes at most four operands that are rounded to fp16, by
+half a step, 2^-11 of the value, each: 4 * 2^-11 = 2^-9 of the largest element, and the rounding of a bf16 output, 2^-8 of the
+element.  fp32, and bf16 with kernel="simt": operands within 2^-22, sums of at most 128 terms in fp32 (2^-24 sqrt(128) < 2^-20),
+at most about 16 such products: 16 * 2^-20 = 2^-16 of the largest element.
+"""
+import pytest
+import torch
+
+from tests import grad_utils as G
+from tests.test_bwd_gpu import NAMES, gdn, make, run  # noqa: F401 (gdn: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+PATHS = [(torch.float32, "auto"), (torch.bfloat16, "auto"), (torch.bfloat16, "simt")]
+
+
+def close(name, got, want, io, kernel, by=1.0):
+    """Head by head (axis 1); ds0 also sequence by sequence.  `by`: how often the tolerance of the operands is allowed."""
+    got, want = got.detach().cpu().double(), want.detach().cpu().double()
+    assert got.shape == want.shape and torch.isfinite(got).all(), name
+    operands = by * (2.0 ** -9 if io == torch.bfloat16 and kernel == "auto" else 2.0 ** -16)
+    own = 0.0 if io == torch.float32 or name == "ds0" else 2.0 ** -8
+    for n in range(want.shape[0]) if name == "ds0" else [slice(None)]:
+        for h in range(want.shape[1]):
+            a, b = got[n, h] if name == "ds0" else got[:, h], want[n, h] if name == "ds0" else want[:, h]
+            top = b.abs().max().item()
+            over = ((a - b).abs() - own * b.abs()).max().item()
+            assert over <= operands * top, "%s of head %d: off by %.2e of its largest element %.2e" % (name, h, over / max(top, 1e-300), top)
+
+
+def check(gdn, x, lens, io, kernel, names, by=1.0, **kw):
+    got = run(gdn, x, lens, kernel=kernel, **kw)
+    assert gdn.device_status() == 0
+    want = G.rule_grads(x["q"], x["k"], x["v"], x["g"], x["beta"], x["s0"], x["dout"], x["ds"], lens)
+    for name, a, b in zip(NAMES, got, want):
+        if name in names:
+            close(name, a, b, io, kernel, by)
+
+
+def starts(lens):
+    """The first token of every chunk."""
+    at, out = 0, []
+    for length in lens:
+        out += list(range(at, at + length, 64))
+        at += length
+    return out
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("lens", [(1,), (40,), (64, 3)])
+@pytest.mark.parametrize("first", [-8.0, -12.0, -16.0, -30.0])
+def test_output_gradients_reach_the_state_behind_a_strong_gate(gdn, io, kernel, lens, first):
+    """d_initial_state is then what dout leaves of it: with beta = 0 nothing else adds to it."""
+    x = make(lens, 1, 2, 128, 64, io, s0=True)
+    x["g"][starts(lens)] = first
+    x["beta"].zero_()
+    check(gdn, x, lens, io, kernel, ("ds0",))
