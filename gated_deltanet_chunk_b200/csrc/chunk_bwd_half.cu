@@ -17,7 +17,7 @@
 // Bounds that the fixed factors of two use (they hold for 0 <= beta <= 2, g <= 0
 // and normalised q, k; the prepare kernel checks the gates, and other calls take
 // chunk_bwd.cu): decays are at most 1, |T| <= 2 (row r of T is beta_r k_r^T times
-// a product of contractions, times k_i), |W| <= 2, |q_r . k_i| <= 1.
+// a product of contractions, times k_i), |W_r| <= beta_r e_r, |q_r . k_i| <= 1.
 //
 // Measured for 2 x 32768 tokens, 16 / 32 heads of 128, as prepare + states + gradients:
 // 1.37 + 1.17 + 2.48 ms (0.35 + 0.28 + 0.65 ms for 15,928 packed tokens).  What they read
@@ -54,7 +54,7 @@ struct Rec {
   static constexpr size_t kS = kV + 2 * C * DV;        // image of S^T [DV][DK] before the chunk, in panels, columns by swap32
   static constexpr size_t kO = kS + 2 * DK * DV;       // image of dO [C][DV]
   static constexpr size_t kD = kO + 2 * C * DV;        // of dS'^T behind the chunk, alike
-  static constexpr size_t kW = kD + 2 * DK * DV;       // image of W 2^7 [C][DK], in panels, columns by swap32
+  static constexpr size_t kW = kD + 2 * DK * DV;       // image of W [C][DK], a factor a row, in panels, columns by swap32
   static constexpr size_t kOq = kW + 2 * C * DK;       // image of diag(qe) dO [C][DV], in panels
   static constexpr size_t kF = kOq + 2 * C * DV;       // floats from here:
   static constexpr int fGc = 0;                        // [C] gcum
@@ -62,7 +62,8 @@ struct Rec {
   static constexpr int fScal = fBeta + C;              // [8] see Scal
   static constexpr int fDV = fScal + 8;                // [DV] factor of every row of dV'^T
   static constexpr int fKw = fDV + DV;                 // [C] l_r / |k_r| in units of K16
-  static constexpr int kFloats = fKw + C;
+  static constexpr int fWr = fKw + C;                  // [C] factor of every row of W
+  static constexpr int kFloats = fWr + C;
   static constexpr size_t kBytes = kF + 4 * kFloats;
   static_assert(kBytes % 16 == 0 && fScal % 4 == 0 && fKw % 4 == 0, "16-byte copies");
 };
@@ -136,8 +137,8 @@ struct PrepSmem {
   static constexpr size_t kO = kV + 2 * C * VP;                         // fp16 [C][VP] dO
   static constexpr size_t kA = kO + 2 * C * VP;                         // fp32 [C][TP] A, then T
   static constexpr size_t kY = kA + 4 * C * TP;                         // fp32 [C / 2][TP] scratch of the inverse
-  static constexpr size_t kF = kY + 2 * C * TP;                         // fp32 [C] each: gc, beta, kf, qf, T's column factors of W
-  static constexpr size_t kQe = kF + 20 * C;                            // fp32 [C] e qf
+  static constexpr size_t kF = kY + 2 * C * TP;                         // fp32 [C] each: gc, beta, kf, qf, T's column and row factors of W
+  static constexpr size_t kQe = kF + 24 * C;                            // fp32 [C] e qf
   static constexpr size_t kTop = kQe + 4 * C;                           // fp32 [3][8] largest |v|, |dO|, |diag(qe) dO| by warp
   static constexpr size_t kBytes = kTop + 96;
   static_assert(kBytes <= 113 * 1024, "two blocks per SM");
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
   __half *K = reinterpret_cast<__half*>(sm + L::kK), *Q = reinterpret_cast<__half*>(sm + L::kQ);
   __half *TB = Q, *P = Q + C * HP, *V = reinterpret_cast<__half*>(sm + L::kV), *O = reinterpret_cast<__half*>(sm + L::kO);
   float *A = reinterpret_cast<float*>(sm + L::kA), *Y = reinterpret_cast<float*>(sm + L::kY);
-  float *gc = reinterpret_cast<float*>(sm + L::kF), *bt = gc + C, *kf = bt + C, *qf = kf + C, *wf = qf + C;
+  float *gc = reinterpret_cast<float*>(sm + L::kF), *bt = gc + C, *kf = bt + C, *qf = kf + C, *wf = qf + C, *wr_f = wf + C;
   float* qe = reinterpret_cast<float*>(sm + L::kQe);
   float* tops = reinterpret_cast<float*>(sm + L::kTop);
   uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
@@ -399,8 +400,14 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     if (tid >= 128 && tid < 128 + C) {  // while warps 0-3 substitute
       const int i = tid - 128;
       const float e = expf(gc[i]);
+      // Row r of W is b_r e_r k_r^T times a product of contractions, so b_r e_r bounds it, and T_ri b_i e_i is at most
+      // 2 b_r e_r: a factor a row keeps the digits of rows that lie any number of binades below the first.
       // 2^7 kf <= 1 (kf is at most 2^-7: the largest element of a row is at most its norm)
-      wf[i] = bt[i] * e * kf[i] * 0x1p13f;
+      float f, inv;
+      pow2_factor(bt[i] * e, f, inv);
+      wr_f[i] = f;
+      rf[R::fWr + i] = inv;
+      wf[i] = bt[i] * e * kf[i] * 0x1p6f;
       qe[i] = e * qf[i];
       rf[R::fGc + i] = gc[i];
       rf[R::fBeta + i] = bt[i];
@@ -429,10 +436,11 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     qtop = warp_top(qtop);
     if (lane == 0) tops[16 + warp] = qtop;
     __syncthreads();
-    {  // W 2^7 = (T diag(b e kf) 2^13) K16 2^-6: this warp's 16 rows, one half of the columns
+    {  // W over its rows' factors = (those T diag(b e kf) 2^6) K16 2^-6: this warp's 16 rows, one half of the columns
       constexpr int NT = DK / 16;
       float x[NT][4] = {};
       const int n0 = (DK / 2) * (warp >> 2);
+      const float fr[2] = {wr_f[r0], wr_f[r0 + 8]};
 #pragma unroll
       for (int k = 0; k < C; k += 16) {  // T's zeros above the diagonal are multiplied too: a branch would cost more
         uint32_t af[4];
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         for (int e = 0; e < 4; ++e) {
           const int r = r0 + 8 * (e & 1), i = k + 8 * (e >> 1) + 2 * t4;
           const float2 t = *reinterpret_cast<const float2*>(A + r * TP + i);
-          af[e] = pack2(t.x * wf[i], t.y * wf[i + 1]);
+          af[e] = pack2(t.x * fr[e & 1] * wf[i], t.y * fr[e & 1] * wf[i + 1]);
         }
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
@@ -521,12 +529,13 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
 // Dv) in two threads of warps w and w + 4, whose TMEM lanes it shares; a chunk is two products on the tensor cores with
 // M = 128 (Dv = 64 leaves half of the lanes unread):
 //   x^T = S^T W^T          then  S^T = e_last S^T + (V'^T diag(kw)) K                    forwards
-//   x^T = dS'^T K^T        then  dS^T = e_last dS'^T + (diag(qe) dO)^T Q - dV'^T W       backwards
-// Their A operands are what the gradients read as well (but for kw and qe), so they are written once to shared memory
-// and leave by bulk copies.  The tiles of a chunk come in two chunks ahead.  All columns of Dk are in the order of
-// swap32, which no product sees.  The state's image has one factor, joined over the
-// block, and so has the image of V', which is written while the second product runs; the products' own V' diag(kw) and
-// dV' keep one a row.
+//   x^T = dS'^T K^T        then  dS^T = e_last dS'^T + (diag(qe) dO)^T Q - (dV'^T diag(wr)) W   backwards
+// Their A operands are written to shared memory: S^T once, as the gradients read it, and V' diag(kw) and dV' diag(wr)
+// (wr: the factors of W's rows) over the U or Y that they were formed from.  Both vectors span any number of binades over
+// a chunk, and so may V' and dV', so these products have factors of their own, a row.  The images leave by bulk copies.
+// The tiles of a chunk come in two chunks ahead.  All columns of Dk are in the order of swap32, which no product sees.
+// The state's image has one factor, joined over the block, and so has the image of V'; that of dV' has one a row.  Both
+// are written while the second product runs.
 // A chunk waits for the one before it, and a thread issues an MMA every 90 to 130 cycles: so N is all of Dk, x is
 // two sums over half of Dk from two warps, and z = (diag(qe) dO)^T Q comes from a third (1.15 ms for 2 x 32768 tokens
 // and 32 heads of 128; 1.54 with one warp and N = 64, 1.51 with a ninth warp for all of them; 2.11 with warp MMAs).
@@ -537,14 +546,13 @@ template <int DK, int DV>
 struct StateSmem {  // from a 1024-byte boundary: tiles of the 128-byte swizzle
   static constexpr uint32_t kTile = 2 * C * DK, kRows = 2 * C * DV;
   static constexpr uint32_t oW = 0, oK = kTile, oU = 3 * kTile, oO = oU + kRows, oF = oO + kRows;  // a stage: W; K16, Q16; U or Y; Oq
-  static constexpr uint32_t kStage = oF + 1024;         // and kw [C], Scal [8]
+  static constexpr uint32_t kStage = oF + 1024;         // and kw [C], wr [C], Scal [8]
   static constexpr uint32_t kS = 2 * kStage;            // S^T, panels of 128 rows
   static constexpr uint32_t kV = kS + 2 * 128 * DK;     // V'^T [128][C]
-  static constexpr uint32_t kTop = kV + 2 * 128 * C;    // fp32 [2][8], [8] the warps' largest of the state and V'; [2][128] of a row's halves
-  static constexpr uint32_t kBar = kTop + 96 + 1024;    // five barriers
+  static constexpr uint32_t kTop = kV + 2 * 128 * C;    // fp32 [2][8], [8] the warps' largest of the state and V'; [2][128] pairs of a row's halves
+  static constexpr uint32_t kBar = kTop + 96 + 2048;    // five barriers
   static constexpr uint32_t kTmem = kBar + 48;
   static constexpr uint32_t kBytes = kTmem + 16 + 1024;
-  static constexpr uint32_t kKw = oO;                   // forwards: V'^T diag(kw) [128][C] where the first stage has no Oq
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -553,6 +561,15 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 }
 __device__ __forceinline__ uint4 pack8(const float* x, float f) {
   return make_uint4(pack2(x[0] * f, x[1] * f), pack2(x[2] * f, x[3] * f), pack2(x[4] * f, x[5] * f), pack2(x[6] * f, x[7] * f));
+}
+
+// The largest magnitude of N values, four at a time: one after another, each fmaxf would wait for the one before
+template <int N>
+__device__ __forceinline__ float top_of(const float (&x)[N]) {
+  float t[4] = {};
+#pragma unroll
+  for (int j = 0; j < N; ++j) t[j & 3] = fmaxf(t[j & 3], fabsf(x[j]));
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
 template <int DK, int DV, bool kBackward>
@@ -568,7 +585,8 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
   const bool active = 32 * (warp & 3) < DV;
   const int hq = h / (a.nv / a.nqk);
   const uint32_t base = ptx::smem_u32(sm);
-  float *tops = reinterpret_cast<float*>(sm + L::kTop), *vtops = tops + 16, *rtops = tops + 24;
+  float *tops = reinterpret_cast<float*>(sm + L::kTop), *vtops = tops + 16;
+  float2* rtops = reinterpret_cast<float2*>(tops + 24);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);     // a stage's copies (two), x, y, z
   int64_t start, end;
   seq_bounds(a, n, start, end);
@@ -592,21 +610,18 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     uint64_t* b = bar + (i & 1);
     const uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
     constexpr uint32_t tiles = (kBackward ? 2 : 1) * L::kTile;
-    ptx::mbar_arrive_expect_tx(b, L::kTile + tiles + (kBackward ? 2 : 1) * L::kRows + 4 * C + 32);
+    ptx::mbar_arrive_expect_tx(b, L::kTile + tiles + (kBackward ? 2 : 1) * L::kRows + 8 * C + 32);
     bulk_copy(st + L::oW, rec + R::kW, L::kTile, b);
     bulk_copy(st + L::oK, qk_at<DK, DV>(a, slot_of(i), hq) + QR::kK, tiles, b);  // Q16 stands behind K16
     bulk_copy(st + L::oU, rec + (kBackward ? R::kX : R::kV), L::kRows, b);
     if (kBackward) bulk_copy(st + L::oO, rec + R::kOq, L::kRows, b);
-    bulk_copy(st + L::oF, rec + R::kF + 4 * R::fKw, 4 * C, b);
-    bulk_copy(st + L::oF + 4 * C, rec + R::kF + 4 * R::fScal, 32, b);
+    bulk_copy(st + L::oF, rec + R::kF + 4 * R::fKw, 8 * C, b);  // and the factors of W behind it
+    bulk_copy(st + L::oF + 8 * C, rec + R::kF + 4 * R::fScal, 32, b);
   };
   // the largest element of the state over the block; also the barrier behind which a chunk's tiles are free
   auto join_top = [&](int64_t i, bool ok) {
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) top = fmaxf(top, fabsf(s[j]));
-    const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    if (lane == 0) tops[8 * (i & 1) + warp] = __uint_as_float(w);
+    const float top = warp_top(top_of(s));
+    if (lane == 0) tops[8 * (i & 1) + warp] = top;
     return __syncthreads_or(!ok);
   };
   if (tid == 0) {
@@ -632,11 +647,9 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     float* rf = reinterpret_cast<float*>(rec + R::kF);
     uint8_t* st = sm + (i & 1) * L::kStage;
     const uint32_t W = base + (uint32_t)(i & 1) * L::kStage + L::oW, K = W + L::oK, Q = K + L::kTile, Oq = W + L::oO;
-    const float *kw = reinterpret_cast<const float*>(st + L::oF), *scal = kw + C;
-    float top = 0.f, sfac, sinv;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, tops[8 * ((i + 1) & 1) + j]);
-    pow2_factor(top, sfac, sinv);
+    const float *kw = reinterpret_cast<const float*>(st + L::oF), *wr = kw + C, *scal = wr + C;
+    float sfac, sinv;
+    pow2_factor(top8(tops + 8 * ((i + 1) & 1)), sfac, sinv);
     if (active) {
 #pragma unroll
       for (int v = 0; v < NS / 8; ++v) {
@@ -672,11 +685,11 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       rf[R::fScal + (kBackward ? kScalD : kScalS)] = sinv;
     }
     const float us = scal[kBackward ? kScalY : kScalU], os = scal[kScalO], gl = scal[kScalGl];
-    // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw)
-    float x[32], w[32], vfac = 0.f, vinv = 0.f;
+    // forwards V'^T = U^T - x diag(wr), backwards dV'^T = Y^T + x diag(kw); then times the other of the two
+    float x[32], w[32], vtop = 0.f, pinv = 0.f;
     uint4 u[4];
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>(kw + 32 * half + j);
+    for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>((kBackward ? kw : wr) + 32 * half + j);
     if (active) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) u[t] = *reinterpret_cast<const uint4*>(st + L::oU + row + (((uint32_t)(4 * half + t) ^ sw) << 4));
@@ -688,50 +701,58 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       ptx::tmem_ld32(tl + 32 * half, x);
       ptx::tmem_ld32(tl + 64 + 32 * half, y);
       ptx::tmem_ld_wait();
-      float rtop = 0.f;
-      const float fx = kBackward ? sinv : -0x1p-7f * sinv;
+      float pfac;
+      const float fx = kBackward ? sinv : -sinv;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {  // columns j, j ^ 1 of this half stand in vector (j / 2) % 4, word j / 8
         const uint4& v = u[(j >> 1) & 3];
         const float2 u2 = unpack2(j < 8 ? v.x : j < 16 ? v.y : j < 24 ? v.z : v.w);
-        x[j] = fmaf(x[j] + y[j], kBackward ? fx * w[j] : fx, us * (j & 1 ? u2.y : u2.x));
-        rtop = fmaxf(rtop, fabsf(x[j]));
+        x[j] = fmaf(x[j] + y[j], fx * w[j], us * (j & 1 ? u2.y : u2.x));
       }
-      rtops[128 * half + c] = rtop;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>((kBackward ? wr : kw) + 32 * half + j);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] *= x[j];
+      const float ptop = top_of(w), xtop = top_of(x);
+      rtops[128 * half + c] = make_float2(ptop, xtop);
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");  // warps w and w + 4
-      pow2_factor(fmaxf(rtop, rtops[128 * (half ^ 1) + c]), vfac, vinv);
+      const float2 other = rtops[128 * (half ^ 1) + c];
+      pow2_factor(fmaxf(ptop, other.x), pfac, pinv);
       if constexpr (kBackward) {
-        if (half == 0) rf[R::fDV + c] = vinv;
+        vtop = fmaxf(xtop, other.y);
       } else {
-        rtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rtop)));
-        if (lane == 0) vtops[warp] = rtop;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = x[j] * (w[j] * 0x1p7f);  // kw 2^7 is at most 1
+        const float top = warp_top(xtop);
+        if (lane == 0) vtops[warp] = top;
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        *reinterpret_cast<uint4*>(sm + (kBackward ? L::kV : L::kKw) + row + (((uint32_t)(4 * half + t) ^ sw) << 4)) =
-            pack8((kBackward ? x : w) + 8 * t, vfac);
+      for (int t = 0; t < 4; ++t) *reinterpret_cast<uint4*>(st + L::oU + row + (((uint32_t)(4 * half + t) ^ sw) << 4)) = pack8(w + 8 * t, pfac);
     } else if (!kBackward && lane == 0) {
       vtops[warp] = 0.f;
     }
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
-    if (!kBackward && tid == 32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last chunk's V has left
+    if (tid == 32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // S, and the last chunk's V' or dV', have left
     __syncthreads();
     if (tid == 0) {
       ptx::tc_fence_after();
-      const uint32_t A = kBackward ? V : base + L::kKw, b = kBackward ? W : K;
+      const uint32_t b = kBackward ? W : K;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        ptx::mma_bf16(tmem + tY, ptx::sdesc_sw128(A + 32 * k, 16, 1024), ptx::sdesc_sw128(b + 2048 * k, 128 * C, 1024),
+        ptx::mma_bf16(tmem + tY, ptx::sdesc_sw128(W + L::oU + 32 * k, 16, 1024), ptx::sdesc_sw128(b + 2048 * k, 128 * C, 1024),
                       idesc_f16_f32(128, DK, false, true), k > 0);
       ptx::mma_commit(bar + 3);
-    } else if (kBackward && tid == 32) {
-      bulk_store(rec + R::kX, V, L::kRows);
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-    // what does not need y, meanwhile
+    // what does not need y, meanwhile: the image of V' or dV'
+    float vfac, vinv;
+    pow2_factor(kBackward ? vtop : top8(vtops), vfac, vinv);
+    if (!kBackward && tid == 32) rf[R::fScal + kScalV] = vinv;
+    if (active) {
+      if (kBackward && half == 0) rf[R::fDV + c] = vinv;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        *reinterpret_cast<uint4*>(sm + L::kV + row + (((uint32_t)(4 * half + t) ^ sw) << 4)) = pack8(x + 8 * t, vfac);
+    }
+    ptx::fence_proxy_async_smem();
     if constexpr (kBackward) {
       ok = ptx::mbar_wait_bounded(bar + 4, (uint32_t)(i & 1), kWaitLimitNs) && ok;
       ptx::tc_fence_after();
@@ -745,21 +766,10 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
         }
       }
     } else {
-      float vtop = 0.f, f, inv;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vtop = fmaxf(vtop, vtops[j]);
-      pow2_factor(vtop, f, inv);
-      if (tid == 32) rf[R::fScal + kScalV] = inv;
-      if (active) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          *reinterpret_cast<uint4*>(sm + L::kV + row + (((uint32_t)(4 * half + t) ^ sw) << 4)) = pack8(x + 8 * t, f);
-      }
-      ptx::fence_proxy_async_smem();
 #pragma unroll
       for (int j = 0; j < NS; ++j) s[j] *= gl;
     }
-    const float fy = vinv * (kBackward ? -0x1p-7f : 0x1p-7f);
+    const float fy = kBackward ? -pinv : pinv;
     ok = ptx::mbar_wait_bounded(bar + 3, (uint32_t)(i & 1), kWaitLimitNs) && ok;
     ptx::tc_fence_after();
     if (active) {
@@ -772,10 +782,9 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       }
     }
     ptx::tc_fence_before();
-    if (tid == 32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // S (and dV') may be written again
     quit = join_top(i, ok);
-    if (!kBackward && tid == 32) {
-      bulk_store(rec + R::kV, V, L::kRows);
+    if (tid == 32) {
+      bulk_store(rec + (kBackward ? R::kX : R::kV), V, L::kRows);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     if (quit) {  // a copy or a product never came: report it, wait once more for what is in flight, and leave
@@ -841,8 +850,8 @@ struct GradSmem {
   static constexpr size_t kB = kN + 2 * C * C;
   static constexpr size_t kK = kB + 2 * C * C;                // two of: K16, Q16 (columns by swap32) and their floats
   static constexpr size_t kKBytes = QkRec<DK>::kBytes;
-  static constexpr size_t kF = kK + 2 * kKBytes;              // two of: the record's floats
-  static constexpr size_t kFBytes = 4 * R::kFloats;
+  static constexpr size_t kF = kK + 2 * kKBytes;              // two of: the record's floats up to fWr
+  static constexpr size_t kFBytes = 4 * R::fWr;
   static constexpr size_t kE = kF + 2 * kFBytes;              // fp32 [C] e
   static constexpr size_t kRed = kE + 4 * C;                  // fp32 [3][4][C] rows' dots by column block
   static constexpr size_t kRedA = kRed + 48 * C;              // fp32 [6][C] row sums: through A and P (two halves: dgc, dbeta), dX V (two)
@@ -1441,12 +1450,12 @@ static cudaError_t launch_one(const BwdArgs& a, cudaStream_t stream) {
 int64_t chunk_bwd_half_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv) {
   if (total_tokens == 0) return 0;
   const int64_t c = bwdh::C, slots = total_tokens / c + num_seqs;
-  const int64_t rec = 2 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (3 * c + 8 + dv);
+  const int64_t rec = 2 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (4 * c + 8 + dv);
   return slots * (nv * rec + nqk * (4 * c * dk + 16 * c) + (int64_t)sizeof(bwdh::SlotInfo));
 }
 
 cudaError_t launch_chunk_bwd_half(const BwdArgs& a, int dk, int dv, cudaStream_t s) {
-  static_assert(bwdh::Rec<128, 64>::kBytes == 2 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (3 * 64 + 8 + 64), "workspace size");
+  static_assert(bwdh::Rec<128, 64>::kBytes == 2 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (4 * 64 + 8 + 64), "workspace size");
   static_assert(bwdh::QkRec<128>::kBytes == 4 * 64 * 128 + 16 * 64, "workspace size");
   if (dk == 64 && dv == 64) return bwdh::launch_one<64, 64>(a, s);
   if (dk == 64 && dv == 128) return bwdh::launch_one<64, 128>(a, s);

@@ -59,3 +59,50 @@ def test_output_gradients_reach_the_state_behind_a_strong_gate(gdn, io, kernel, 
     x["g"][starts(lens)] = first
     x["beta"].zero_()
     check(gdn, x, lens, io, kernel, ("ds0",))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("lens", [(1,), (40,), (64, 3)])
+@pytest.mark.parametrize("first", [-8.0, -12.0, -16.0, -30.0])
+def test_state_gradient_behind_a_strong_gate(gdn, io, kernel, lens, first):
+    x = make(lens, 1, 2, 128, 64, io, s0=True, ds=True)
+    x["g"][starts(lens)] = first
+    check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dbeta", "ds0"))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS[1:2])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
+@pytest.mark.parametrize("length,gate", [(64, -0.1), (64, -0.25), (64, -0.4), (64, -0.8), (130, -0.25), (130, -0.4)])
+def test_state_gradient_through_tokens_without_one(gdn, io, kernel, dk, dv, length, gate):
+    """dout = 0, as where a loss is masked: what comes from behind still has to pass all these tokens.  Their shares of it
+    are of one size, while the decays up to them differ by exp(gate * length)."""
+    lens = (length,)
+    x = make(lens, 1, 2, dk, dv, io, s0=True, ds=True)
+    x["g"][:] = gate
+    x["dout"].zero_()
+    check(gdn, x, lens, io, kernel, ("ds0",), by=-(-length // 64))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS[1:2])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
+@pytest.mark.parametrize("length,gate", [(64, -0.1), (64, -0.25), (64, -0.4), (64, -0.8), (128, -0.25), (128, -0.4)])
+def test_state_through_tokens_without_a_value(gdn, io, kernel, dk, dv, length, gate):
+    """The same forwards: v = 0, and the first token with a gradient reads what is left of the initial state."""
+    lens = (length + 6,)
+    x = make(lens, 1, 2, dk, dv, io, s0=True)
+    x["g"][:] = gate
+    x["v"].zero_()
+    x["dout"][:length] = 0
+    check(gdn, x, lens, io, kernel, ("dq",), by=-(-length // 64))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("last", [-8.0, -16.0, -30.0])
+def test_state_behind_a_strong_last_gate(gdn, io, kernel, last):
+    """What a chunk writes, decayed at its last token, which writes nothing itself; read by the next chunk's first."""
+    lens = (65,)
+    x = make(lens, 1, 2, 128, 128, io)
+    x["g"][63] = last
+    x["beta"][63:] = 0
+    x["dout"][:64] = 0
+    check(gdn, x, lens, io, kernel, ("dq",))
