@@ -139,12 +139,13 @@ struct Rec {
   static constexpr int fV = fD + DV;                   // [DV] of V'^T
   static constexpr int fDV = fV + DV;                  // [DV] of dV'^T
   static constexpr int fKw = fDV + DV;                 // [C] l_r over the factor of row r of K16
-  static constexpr int fOq = fKw + C;                  // [DV] factor of the rows of Oq
+  static constexpr int fWr = fKw + C;                  // [C] factor of the rows of W
+  static constexpr int fOq = fWr + C;                  // [DV] factor of the rows of Oq
   static constexpr int kFloats = fOq + DV;
   static constexpr size_t kBytes = kF + 4 * kFloats;
   static_assert(kBytes % 16 == 0 && fScal % 4 == 0 && fKw % 4 == 0, "16-byte copies");
 };
-enum Scal { kScalGl, kScalW, kScalT, kScalDo };  // e_last; factors of W, T, dO
+enum Scal { kScalGl, kScalT, kScalDo };  // e_last; factors of T, dO
 
 // One record per (chunk slot, qk-head), in bytes.
 template <int DK>
@@ -216,8 +217,8 @@ struct PrepSmem {
   static constexpr size_t kA = kO + 4 * C * DV;                     // fp32 [C][TP] A, then T
   static constexpr size_t kY = kA + 4 * C * TP;                     // fp32 [C / 2][TP] scratch of the inverse
   static constexpr size_t kF = kY + 2 * C * TP;                     // fp32 [C] each: gc, beta, kf, qf, beta e kf, s e qf
-  static constexpr size_t kTop = kF + 24 * C;                       // fp32 [4][16] largest elements by warp; [2][C] of rows
-  static constexpr size_t kBytes = kTop + 256 + 8 * C;
+  static constexpr size_t kTop = kF + 24 * C;                       // fp32 [4][16] largest elements by warp; [4][C] of rows
+  static constexpr size_t kBytes = kTop + 256 + 16 * C;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -481,10 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
     }
     __syncthreads();
     ln.again();
-    {  // W = T diag(b e) k_hat: this warp's 16 rows, a quarter of the columns; pairs under one factor for the tile
+    {  // W = T diag(b e) k_hat: this warp's 16 rows, a quarter of the columns; pairs under a factor for every row, since
+       // the rows fall with the decay up to their token, and the walk multiplies that out again
       constexpr int NT = DK / 32;
       const int n0 = (DK / 4) * (warp >> 2);
-      float t[4][2][4], top[2] = {0.f, 0.f}, f[2], inv[2], x[NT][4] = {}, wtop = 0.f, ws, winv;
+      float t[4][2][4], top[2] = {0.f, 0.f}, f[2], inv[2], x[NT][4] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -516,25 +518,34 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
           mma_pair(x[j + 1], ah, al, bh + 2, bl + 2);
         }
       }
+      top[0] = top[1] = 0.f;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[j][e] *= inv[e >> 1];
-          wtop = fmaxf(wtop, fabsf(x[j][e]));
+          top[e >> 1] = fmaxf(top[e >> 1], fabsf(x[j][e]));
         }
-      wtop = warp_top(wtop);
-      if (lane == 0) tops[48 + warp] = wtop;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+        if (ln.t == 0) rows[(warp >> 2) * C + wr + ln.g + 8 * e] = top[e];
+      }
       __syncthreads();
-      pow2_factor(top16(tops + 48, lane), ws, winv);
-      if (tid == 0) rf[R::fScal + kScalW] = winv;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = wr + ln.g + 8 * e;
+        pow2_factor(fmaxf(fmaxf(rows[r], rows[C + r]), fmaxf(rows[2 * C + r], rows[3 * C + r])), f[e], inv[e]);
+        if (warp < 4 && ln.t == 0) rf[R::fWr + r] = inv[e];
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint8_t* dst = rec + R::kW + pair_at<RK>(wr + ln.g + 8 * e, n0 + 8 * j + 2 * ln.t);
           uint32_t hi, lo;
-          pair2(x[j][2 * e], x[j][2 * e + 1], ws, hi, lo);
+          pair2(x[j][2 * e], x[j][2 * e + 1], f[e], hi, lo);
           *reinterpret_cast<uint32_t*>(dst) = hi;
           *reinterpret_cast<uint32_t*>(dst + 16 * RK) = lo;
         }
@@ -607,7 +618,7 @@ constexpr int kStateThreads = 64 * kStateSlices;
 template <int DK>
 struct StateSmem {
   static constexpr size_t kTile = 4 * C * DK;            // a pair image: W, K16 and (backwards) Q16
-  static constexpr size_t kStage = 3 * kTile + 4 * C;    // and kw
+  static constexpr size_t kStage = 3 * kTile + 8 * C;    // and kw, wr
   static constexpr size_t kX = 2 * kStage;               // float4 [8 warps][8][32] a warp's part of x
   static constexpr size_t kTop = kX + 8 * 4096;          // fp32 [2][8] the warps' largest of the state
   static constexpr size_t kBar = kTop + 64;
@@ -680,10 +691,10 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     uint8_t* st = sm + (i & 1) * L::kStage;
     const uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
     constexpr uint32_t tiles = (kBackward ? 2 : 1) * L::kTile;
-    ptx::mbar_arrive_expect_tx(bar + (i & 1), (uint32_t)(L::kTile + tiles + 4 * C));
+    ptx::mbar_arrive_expect_tx(bar + (i & 1), (uint32_t)(L::kTile + tiles + 8 * C));
     bulk_copy(st, rec + R::kW, L::kTile, bar + (i & 1));
     bulk_copy(st + L::kTile, qk_at<DK, DV>(a, slot_of(i), hq) + QR::kK, tiles, bar + (i & 1));  // Q16 stands behind K16
-    bulk_copy(st + 3 * L::kTile, rec + R::kF + 4 * R::fKw, 4 * C, bar + (i & 1));
+    bulk_copy(st + 3 * L::kTile, rec + R::kF + 4 * R::fKw, 8 * C, bar + (i & 1));  // and the factors of W behind it
   };
   if (tid == 0) {
     ptx::mbar_init(bar, 1);
@@ -708,7 +719,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
   for (int64_t i = 0; i < chunks; ++i) {
     uint8_t* rec = rec_at<DK, DV>(a, slot_of(i), h);
     float* rf = reinterpret_cast<float*>(rec + R::kF);
-    const float gl = rf[R::fScal + kScalGl], winv = rf[R::fScal + kScalW];
+    const float gl = rf[R::fScal + kScalGl];
     const float4* uw = reinterpret_cast<const float4*>(rec + (kBackward ? R::kX : R::kV)) + slice * 256 + lane;
     float4 u[8];
 #pragma unroll
@@ -726,7 +737,7 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
     const bool ok = ptx::mbar_wait_bounded(bar + (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs);
     const uint8_t* st = sm + (i & 1) * L::kStage;
     const uint32_t W = ptx::smem_u32(st), K = W + (uint32_t)L::kTile, Q = K + (uint32_t)L::kTile;
-    const float* kw = reinterpret_cast<const float*>(st + 3 * L::kTile);
+    const float *kw = reinterpret_cast<const float*>(st + 3 * L::kTile), *wr = kw + C;
     // x = S^T W^T (forwards) or dS'^T K^T (backwards), [16 x C]; the operand is also what the gradients read: two
     // steps of 16 columns are one vector a lane
     float x[8][4] = {};
@@ -757,13 +768,13 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
       x[j][2] += y.z;
       x[j][3] += y.w;
     }
-    // forwards V'^T = U^T - x, backwards dV'^T = Y^T + x diag(kw); stored over U^T, Y^T (these warps' 4 KB, read by both)
+    // forwards V'^T = U^T - x diag(wr), backwards dV'^T = Y^T + x diag(kw); stored over U^T, Y^T (these warps' 4 KB, read by both)
     top[0] = top[1] = 0.f;
     float vf[2], vinv[2];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 w = *reinterpret_cast<const float2*>(kw + 8 * j + 2 * t);
-      const float2 f = kBackward ? w : make_float2(-winv, -winv);
+      float2 f = *reinterpret_cast<const float2*>((kBackward ? kw : wr) + 8 * j + 2 * t);
+      if (!kBackward) f = make_float2(-f.x, -f.y);
       x[j][0] = fmaf(x[j][0] * sinv, f.x, u[j].x);
       x[j][1] = fmaf(x[j][1] * sinv, f.y, u[j].y);
       x[j][2] = fmaf(x[j][2] * sinv, f.x, u[j].z);
@@ -789,24 +800,23 @@ __device__ __forceinline__ void walk(const BwdArgs& a, uint8_t* sm, int n, int h
         *reinterpret_cast<uint32_t*>(dst + 16 * RC) = vl[k][e];
       }
     }
-    if (!kBackward) {  // the operand of the update is V' diag(kw), with factors of its own
-      top[0] = top[1] = 0.f;
+    // the operand of the update is V' diag(kw) or dV' diag(wr), with factors of its own
+    top[0] = top[1] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 w = *reinterpret_cast<const float2*>(kw + 8 * j + 2 * t);
-        x[j][0] *= w.x;
-        x[j][1] *= w.y;
-        x[j][2] *= w.x;
-        x[j][3] *= w.y;
-        top[0] = fmaxf(top[0], fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
-        top[1] = fmaxf(top[1], fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
-      }
-      row_factors(top, vf, vinv);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) pair_frag(x[2 * k], x[2 * k + 1], vf[0], vf[1], vh[k], vl[k]);
+    for (int j = 0; j < 8; ++j) {
+      const float2 w = *reinterpret_cast<const float2*>((kBackward ? wr : kw) + 8 * j + 2 * t);
+      x[j][0] *= w.x;
+      x[j][1] *= w.y;
+      x[j][2] *= w.x;
+      x[j][3] *= w.y;
+      top[0] = fmaxf(top[0], fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
+      top[1] = fmaxf(top[1], fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
     }
-    // forwards S^T = e_last S^T + (V' diag(kw))^T K, backwards dS^T = e_last dS'^T + (s diag(e) dO)^T Q - dV'^T W
-    const float f0 = kBackward ? -vinv[0] * winv : vinv[0], f1 = kBackward ? -vinv[1] * winv : vinv[1];
+    row_factors(top, vf, vinv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) pair_frag(x[2 * k], x[2 * k + 1], vf[0], vf[1], vh[k], vl[k]);
+    // forwards S^T = e_last S^T + (V' diag(kw))^T K, backwards dS^T = e_last dS'^T + (s diag(e) dO)^T Q - (dV' diag(wr))^T W
+    const float f0 = kBackward ? -vinv[0] : vinv[0], f1 = kBackward ? -vinv[1] : vinv[1];
     {
       float y[ND][4] = {};
 #pragma unroll
@@ -1438,12 +1448,12 @@ static cudaError_t launch_io(const BwdArgs& a, int io_bf16, cudaStream_t s) {
 
 int64_t chunk_bwd_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv) {
   if (total_tokens == 0) return 0;
-  const int64_t c = bwd::C, rec = 4 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (3 * c + 8 + 5 * dv);
+  const int64_t c = bwd::C, rec = 4 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (4 * c + 8 + 5 * dv);
   return (total_tokens / c + num_seqs) * (nv * rec + nqk * (16 * c * dk + 16 * c + 8 * c * c));
 }
 
 cudaError_t launch_chunk_bwd(const BwdArgs& a, int dk, int dv, int io_bf16, cudaStream_t s) {
-  static_assert(bwd::Rec<128, 64>::kBytes == 4 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (3 * 64 + 8 + 5 * 64), "workspace size");
+  static_assert(bwd::Rec<128, 64>::kBytes == 4 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (4 * 64 + 8 + 5 * 64), "workspace size");
   static_assert(bwd::QkRec<128>::kBytes == 16 * 64 * 128 + 16 * 64 + 8 * 64 * 64, "workspace size");
   if (dk == 64 && dv == 64) return bwd::launch_io<64, 64>(a, io_bf16, s);
   if (dk == 64 && dv == 128) return bwd::launch_io<64, 128>(a, io_bf16, s);

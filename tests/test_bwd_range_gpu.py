@@ -70,7 +70,7 @@ def test_state_gradient_behind_a_strong_gate(gdn, io, kernel, lens, first):
     check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dbeta", "ds0"))
 
 
-@pytest.mark.parametrize("io,kernel", PATHS[1:2])
+@pytest.mark.parametrize("io,kernel", PATHS)
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
 @pytest.mark.parametrize("length,gate", [(64, -0.1), (64, -0.25), (64, -0.4), (64, -0.8), (130, -0.25), (130, -0.4)])
 def test_state_gradient_through_tokens_without_one(gdn, io, kernel, dk, dv, length, gate):
@@ -83,7 +83,7 @@ def test_state_gradient_through_tokens_without_one(gdn, io, kernel, dk, dv, leng
     check(gdn, x, lens, io, kernel, ("ds0",), by=-(-length // 64))
 
 
-@pytest.mark.parametrize("io,kernel", PATHS[1:2])
+@pytest.mark.parametrize("io,kernel", PATHS)
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64)])
 @pytest.mark.parametrize("length,gate", [(64, -0.1), (64, -0.25), (64, -0.4), (64, -0.8), (128, -0.25), (128, -0.4)])
 def test_state_through_tokens_without_a_value(gdn, io, kernel, dk, dv, length, gate):
