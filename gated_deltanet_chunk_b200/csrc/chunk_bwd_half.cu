@@ -131,7 +131,7 @@ template <int DK, int DV>
 struct PrepSmem {
   static constexpr int DP = DK + 8, VP = DV + 8;
   static constexpr size_t kK = 0;                                       // fp16 [C][DP] K16
-  static constexpr size_t kQ = kK + 2 * C * DP;                         // fp16 [C][DP] Q16, then T beta 2^6 and P 2^8, [C][HP] each
+  static constexpr size_t kQ = kK + 2 * C * DP;                         // fp16 [C][DP] Q16, then T beta and P 2^8, [C][HP] each
   static constexpr size_t kQBytes = 2 * C * DP > 4 * C * HP ? 2 * C * DP : 4 * C * HP;
   static constexpr size_t kV = kQ + kQBytes;                            // fp16 [C][VP] V
   static constexpr size_t kO = kV + 2 * C * VP;                         // fp16 [C][VP] dO
@@ -139,8 +139,8 @@ struct PrepSmem {
   static constexpr size_t kY = kA + 4 * C * TP;                         // fp32 [C / 2][TP] scratch of the inverse
   static constexpr size_t kF = kY + 2 * C * TP;                         // fp32 [C] each: gc, beta, kf, qf, T's column and row factors of W
   static constexpr size_t kQe = kF + 24 * C;                            // fp32 [C] e qf
-  static constexpr size_t kTop = kQe + 4 * C;                           // fp32 [3][8] largest |v|, |dO|, |diag(qe) dO| by warp
-  static constexpr size_t kBytes = kTop + 96;
+  static constexpr size_t kTop = kQe + 4 * C;                           // fp32 [3][8] largest |v|, |dO|, |diag(qe) dO| by warp, [2] beta
+  static constexpr size_t kBytes = kTop + 112;
   static_assert(kBytes <= 113 * 1024, "two blocks per SM");
 };
 
@@ -371,6 +371,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     if (tid < C) {
       gc[tid] = gv;
       bt[tid] = bv;
+      const float top = warp_top(bv);
+      if (lane == 0) tops[24 + warp] = top;
     }
     __syncthreads();
     if (warp == 0) bwd::cumsum_chunk(gc, lane);
@@ -403,23 +405,28 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
       // Row r of W is b_r e_r k_r^T times a product of contractions, so b_r e_r bounds it, and T_ri b_i e_i is at most
       // 2 b_r e_r: a factor a row keeps the digits of rows that lie any number of binades below the first.
       // 2^7 kf <= 1 (kf is at most 2^-7: the largest element of a row is at most its norm)
-      float f, inv;
-      pow2_factor(bt[i] * e, f, inv);
-      wr_f[i] = f;
-      rf[R::fWr + i] = inv;
+      float wrow, winv;
+      pow2_factor(bt[i] * e, wrow, winv);
+      wr_f[i] = wrow;
+      rf[R::fWr + i] = winv;
       wf[i] = bt[i] * e * kf[i] * 0x1p6f;
       qe[i] = e * qf[i];
       rf[R::fGc + i] = gc[i];
       rf[R::fBeta + i] = bt[i];
       rf[R::fKw + i] = expf(gc[C - 1] - gc[i]) * kf[i];
       if (i == C - 1) {
-        rf[R::fScal + kScalU] = 2.f * vinv;
+        float f, inv;
+        pow2_factor(fmaxf(tops[24], tops[25]), f, inv);
+        rf[R::fScal + kScalU] = 0x1p8f * inv * vinv;
         rf[R::fScal + kScalY] = a.scale * oinv;
         rf[R::fScal + kScalGl] = e;
         rf[R::fScal + kScalDo] = oinv;
       }
     }
     bwd::invert_chunk<false>(A, Y, warp, lane);
+    float bs, binv;  // beta's factor: T beta is at most 2^8 times a half of it
+    pow2_factor(fmaxf(tops[24], tops[25]), bs, binv);
+    bs *= 0.5f;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         const int r = r0 + 4 * e, i = wc + 8 * j + 2 * t4;
         const float2 t = *reinterpret_cast<const float2*>(A + r * TP + i);
         *reinterpret_cast<uint32_t*>(P + r * HP + i) = pack2(p[j][e], p[j][e + 1]);
-        *reinterpret_cast<uint32_t*>(TB + r * HP + i) = pack2(t.x * bt[i] * 0x1p6f, t.y * bt[i + 1] * 0x1p6f);
+        *reinterpret_cast<uint32_t*>(TB + r * HP + i) = pack2(t.x * (bt[i] * bs), t.y * (bt[i + 1] * bs));
         *reinterpret_cast<uint32_t*>(rec + R::kT + image<2 * C>(r, i)) = pack2(t.x * 0x1p7f, t.y * 0x1p7f);
       }
     float qtop = 0.f;

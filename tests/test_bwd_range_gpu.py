@@ -106,3 +106,13 @@ def test_state_behind_a_strong_last_gate(gdn, io, kernel, last):
     x["beta"][63:] = 0
     x["dout"][:64] = 0
     check(gdn, x, lens, io, kernel, ("dq",))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("beta", [1e-4, 1e-8, 1e-16])
+def test_small_beta(gdn, io, kernel, beta):
+    """All writes small: what they leave in the outputs' gradients is as small, and as exact."""
+    lens = (100,)
+    x = make(lens, 1, 2, 128, 64, io)
+    x["beta"] = beta * (0.5 + 0.5 * x["beta"])
+    check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dg", "dbeta"))
