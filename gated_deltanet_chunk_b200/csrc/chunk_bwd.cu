@@ -131,8 +131,8 @@ struct Rec {
   static constexpr size_t kW = kO + 4 * C * DV;        // pair image of W [C][DK]
   static constexpr size_t kOq = kW + 4 * C * DK;       // (diag(qe) dO)^T as A fragments: hi, lo
   static constexpr size_t kF = kOq + 4 * C * DV;       // floats from here:
-  static constexpr int fGc = 0;                        // [C] gcum
-  static constexpr int fBeta = fGc + C;                // [C] beta
+  static constexpr int fGc = 0;                        // [C] gcum, and [C] what it has beyond fp32
+  static constexpr int fBeta = fGc + 2 * C;            // [C] beta
   static constexpr int fScal = fBeta + C;              // [8] see Scal
   static constexpr int fS = fScal + 8;                 // [DV] factor of every row of S^T (one for 64 rows)
   static constexpr int fD = fS + DV;                   // [DV] of dS'^T
@@ -204,6 +204,9 @@ __device__ __forceinline__ void pair8(const float (&v)[8], float f, uint4& hi, u
   pair2(v[6], v[7], f, hi.w, lo.w);
 }
 
+// exp(gcum_r - gcum_i) from [C] gcum and [C] its low part
+__device__ __forceinline__ float decay(const float* gc, int r, int i) { return expf((gc[r] - gc[i]) + (gc[C + r] - gc[C + i])); }
+
 // ------------------------------------------------------------------ 1. prepare
 // One block of 16 warps per (slot, qk-head): K16, Q16 and their products once, then its v-heads in turn.
 
@@ -216,8 +219,8 @@ struct PrepSmem {
   static constexpr size_t kO = kV + 4 * C * DV;                     // of dO, [C][64] for 64 columns at a time
   static constexpr size_t kA = kO + 4 * C * DV;                     // fp32 [C][TP] A, then T
   static constexpr size_t kY = kA + 4 * C * TP;                     // fp32 [C / 2][TP] scratch of the inverse
-  static constexpr size_t kF = kY + 2 * C * TP;                     // fp32 [C] each: gc, beta, kf, qf, beta e kf, s e qf
-  static constexpr size_t kTop = kF + 24 * C;                       // fp32 [4][16] largest elements by warp; [4][C] of rows
+  static constexpr size_t kF = kY + 2 * C * TP;                     // fp32 [C] each: gc, its low part, beta, kf, qf, beta e kf, s e qf
+  static constexpr size_t kTop = kF + 28 * C;                       // fp32 [4][16] largest elements by warp; [4][C] of rows
   static constexpr size_t kBytes = kTop + 256 + 16 * C;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
   const uint32_t base = ptx::smem_u32(sm);
   const uint32_t K = base + L::kK, Q = base + L::kQ, TB = Q, P = Q + 4 * C * C, V = base + L::kV, O = base + L::kO;
   float *A = reinterpret_cast<float*>(sm + L::kA), *Y = reinterpret_cast<float*>(sm + L::kY);
-  float *gc = reinterpret_cast<float*>(sm + L::kF), *bt = gc + C, *kf = bt + C, *qf = kf + C, *wf = qf + C, *qe = wf + C;
+  float *gc = reinterpret_cast<float*>(sm + L::kF), *gl = gc + C, *bt = gl + C, *kf = bt + C, *qf = kf + C, *wf = qf + C, *qe = wf + C;
   float *tops = reinterpret_cast<float*>(sm + L::kTop), *rows = tops + 64;
   uint8_t* qrec = qk_at<DK, DV>(a, slot, hq);
   float* qfl = reinterpret_cast<float*>(qrec + QR::kF);
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
       bt[tid] = bv;
     }
     __syncthreads();
-    if (warp == 0) cumsum_chunk(gc, lane);
+    if (warp == 0) cumsum_chunk(gc, gl, lane);
     float vs, vinv, os, oinv;
     pow2_factor(top16(tops, lane), vs, vinv);
     pow2_factor(top16(tops + 16, lane), os, oinv);
@@ -419,19 +422,20 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = r0 + 8 * (e >> 1), i = i0 + 8 * j + (e & 1);
-        const float gamma = i <= r ? expf(gc[r] - gc[i]) : 0.f;  // masked before exp
+        const float gamma = i <= r ? decay(gc, r, i) : 0.f;  // masked before exp
         A[r * TP + i] = i < r ? -bt[r] * (kk[j][e] * gamma) : 0.f;
         p[j][e] = i <= r ? a.scale * qk[j][e] * gamma : 0.f;
       }
     __syncthreads();
     if (tid >= 128 && tid < 128 + C) {  // while warps 0-3 substitute
       const int i = tid - 128;
-      const float e = expf(gc[i]);
+      const float e = expf(gc[i] + gl[i]);
       wf[i] = bt[i] * e * kf[i];
       qe[i] = a.scale * e * qf[i];
       rf[R::fGc + i] = gc[i];
+      rf[R::fGc + C + i] = gl[i];
       rf[R::fBeta + i] = bt[i];
-      rf[R::fKw + i] = expf(gc[C - 1] - gc[i]) * kf[i];
+      rf[R::fKw + i] = decay(gc, C - 1, i) * kf[i];
       if (i == C - 1) {
         rf[R::fScal + kScalGl] = e;
         rf[R::fScal + kScalDo] = oinv;
@@ -1118,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = m0 + 16 * m + 8 * e + ln.g;
-              f[m][e] = a.scale * expf(gc[r]) * qf[r] * oinv * mS;
+              f[m][e] = a.scale * expf(gc[r] + gc[C + r]) * qf[r] * oinv * mS;
             }
           take<NT, RK>(x, Q, m0, n0, f, sum, dot, ln);
         }
@@ -1166,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = m0 + 16 * m + 8 * e + ln.g;
-              f[m][e] = expf(gc[C - 1] - gc[r]) * kf[r] * mV * mD;
+              f[m][e] = decay(gc, C - 1, r) * kf[r] * mV * mD;
             }
           take<NT, RK>(x, K, m0, n0, f, sum, dot, ln);
         }
@@ -1184,7 +1188,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int r = m0 + 16 * m + 8 * e + ln.g;
-              u[m][e] = -expf(gc[r]) * kf[r] * mX * mS;
+              u[m][e] = -expf(gc[r] + gc[C + r]) * kf[r] * mX * mS;
               f[m][e] = rf[R::fBeta + r] * u[m][e];
             }
           take<NT, RK>(x, K, m0, n0, f, sum, dot, ln);
@@ -1234,7 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 1) grads_kernel(BwdArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = r0 + 8 * (e >> 1), i = i0 + 8 * j + (e & 1);
-            const float gamma = i <= r ? expf(gc[r] - gc[i]) : 0.f, strict = i < r ? gamma : 0.f;  // masked before exp
+            const float gamma = i <= r ? decay(gc, r, i) : 0.f, strict = i < r ? gamma : 0.f;  // masked before exp
             const float da = sA * dA[j][e], dp = a.scale * sP * dP[j][e];
             const float fk = kf[r] * kf[i], fq = qf[r] * kf[i];
             const float akd = da * (kk[e] * strict);
@@ -1448,12 +1452,12 @@ static cudaError_t launch_io(const BwdArgs& a, int io_bf16, cudaStream_t s) {
 
 int64_t chunk_bwd_workspace(int64_t total_tokens, int num_seqs, int nqk, int nv, int dk, int dv) {
   if (total_tokens == 0) return 0;
-  const int64_t c = bwd::C, rec = 4 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (4 * c + 8 + 5 * dv);
+  const int64_t c = bwd::C, rec = 4 * (c * (c + dk + 4 * dv) + 2 * (int64_t)dk * dv) + 4 * (5 * c + 8 + 5 * dv);
   return (total_tokens / c + num_seqs) * (nv * rec + nqk * (16 * c * dk + 16 * c + 8 * c * c));
 }
 
 cudaError_t launch_chunk_bwd(const BwdArgs& a, int dk, int dv, int io_bf16, cudaStream_t s) {
-  static_assert(bwd::Rec<128, 64>::kBytes == 4 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (4 * 64 + 8 + 5 * 64), "workspace size");
+  static_assert(bwd::Rec<128, 64>::kBytes == 4 * (64 * (64 + 128 + 4 * 64) + 2 * 128 * 64) + 4 * (5 * 64 + 8 + 5 * 64), "workspace size");
   static_assert(bwd::QkRec<128>::kBytes == 16 * 64 * 128 + 16 * 64 + 8 * 64 * 64, "workspace size");
   if (dk == 64 && dv == 64) return bwd::launch_io<64, 64>(a, io_bf16, s);
   if (dk == 64 && dv == 128) return bwd::launch_io<64, 128>(a, io_bf16, s);

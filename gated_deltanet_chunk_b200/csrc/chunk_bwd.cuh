@@ -92,6 +92,10 @@ __device__ __forceinline__ void warp_gemm(float (&acc)[NT][4], int k0, int k1, F
   }
 }
 
+// A gate below this decays to 0 in fp32, as this one does (exp(-105) < 2^-150).  It is raised to it, so that sums of gates
+// stay where their differences keep digits: a token's decay from the ones behind a reset must not depend on the reset.
+constexpr float kGateFloor = -105.f;
+
 // In-chunk inclusive cumsum of x[0..C) by one warp.
 __device__ __forceinline__ void cumsum_chunk(float* x, int lane) {
   const float x0 = x[2 * lane], x1 = x[2 * lane + 1];
@@ -105,6 +109,34 @@ __device__ __forceinline__ void cumsum_chunk(float* x, int lane) {
   if (lane == 0) excl = 0.f;
   x[2 * lane] = excl + x0;
   x[2 * lane + 1] = excl + x0 + x1;
+}
+// hi + lo += x + y, without a rounding but lo's
+__device__ __forceinline__ void add_pair(float& hi, float& lo, float x, float y) {
+  const float s = hi + x, b = s - hi;
+  lo += y + ((hi - (s - b)) + (x - b));
+  hi = s;
+}
+// The same as a pair hi + lo, so that differences are exact to fp32 however large the sums; gates of either sign: what the
+// chunk's positive ones add up to lowers the floor.
+__device__ __forceinline__ void cumsum_chunk(float* x, float* low, int lane) {
+  float x0 = x[2 * lane], x1 = x[2 * lane + 1];
+  const float least = kGateFloor - warp_sum(fmaxf(x0, 0.f) + fmaxf(x1, 0.f));
+  x0 = x0 < least ? least : x0;
+  x1 = x1 < least ? least : x1;
+  float hi = x0, lo = 0.f;
+  add_pair(hi, lo, x1, 0.f);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_up_sync(0xffffffffu, hi, o), z = __shfl_up_sync(0xffffffffu, lo, o);
+    if (lane >= o) add_pair(hi, lo, y, z);
+  }
+  float eh = __shfl_up_sync(0xffffffffu, hi, 1), el = __shfl_up_sync(0xffffffffu, lo, 1);
+  if (lane == 0) eh = el = 0.f;
+  add_pair(eh, el, x0, 0.f);
+  x[2 * lane] = eh;
+  low[2 * lane] = el;
+  x[2 * lane + 1] = hi;
+  low[2 * lane + 1] = lo;
 }
 
 // T = (I - A)^-1 over A (strictly lower, pitch TP), as in chunk_simt.cu: 16 x 16

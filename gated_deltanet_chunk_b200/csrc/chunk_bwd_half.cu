@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     if (tid < C && c0 + tid < end) {
       load_gate(a, (size_t)(c0 + tid) * a.nv + h, h, gv, bv);
       if (!(gv <= 0.f) || !(bv >= 0.f && bv <= 2.f)) report_status(a.status, kStatusGate);
+      gv = gv < kGateFloor ? kGateFloor : gv;
     }
     __syncthreads();  // the head before is done with the tiles
     if (lane == 0) {
@@ -1156,7 +1157,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            gr[e] = kLog2e * gc[r0 + 8 * e];
+            gr[e] = gc[r0 + 8 * e];
             br[e] = -bt[r0 + 8 * e];
             qr[e] = qf[r0 + 8 * e] * 0x1p6f;    // 2^14 for the factors, 2^-8
             kr[e] = kf[r0 + 8 * e] * 0x1p-2f;   // 2^14, 2^-16
@@ -1177,8 +1178,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
               float nn[2], bb[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                // masked before exp; the strict triangle for A
-                const float gamma = i + e <= r ? ptx::ex2_approx(fmaf(-kLog2e, e ? gi[j].y : gi[j].x, gr[e2])) : 0.f;
+                // masked before exp, and the difference before the factor: 1 on the diagonal; the strict triangle for A
+                const float gamma = i + e <= r ? ptx::ex2_approx(kLog2e * (gr[e2] - (e ? gi[j].y : gi[j].x))) : 0.f;
                 const float strict = i + e < r ? gamma : 0.f, kc = e ? ki[j].y : ki[j].x;
                 const float dp = dP[j][2 * e2 + e], da = dA[j][2 * e2 + e];
                 const float akd = sA * da * ((e ? kd2.y : kd2.x) * strict);

@@ -116,3 +116,35 @@ def test_small_beta(gdn, io, kernel, beta):
     x = make(lens, 1, 2, 128, 64, io)
     x["beta"] = beta * (0.5 + 0.5 * x["beta"])
     check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("gate", [-100.0, -1e3, -1e4, -1e6, -3.4e38, -float("inf")])
+def test_gates_that_reset_the_state(gdn, io, kernel, gate):
+    """The tokens behind a reset keep their decays among themselves, whatever the gate that did it."""
+    lens = (100,)
+    x = make(lens, 1, 2, 64, 64, io, s0=True, ds=True)
+    for t in (5, 20, 21, 60):
+        x["g"][t] = gate
+    check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("gate", [-1e3, -1e6, -3.4e38, -float("inf")])
+def test_gates_that_all_reset_the_state(gdn, io, kernel, gate):
+    """Every token by itself."""
+    lens = (70,)
+    x = make(lens, 1, 2, 64, 64, io, s0=True, ds=True)
+    x["g"][:] = gate
+    check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dbeta"))
+
+
+@pytest.mark.parametrize("io,kernel", [PATHS[0], PATHS[2]])
+def test_resets_among_growing_gates(gdn, io, kernel):
+    """Gates of both signs: what grows behind a reset does not bring back what it took."""
+    lens = (60,)
+    x = make(lens, 1, 2, 64, 64, io, s0=True, ds=True)
+    x["g"] = 0.5 * torch.rand(x["g"].shape, generator=torch.Generator().manual_seed(3))
+    x["beta"] = 1 + 0.0 * x["beta"]
+    x["g"][20], x["g"][40] = -300.0, -1e5
+    check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dg", "dbeta"))
