@@ -1339,30 +1339,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
             for (int e = 0; e < 4; ++e) sum[m][j][e] = fmaf(sB, x[m][j][e], sum[m][j][e]);
       }
       if (warp == 0) {
-        // dgc of rows 2 lane, 2 lane + 1; then the suffix sums
+        // dgc of rows 2 lane, 2 lane + 1; then the suffix sums.  l_r k_r . (V' dS'^T)_r is taken from dgc_r and added to the
+        // last row: in dg_t only the rows before t are left of it, and are added as such, since the difference of the two
+        // sums would have no digits where a chunk's own decay is small beside it (one token behind a strong gate).
         auto four = [&](int m, int r) { return (red[(4 * m) * C + r] + red[(4 * m + 1) * C + r]) + (red[(4 * m + 2) * C + r] + red[(4 * m + 3) * C + r]); };
-        float d[2], th = 0.f, bsum[2];
+        float d[2], th[2], bsum[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = 2 * lane + e;
-          const float through = four(1, r), u = four(2, r);
+          const float u = four(2, r);
           const float cols = (col[r] + col[C + r]) + (col[2 * C + r] + col[3 * C + r]);
-          th += through;
-          d[e] = (reda[r] + reda[2 * C + r]) + four(0, r) + rf[R::fBeta + r] * u - through - cols;
+          th[e] = four(1, r);
+          d[e] = (reda[r] + reda[2 * C + r]) + four(0, r) + rf[R::fBeta + r] * u - cols;
           bsum[e] = (reda[C + r] + reda[3 * C + r]) + (reda[4 * C + r] + reda[5 * C + r]) + u;
         }
-        th = warp_sum(th);
-        const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f);
-        if (lane == 31) d[1] += th + rf[R::fScal + kScalGl] * dsum;
-        float suf = d[0] + d[1];
+        const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f) * rf[R::fScal + kScalGl];
+        float suf = d[0] + d[1], pre = th[0] + th[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const float y = __shfl_down_sync(0xffffffffu, suf, o);
+          const float y = __shfl_down_sync(0xffffffffu, suf, o), z = __shfl_up_sync(0xffffffffu, pre, o);
           if (lane + o < 32) suf += y;
+          if (lane >= o) pre += z;
         }
-        float beyond = __shfl_down_sync(0xffffffffu, suf, 1);
+        float beyond = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
         if (lane == 31) beyond = 0.f;
-        const float dg[2] = {suf, beyond + d[1]};
+        if (lane == 0) before = 0.f;
+        const float dg[2] = {suf + (before + dsum), beyond + d[1] + (before + th[0] + dsum)};
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (2 * lane + e < rows) {

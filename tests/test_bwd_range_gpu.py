@@ -148,3 +148,17 @@ def test_resets_among_growing_gates(gdn, io, kernel):
     x["beta"] = 1 + 0.0 * x["beta"]
     x["g"][20], x["g"][40] = -300.0, -1e5
     check(gdn, x, lens, io, kernel, ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("gate", [-1.0, -8.0, -16.0, -30.0])
+@pytest.mark.parametrize("length", [1, 2])
+def test_gate_gradients_of_short_sequences_behind_strong_gates(gdn, io, kernel, gate, length):
+    """dg is what passes through the gate, exp(gate) of what the token itself does.  The last tokens of the sequences, each
+    behind one gate, are held to the largest of theirs."""
+    lens = (length,) * 5
+    x = make(lens, 1, 2, 64, 64, io, s0=True, ds=True)
+    x["g"][:] = gate
+    got = run(gdn, x, lens, kernel=kernel)[3]
+    want = G.rule_grads(x["q"], x["k"], x["v"], x["g"], x["beta"], x["s0"], x["dout"], x["ds"], lens)[3]
+    close("dg", got[length - 1::length], want[length - 1::length], io, kernel)
