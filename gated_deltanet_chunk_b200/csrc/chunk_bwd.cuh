@@ -55,40 +55,25 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   lo = ptx::to_tf32(x - __uint_as_float(hi));
 }
 
-// acc += a b with both operands' hi and lo parts; an operand known to be exact in TF32 has no lo part.
-template <bool XA, bool XB>
-__device__ __forceinline__ void mma3(float* acc, const uint32_t* ah, const uint32_t* al, const uint32_t* bh,
-                                     const uint32_t* bl) {
-  if constexpr (!XA) ptx::mma_tf32_16x8x8(acc, al, bh);
-  if constexpr (!XB) ptx::mma_tf32_16x8x8(acc, ah, bl);
-  ptx::mma_tf32_16x8x8(acc, ah, bh);
-}
-
-// acc[NT] (16 x 8 tiles: a 16 x 8 NT block) += A[16 x K] B[K x 8 NT] over k in [k0, k1), one warp;
-// a(m, k) and b(k, n) read the operands' elements.  kPairs = false: operands rounded to TF32 once, one MMA.
-template <int NT, bool kPairs = true, typename FA, typename FB>
-__device__ __forceinline__ void warp_gemm(float (&acc)[NT][4], int k0, int k1, FA a, FB b, int g, int t) {
+// acc (a 16 x 8 tile) += A[16 x K] B[K x 8] over k in [k0, k1), one warp; a(m, k) and b(k, n) read the operands'
+// elements, which are split into hi + lo: three MMAs, whose 8 terms are added in fp32, since an MMA truncates as it adds.
+template <typename FA, typename FB>
+__device__ __forceinline__ void warp_gemm(float (&acc)[4], int k0, int k1, FA a, FB b, int g, int t) {
 #pragma unroll 2
   for (int kk = k0; kk < k1; kk += 8) {
-    uint32_t ah[4], al[4];
+    uint32_t ah[4], al[4], bh[2], bl[2];
     split_tf32(a(g, kk + t), ah[0], al[0]);
     split_tf32(a(g + 8, kk + t), ah[1], al[1]);
     split_tf32(a(g, kk + t + 4), ah[2], al[2]);
     split_tf32(a(g + 8, kk + t + 4), ah[3], al[3]);
+    split_tf32(b(kk + t, g), bh[0], bl[0]);
+    split_tf32(b(kk + t + 4, g), bh[1], bl[1]);
+    float d[4] = {}, e[4] = {};
+    ptx::mma_tf32_16x8x8(e, al, bh);
+    ptx::mma_tf32_16x8x8(d, ah, bh);
+    ptx::mma_tf32_16x8x8(e, ah, bl);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      uint32_t bh[2], bl[2];
-      split_tf32(b(kk + t, 8 * j + g), bh[0], bl[0]);
-      split_tf32(b(kk + t + 4, 8 * j + g), bh[1], bl[1]);
-      if constexpr (kPairs) {  // the MMA truncates as it adds: only its 8 terms are its own
-        float d[4] = {};
-        mma3<false, false>(d, ah, al, bh, bl);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
-      } else {
-        mma3<true, true>(acc[j], ah, al, bh, bl);
-      }
-    }
+    for (int i = 0; i < 4; ++i) acc[i] += d[i] + e[i];
   }
 }
 
@@ -143,7 +128,6 @@ __device__ __forceinline__ void cumsum_chunk(float* x, float* low, int lane) {
 // diagonal blocks by forward substitution in fp32 (a warp per block, a column
 // per lane), then T10 = T11 A10 T00 for blocks of 16 and of 32.  Y: [C / 2][TP]
 // scratch.  Zeros above the diagonal are written; the unit diagonal is stored.
-template <bool kPairs>
 __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int lane) {
   if (warp < C / 16 && lane < 16) {
     float* blk = A + (16 * warp) * TP + 16 * warp;
@@ -165,32 +149,24 @@ __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int l
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int s = 16; s < C; s *= 2) {
-    const int nb = s / 16, nunit = (C / (2 * s)) * nb * nb;  // 16 x 16 blocks of all T10 of this size
-    const int p = warp / (nb * nb), rb = (warp / nb) % nb, cb = warp % nb, base = 2 * s * p;
+    const int nb = s / 16, nunit = (C / (2 * s)) * nb * nb * 2;  // 16 x 8 blocks of all T10 of this size
+    const int u = warp / 2, p = u / (nb * nb), rb = (u / nb) % nb, c0 = 16 * (u % nb) + 8 * (warp & 1), base = 2 * s * p;
     if (warp < nunit) {  // Y = A10 T00
       const float* a10 = A + (base + s + 16 * rb) * TP + base;
-      const float* t00 = A + base * TP + base + 16 * cb;
-      float acc[2][4] = {};
-      warp_gemm<2, kPairs>(acc, 16 * cb, s, [&](int m, int k) { return a10[m * TP + k]; },
-                   [&](int k, int n) { return t00[k * TP + n]; }, g, t);
+      const float* t00 = A + base * TP + base + c0;
+      float acc[4] = {};
+      warp_gemm(acc, c0, s, [&](int m, int k) { return a10[m * TP + k]; }, [&](int k, int n) { return t00[k * TP + n]; }, g, t);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          Y[(p * s + 16 * rb + g + 8 * (e >> 1)) * TP + 16 * cb + 8 * j + 2 * t + (e & 1)] = acc[j][e];
+      for (int e = 0; e < 4; ++e) Y[(p * s + 16 * rb + g + 8 * (e >> 1)) * TP + c0 + 2 * t + (e & 1)] = acc[e];
     }
     __syncthreads();
     if (warp < nunit) {  // T10 = T11 Y
       const float* t11 = A + (base + s + 16 * rb) * TP + base + s;
-      const float* yp = Y + p * s * TP + 16 * cb;
-      float acc[2][4] = {};
-      warp_gemm<2, kPairs>(acc, 0, 16 * rb + 16, [&](int m, int k) { return t11[m * TP + k]; },
-                   [&](int k, int n) { return yp[k * TP + n]; }, g, t);
+      const float* yp = Y + p * s * TP + c0;
+      float acc[4] = {};
+      warp_gemm(acc, 0, 16 * rb + 16, [&](int m, int k) { return t11[m * TP + k]; }, [&](int k, int n) { return yp[k * TP + n]; }, g, t);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          A[(base + s + 16 * rb + g + 8 * (e >> 1)) * TP + base + 16 * cb + 8 * j + 2 * t + (e & 1)] = acc[j][e];
+      for (int e = 0; e < 4; ++e) A[(base + s + 16 * rb + g + 8 * (e >> 1)) * TP + base + c0 + 2 * t + (e & 1)] = acc[e];
     }
     __syncthreads();
   }

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         rf[R::fScal + kScalDo] = oinv;
       }
     }
-    bwd::invert_chunk<false>(A, Y, warp, lane);
+    bwd::invert_chunk(A, Y, warp, lane);
     float bs, binv;  // beta's factor: T beta is at most 2^8 times a half of it
     pow2_factor(fmaxf(tops[24], tops[25]), bs, binv);
     bs *= 0.5f;
@@ -444,26 +444,32 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
     qtop = warp_top(qtop);
     if (lane == 0) tops[16 + warp] = qtop;
     __syncthreads();
-    {  // W over its rows' factors = (those T diag(b e kf) 2^6) K16 2^-6: this warp's 16 rows, one half of the columns
+    {  // W over its rows' factors = (those T diag(b e kf) 2^6) K16 2^-6: this warp's 16 rows, one half of the columns.  Where
+       // keys repeat, the terms of a row cancel, so the first operand is a pair hi + lo (K16 is exact)
       constexpr int NT = DK / 16;
       float x[NT][4] = {};
       const int n0 = (DK / 2) * (warp >> 2);
       const float fr[2] = {wr_f[r0], wr_f[r0 + 8]};
 #pragma unroll
       for (int k = 0; k < C; k += 16) {  // T's zeros above the diagonal are multiplied too: a branch would cost more
-        uint32_t af[4];
+        uint32_t ah[4], al[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = r0 + 8 * (e & 1), i = k + 8 * (e >> 1) + 2 * t4;
           const float2 t = *reinterpret_cast<const float2*>(A + r * TP + i);
-          af[e] = pack2(t.x * fr[e & 1] * wf[i], t.y * fr[e & 1] * wf[i + 1]);
+          const float p0 = t.x * fr[e & 1] * wf[i], p1 = t.y * fr[e & 1] * wf[i + 1];
+          ah[e] = pack2(p0, p1);
+          const float2 h = unpack2(ah[e]);
+          al[e] = pack2(p0 - h.x, p1 - h.y);
         }
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
           uint32_t b[4];
           frag_b_t<L::DP>(b, K, n0 + 8 * j, k, lane);
-          mma_f16(x[j], af, b);
-          mma_f16(x[j + 1], af, b + 2);
+          mma_f16(x[j], al, b);
+          mma_f16(x[j + 1], al, b + 2);
+          mma_f16(x[j], ah, b);
+          mma_f16(x[j + 1], ah, b + 2);
         }
       }
 #pragma unroll

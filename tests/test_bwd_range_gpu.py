@@ -2,9 +2,9 @@
 value or a gradient, small or large beta, keys that repeat.  Every head is held to its own largest element, against 64-bit
 autograd of the token recurrence.
 
-Tolerances.  bf16 tensors: a path from the inputs to a gradient takes at most four operands that are rounded to fp16, by
-half a step, 2^-11 of the value, each: 4 * 2^-11 = 2^-9 of the largest element, and the rounding of a bf16 output, 2^-8 of the
-element.  fp32, and bf16 with kernel="simt": operands within 2^-22, sums of at most 128 terms in fp32 (2^-24 sqrt(128) < 2^-20),
+Tolerances.  bf16 tensors: a path from the inputs to a gradient takes at most eleven operands that are rounded to fp16 (five
+to V', six to dX), by half a step, 2^-11 of the value, each.  The roundings are independent: sqrt(11) * 2^-11 < 2^-9 of the
+largest element, and the rounding of a bf16 output, 2^-8 of the element.  fp32, and bf16 with kernel="simt": operands within 2^-22, sums of at most 128 terms in fp32 (2^-24 sqrt(128) < 2^-20),
 at most about 16 such products: 16 * 2^-20 = 2^-16 of the largest element.
 """
 import pytest
@@ -162,3 +162,23 @@ def test_gate_gradients_of_short_sequences_behind_strong_gates(gdn, io, kernel, 
     got = run(gdn, x, lens, kernel=kernel)[3]
     want = G.rule_grads(x["q"], x["k"], x["v"], x["g"], x["beta"], x["s0"], x["dout"], x["ds"], lens)[3]
     close("dg", got[length - 1::length], want[length - 1::length], io, kernel)
+
+
+def near(kind, lo, hi, dk, io):
+    """Keys that repeat through the sequence, or all but, and beta in [lo, hi]; nothing decays."""
+    x = make((128,), 8, 8, dk, dk, io, s0=True, ds=True, decay="none", seed=11)
+    k = x["k"][:1].expand_as(x["k"])
+    x["k"] = (k if kind == "repeated" else (k.float() + 0.1 * x["k"].float()).to(io)).contiguous()
+    x["beta"] = lo + (hi - lo) * x["beta"]
+    return x
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("kind", ["repeated", "near"])
+@pytest.mark.parametrize("lo,hi,by", [(0.0, 1.0, 2), (0.9, 1.0, 2), (1.0, 2.0, 5), (1.8, 2.0, 16), (2.0, 2.0, 16)])
+def test_keys_that_repeat(gdn, io, kernel, dk, kind, lo, hi, by):
+    """T_ri = -beta_r prod (1 - beta_m) between them, so what a product with T takes shows as often as its rows' magnitudes
+    sum to: 1 + 1 where beta <= 1; 1 + 2 (1 + 1/2 + 1/4 + ...) = 5 for beta evenly in [1, 2]; and where nothing falls off,
+    64 independent roundings of entries of 2: 2 sqrt(64)."""
+    check(gdn, near(kind, lo, hi, dk, io), (128,), io, kernel, ("dq", "dk", "dv", "ds0"), by=by)
