@@ -868,8 +868,8 @@ struct GradSmem {
   static constexpr size_t kFBytes = 4 * R::fWr;
   static constexpr size_t kE = kF + 2 * kFBytes;              // fp32 [C] e
   static constexpr size_t kRed = kE + 4 * C;                  // fp32 [3][4][C] rows' dots by column block
-  static constexpr size_t kRedA = kRed + 48 * C;              // fp32 [6][C] row sums: through A and P (two halves: dgc, dbeta), dX V (two)
-  static constexpr size_t kCol = kRedA + 24 * C;              // fp32 [4][C] column sums by row block
+  static constexpr size_t kRedA = kRed + 48 * C;              // fp32 [7][C] row sums: through A and P (two halves: dgc, dbeta), dX V (two); dX V'
+  static constexpr size_t kCol = kRedA + 28 * C;              // fp32 [4][C] column sums by row block
   static constexpr size_t kDot = kCol + 16 * C;               // fp32 [16] <S, dS'> by warp
   static constexpr size_t kBar = kDot + 64;                   // barriers: X, V, S, K16 and Q16 (two)
   static constexpr size_t kBytes = kBar + 40;
@@ -1151,6 +1151,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
               mma_f16(dP[j], ao, b + 2 * j);
             }
           }
+          if ((w8 & 3) >> 1 == w8 >> 2 && ln.t == ln.g >> 1) {  // the diagonal: dX_r . V'_r of rows r0 and r0 + 8
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x0 = w8 & 1 ? dA[2 + e][2 * e] : dA[e][2 * e], x1 = w8 & 1 ? dA[2 + e][2 * e + 1] : dA[e][2 * e + 1];
+              reda[6 * C + r0 + 8 * e] = sA * (ln.g & 1 ? x1 : x0);
+            }
+          }
           // ---- 3. what goes through A and P
           const float *gc = rf + R::fGc, *bt = rf + R::fBeta;
           float s_gc[2] = {0.f, 0.f}, s_bt[2] = {0.f, 0.f}, gr[2], br[2], qr[2], kr[2], cs[8];
@@ -1344,40 +1351,39 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[m][j][e] = fmaf(sB, x[m][j][e], sum[m][j][e]);
       }
-      if (warp == 0) {
-        // dgc of rows 2 lane, 2 lane + 1; then the suffix sums.  l_r k_r . (V' dS'^T)_r is taken from dgc_r and added to the
-        // last row: in dg_t only the rows before t are left of it, and are added as such, since the difference of the two
-        // sums would have no digits where a chunk's own decay is small beside it (one token behind a strong gate).
-        auto four = [&](int m, int r) { return (red[(4 * m) * C + r] + red[(4 * m + 1) * C + r]) + (red[(4 * m + 2) * C + r] + red[(4 * m + 3) * C + r]); };
-        float d[2], th[2], bsum[2];
+      if (warp == 0 || warp == 2) {  // two of the warps whose product above was the shorter: rows 2 lane, 2 lane + 1 of dg and dbeta
+        auto add = [](float2 x, float2 y) { return make_float2(x.x + y.x, x.y + y.y); };
+        auto pair = [&](const float* x) { return *reinterpret_cast<const float2*>(x + 2 * lane); };
+        auto four = [&](const float* x) { return add(add(pair(x), pair(x + C)), add(pair(x + 2 * C), pair(x + 3 * C))); };
+        const float2 b = pair(rf + R::fBeta), u = four(red + 8 * C);
+        float2 out;
+        if (warp == 0) {
+          // dgc; then the suffix sums.  l_r k_r . (V' dS'^T)_r is taken from dgc_r and added to the last row: in dg_t only
+          // the rows before t are left of it, and are added as such, since the difference of the two sums would have no
+          // digits where a chunk's own decay is small beside it (one token behind a strong gate).
+          const float2 th = four(red + 4 * C), cols = four(col), r0 = four(red), ra = add(pair(reda), pair(reda + 2 * C));
+          const float d[2] = {ra.x + r0.x + b.x * u.x - cols.x, ra.y + r0.y + b.y * u.y - cols.y};
+          const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f) * rf[R::fScal + kScalGl];
+          float suf = d[0] + d[1], pre = th.x + th.y;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 2 * lane + e;
-          const float u = four(2, r);
-          const float cols = (col[r] + col[C + r]) + (col[2 * C + r] + col[3 * C + r]);
-          th[e] = four(1, r);
-          d[e] = (reda[r] + reda[2 * C + r]) + four(0, r) + rf[R::fBeta + r] * u - cols;
-          bsum[e] = (reda[C + r] + reda[3 * C + r]) + (reda[4 * C + r] + reda[5 * C + r]) + u;
-        }
-        const float dsum = warp_sum(lane < 16 ? dots[lane] : 0.f) * rf[R::fScal + kScalGl];
-        float suf = d[0] + d[1], pre = th[0] + th[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float y = __shfl_down_sync(0xffffffffu, suf, o), z = __shfl_up_sync(0xffffffffu, pre, o);
-          if (lane + o < 32) suf += y;
-          if (lane >= o) pre += z;
-        }
-        float beyond = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
-        if (lane == 31) beyond = 0.f;
-        if (lane == 0) before = 0.f;
-        const float dg[2] = {suf + (before + dsum), beyond + d[1] + (before + th[0] + dsum)};
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (2 * lane + e < rows) {
-            const size_t at = (size_t)(c0 + 2 * lane + e) * a.nv + h;
-            static_cast<bf16*>(a.dg)[at] = __float2bfloat16_rn(dg[e]);
-            static_cast<bf16*>(a.dbeta)[at] = __float2bfloat16_rn(bsum[e]);
+          for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_down_sync(0xffffffffu, suf, o), z = __shfl_up_sync(0xffffffffu, pre, o);
+            if (lane + o < 32) suf += y;
+            if (lane >= o) pre += z;
           }
+          float beyond = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
+          if (lane == 31) beyond = 0.f;
+          if (lane == 0) before = 0.f;
+          out = make_float2(suf + (before + dsum), beyond + d[1] + (before + th.x + dsum));
+        } else {
+          // V' = diag(b) (V - diag(e) K S - Kd V'), so dbeta_r = dX_r . V'_r / b_r: no difference of large terms where keys
+          // repeat.  A small b_r leaves V'_r few digits beside the tile's largest: there, and for 0, the terms one by one
+          const float2 xv = pair(reda + 6 * C), sum = add(add(add(pair(reda + C), pair(reda + 3 * C)), add(pair(reda + 4 * C), pair(reda + 5 * C))), u);
+          out = make_float2(b.x >= 0x1p-10f ? __fdividef(xv.x, b.x) : sum.x, b.y >= 0x1p-10f ? __fdividef(xv.y, b.y) : sum.y);
+        }
+        bf16* dst = static_cast<bf16*>(warp == 0 ? a.dg : a.dbeta) + (size_t)(c0 + 2 * lane) * a.nv + h;
+        if (2 * lane < rows) dst[0] = __float2bfloat16_rn(out.x);
+        if (2 * lane + 1 < rows) dst[a.nv] = __float2bfloat16_rn(out.y);
       }
     }
     if (quit) break;

@@ -182,3 +182,23 @@ def test_keys_that_repeat(gdn, io, kernel, dk, kind, lo, hi, by):
     sum to: 1 + 1 where beta <= 1; 1 + 2 (1 + 1/2 + 1/4 + ...) = 5 for beta evenly in [1, 2]; and where nothing falls off,
     64 independent roundings of entries of 2: 2 sqrt(64)."""
     check(gdn, near(kind, lo, hi, dk, io), (128,), io, kernel, ("dq", "dk", "dv", "ds0"), by=by)
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("kind", ["repeated", "near"])
+@pytest.mark.parametrize("lo,hi", [(0.0, 1.0), (0.9, 1.0)])
+def test_beta_gradients_where_keys_repeat(gdn, io, kernel, dk, kind, lo, hi):
+    """dbeta_r is the product of what the token writes and of the gradient of that, V' and dX: each may show its roundings
+    twice (see above), and the largest element need not be where the terms are large, so the eleven are taken one by one:
+    2 * 11 * 2^-11, 5.5 times the tolerance of independent ones."""
+    check(gdn, near(kind, lo, hi, dk, io), (128,), io, kernel, ("dbeta",), by=5.5)
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+def test_beta_gradients_at_and_near_zero(gdn, io, kernel):
+    """Of tokens that write nothing, or next to nothing, beside tokens that do."""
+    x = make((100,), 1, 2, 128, 64, io, s0=True, ds=True)
+    x["beta"][::3] = 0.0
+    x["beta"][1::3] = 10.0 ** -torch.linspace(1, 12, x["beta"][1::3].shape[0])[:, None]
+    check(gdn, x, (100,), io, kernel, ("dbeta",))
