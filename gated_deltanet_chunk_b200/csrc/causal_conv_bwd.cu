@@ -329,6 +329,10 @@ __global__ void __launch_bounds__(kThreads, Io<IO>::kPerSm) conv_bwd_kernel(Conv
           ++n;
           seq_bounds(a, n, s0, s1);
         }
+        if (t0 + i >= s1) {  // of no sequence, and neither is what follows (inconsistent cu_seqlens, already reported)
+          i = rows + 1;
+          break;
+        }
         enter();
 #pragma unroll
         for (int j = 0; j < H; ++j)
