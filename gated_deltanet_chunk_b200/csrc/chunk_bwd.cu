@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(BwdArgs a) {
         rf[R::fScal + kScalDo] = oinv;
       }
     }
-    invert_chunk(A, Y, warp, lane);
+    invert_chunk<false>(A, Y, warp, lane);
     {  // pairs of T, T diag(b) and P, each under one factor
       float2 t[2][2], tb[2][2];
       float top[3] = {0.f, 0.f, 0.f}, f[3], inv[3];

@@ -50,24 +50,33 @@ static inline dim3 slot_grid(int64_t slots, int nqk) {
   return dim3((unsigned int)nqk, (unsigned int)(slots < 65535 ? slots : 65535), (unsigned int)((slots + 65534) / 65535));
 }
 
+// x as hi + lo of TF32: rounded, within 2^-24 of x, or (kCut) cut off by masks, within 2^-21 and always towards zero.
+// Cutting is what the kernels with fp16 operands do, which keep 11 bits of what comes of it: prepare takes 5 % less there.
+// For those with pairs it is too little: where keys repeat, the gradients' errors were three to eight times as large.
+template <bool kCut>
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = ptx::to_tf32(x);
-  lo = ptx::to_tf32(x - __uint_as_float(hi));
+  if constexpr (kCut) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+  } else {
+    hi = ptx::to_tf32(x);
+    lo = ptx::to_tf32(x - __uint_as_float(hi));
+  }
 }
 
 // acc (a 16 x 8 tile) += A[16 x K] B[K x 8] over k in [k0, k1), one warp; a(m, k) and b(k, n) read the operands'
 // elements, which are split into hi + lo: three MMAs, whose 8 terms are added in fp32, since an MMA truncates as it adds.
-template <typename FA, typename FB>
+template <bool kCut, typename FA, typename FB>
 __device__ __forceinline__ void warp_gemm(float (&acc)[4], int k0, int k1, FA a, FB b, int g, int t) {
 #pragma unroll 2
   for (int kk = k0; kk < k1; kk += 8) {
     uint32_t ah[4], al[4], bh[2], bl[2];
-    split_tf32(a(g, kk + t), ah[0], al[0]);
-    split_tf32(a(g + 8, kk + t), ah[1], al[1]);
-    split_tf32(a(g, kk + t + 4), ah[2], al[2]);
-    split_tf32(a(g + 8, kk + t + 4), ah[3], al[3]);
-    split_tf32(b(kk + t, g), bh[0], bl[0]);
-    split_tf32(b(kk + t + 4, g), bh[1], bl[1]);
+    split_tf32<kCut>(a(g, kk + t), ah[0], al[0]);
+    split_tf32<kCut>(a(g + 8, kk + t), ah[1], al[1]);
+    split_tf32<kCut>(a(g, kk + t + 4), ah[2], al[2]);
+    split_tf32<kCut>(a(g + 8, kk + t + 4), ah[3], al[3]);
+    split_tf32<kCut>(b(kk + t, g), bh[0], bl[0]);
+    split_tf32<kCut>(b(kk + t + 4, g), bh[1], bl[1]);
     float d[4] = {}, e[4] = {};
     ptx::mma_tf32_16x8x8(e, al, bh);
     ptx::mma_tf32_16x8x8(d, ah, bh);
@@ -128,6 +137,7 @@ __device__ __forceinline__ void cumsum_chunk(float* x, float* low, int lane) {
 // diagonal blocks by forward substitution in fp32 (a warp per block, a column
 // per lane), then T10 = T11 A10 T00 for blocks of 16 and of 32.  Y: [C / 2][TP]
 // scratch.  Zeros above the diagonal are written; the unit diagonal is stored.
+template <bool kCut>
 __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int lane) {
   if (warp < C / 16 && lane < 16) {
     float* blk = A + (16 * warp) * TP + 16 * warp;
@@ -155,7 +165,7 @@ __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int l
       const float* a10 = A + (base + s + 16 * rb) * TP + base;
       const float* t00 = A + base * TP + base + c0;
       float acc[4] = {};
-      warp_gemm(acc, c0, s, [&](int m, int k) { return a10[m * TP + k]; }, [&](int k, int n) { return t00[k * TP + n]; }, g, t);
+      warp_gemm<kCut>(acc, c0, s, [&](int m, int k) { return a10[m * TP + k]; }, [&](int k, int n) { return t00[k * TP + n]; }, g, t);
 #pragma unroll
       for (int e = 0; e < 4; ++e) Y[(p * s + 16 * rb + g + 8 * (e >> 1)) * TP + c0 + 2 * t + (e & 1)] = acc[e];
     }
@@ -164,7 +174,7 @@ __device__ __forceinline__ void invert_chunk(float* A, float* Y, int warp, int l
       const float* t11 = A + (base + s + 16 * rb) * TP + base + s;
       const float* yp = Y + p * s * TP + c0;
       float acc[4] = {};
-      warp_gemm(acc, 0, 16 * rb + 16, [&](int m, int k) { return t11[m * TP + k]; }, [&](int k, int n) { return yp[k * TP + n]; }, g, t);
+      warp_gemm<kCut>(acc, 0, 16 * rb + 16, [&](int m, int k) { return t11[m * TP + k]; }, [&](int k, int n) { return yp[k * TP + n]; }, g, t);
 #pragma unroll
       for (int e = 0; e < 4; ++e) A[(base + s + 16 * rb + g + 8 * (e >> 1)) * TP + base + c0 + 2 * t + (e & 1)] = acc[e];
     }

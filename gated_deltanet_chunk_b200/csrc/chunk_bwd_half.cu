@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
         rf[R::fScal + kScalDo] = oinv;
       }
     }
-    bwd::invert_chunk(A, Y, warp, lane);
+    bwd::invert_chunk<true>(A, Y, warp, lane);
     float bs, binv;  // beta's factor: T beta is at most 2^8 times a half of it
     pow2_factor(fmaxf(tops[24], tops[25]), bs, binv);
     bs *= 0.5f;
