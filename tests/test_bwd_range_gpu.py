@@ -202,3 +202,20 @@ def test_beta_gradients_at_and_near_zero(gdn, io, kernel):
     x["beta"][::3] = 0.0
     x["beta"][1::3] = 10.0 ** -torch.linspace(1, 12, x["beta"][1::3].shape[0])[:, None]
     check(gdn, x, (100,), io, kernel, ("dbeta",))
+
+
+@pytest.mark.parametrize("io,kernel", PATHS)
+def test_raw_gates_of_every_rate(gdn, io, kernel):
+    """a and b in the places of g and beta: rates up to 16, so that heads forget in one token or in thousands."""
+    lens = (70, 129, 1)
+    x = make(lens, 4, 8, 128, 128, io, s0=True, ds=True)
+    r = torch.Generator().manual_seed(9)
+    a, b, dt = torch.randn(200, 8, generator=r), torch.randn(200, 8, generator=r), torch.randn(8, generator=r) - 1
+    A_log = torch.log(torch.tensor([0.001, 0.01, 0.1, 0.5, 1.0, 4.0, 10.0, 16.0]))
+    x["g"], x["beta"] = a, b
+    got = run(gdn, x, lens, kernel=kernel, A_log=A_log.cuda(), dt_bias=dt.cuda())
+    assert gdn.device_status() == 0
+    g, beta = G.gate(a.double(), b.double(), A_log.double(), dt.double())
+    want = G.rule_grads(x["q"], x["k"], x["v"], g, beta, x["s0"], x["dout"], x["ds"], lens)
+    for name, y, z in zip(NAMES[:5], got, want):
+        close(name, y, z, io, kernel)
