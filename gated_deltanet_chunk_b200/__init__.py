@@ -503,6 +503,11 @@ def chunk_bwd(q, k, v, g, beta, dout, initial_state=None, d_final_state=None, cu
     gradients in the dtype of q; d_initial_state is None unless an initial state was
     given or it was asked for.
 
+    bf16 tensors with qk_l2norm need g <= 0 and 0 <= beta <= 2 unless ``kernel="simt"``: this
+    is not looked at before the launch, a gate outside leaves the results undefined, and
+    ``device_status()`` then returns GDN_ERR_GATE.  ``kernel="simt"`` takes any finite gate and
+    holds operands in twice as many bits.
+
     Of this call and the training calls below: tensors of another type, shape or device
     than stated, or that are not contiguous, are refused (``GdnError``, GDN_ERR_SHAPE).
     The call runs on the tensors' device; with ``stream=`` it belongs to that stream as

@@ -44,18 +44,21 @@
 //      are summed in registers, in a fixed order.
 // Every operand of a product is a pair hi + lo of fp16, scaled by a power of two that
 // a row or a tile shares, and a product is three MMAs: within about 2^-22 of its value.
+// Rows of W and the columns of V' diag(kw), dV' diag(wr) and diag(s e) dO have factors
+// of their own: they take any number of binades over a chunk, with the decay.
 // Pairs are formed once, where a tile is made, and stand in the caller's workspace as
 // images that one bulk copy brings into shared memory.  An MMA of fp16 takes twice the
 // terms of one of TF32, and ldmatrix feeds it; with pairs of TF32 split as they were
 // loaded the three kernels took 0.56, 2.26 and 1.25 ms for 4 x 4096 tokens, 4 / 8 heads
-// of 128, against 0.26, 0.46 and 0.46 now (1 x 256 tokens, one head of 64: 16, 18 and
+// of 128, against 0.27, 0.47 and 0.46 now (1 x 256 tokens, one head of 64: 16, 17 and
 // 14 us).  Partial sums of one MMA step (16 terms) are added in fp32: the MMA itself
 // truncates, and over long sums that showed (3.8e-6 relative against 64 bits; now
-// 3.1e-7).  Only the inverse's 16 x 16 blocks split TF32.
+// 2.7e-7).  Only the inverse's blocks off its 16 x 16 diagonal split TF32.  The sums of
+// gates are pairs of fp32, so that decays do not lose digits behind a strong one.
 //
 // Bound by latency: prepare and gradients run one block per SM in 7 waves and issue in
 // a third of the cycles (the tensor pipe is busy in 16 and 24 %); states has 128
-// blocks, whose 64 chunks wait for one another, 13,000 cycles each, of which the MMAs
+// blocks, whose 64 chunks wait for one another, 13,500 cycles each, of which the MMAs
 // are 4,600.
 
 #include "chunk_bwd.cuh"

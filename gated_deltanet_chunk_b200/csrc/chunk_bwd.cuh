@@ -50,7 +50,7 @@ static inline dim3 slot_grid(int64_t slots, int nqk) {
   return dim3((unsigned int)nqk, (unsigned int)(slots < 65535 ? slots : 65535), (unsigned int)((slots + 65534) / 65535));
 }
 
-// x as hi + lo of TF32: rounded, within 2^-24 of x, or (kCut) cut off by masks, within 2^-21 and always towards zero.
+// x as hi + lo of TF32: rounded, within 2^-22 of x, or (kCut) cut off by masks, within 2^-21 and always towards zero.
 // Cutting is what the kernels with fp16 operands do, which keep 11 bits of what comes of it: prepare takes 5 % less there.
 // For those with pairs it is too little: where keys repeat, the gradients' errors were three to eight times as large.
 template <bool kCut>

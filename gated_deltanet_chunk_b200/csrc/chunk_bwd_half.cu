@@ -1,28 +1,34 @@
 // chunk_bwd_half.cu -- gradients of the chunked gated delta rule for bf16 tensors.
 //
 // The mathematics, the notation and the three kernels are those of chunk_bwd.cu.
-// Here every product is one MMA in fp16 with fp32 accumulation (mma.sync.m16n8k16;
-// tcgen05 in the states kernel, where the next chunk waits for it): an operand is an fp16 number (11 significant bits) times a power
-// of two that its tile, row or column shares, chosen so that the largest
-// magnitude is in [2^7, 2^8) or bounded by it.  So
+// Here a product is one MMA in fp16 with fp32 accumulation (mma.sync.m16n8k16; tcgen05 in
+// the states kernel, where the next chunk waits for it): an operand is an fp16 number (11
+// significant bits) times a power of two that its tile, row or column shares, chosen so that
+// the largest magnitude is in [2^7, 2^8) or bounded by it.  So
 //   - q, k, v and dout, which have 8 significant bits, are exact,
-//   - what is formed on the way (T, W, S, V', dS', ...) is rounded by at most
-//     2^-12 of its value, or 2^-33 of its tile's largest: an eighth of the bf16
-//     rounding that the outputs get, at the cost of one MMA, where bf16 operands
-//     of that accuracy would need two or three,
+//   - what is formed on the way (T, W, S, V', dS', ...) is rounded by at most 2^-11 of its
+//     value, or 2^-32 of its tile's largest: an eighth of the bf16 rounding that the outputs
+//     get, at the cost of one MMA, where bf16 operands of that accuracy would need two or
+//     three.  A gradient meets up to eleven of them, 2e-4 to 1.3e-3 of its largest element,
+//   - W's operand T diag(b e), whose terms cancel where keys repeat, is a pair hi + lo,
 //   - 2^8 against fp16's 65504 leaves room for what follows from a bounded sum.
-// The recurrences themselves (S and dS), the cumsums, the inverse, the decays and
-// every sum are fp32.
+// The recurrences themselves (S and dS), the cumsums, the decays and every sum are fp32; the
+// inverse is fp32 in its 16 x 16 diagonal blocks and products of TF32 pairs off them.
 //
-// Bounds that the fixed factors of two use (they hold for 0 <= beta <= 2, g <= 0
-// and normalised q, k; the prepare kernel checks the gates, and other calls take
-// chunk_bwd.cu): decays are at most 1, |T| <= 2 (row r of T is beta_r k_r^T times
-// a product of contractions, times k_i), |W_r| <= beta_r e_r, |q_r . k_i| <= 1.
+// Bounds that the factors of two use (they hold for 0 <= beta <= 2, g <= 0 and normalised q,
+// k; the prepare kernel reports gates outside, where the results are undefined): decays are
+// at most 1, |T_ri| <= 2 (row r of T is beta_r k_r^T times a product of contractions, times
+// k_i), |W_r| <= beta_r e_r, |q_r . k_i| <= 1.  T and P have a fixed
+// factor, since T's diagonal is 1 and P's products are of unit rows.  Factors that depend on
+// the gates follow them: e takes any number of binades over a chunk and from one to the
+// next, beta any value, so W has a power of two for every row, T diag(b), diag(qe) dO,
+// V' diag(kw) and dV' diag(wr) one of their largest (6 % of prepare's time for diag(qe) dO, 4 to
+// 10 % of states' for its two, against fixed ones, which lost all digits behind strong gates).
 //
 // Measured for 2 x 32768 tokens, 16 / 32 heads of 128, as prepare + states + gradients:
-// 1.37 + 1.17 + 2.48 ms (0.35 + 0.28 + 0.65 ms for 15,928 packed tokens).  What they read
+// 1.51 + 1.29 + 2.48 ms (0.39 + 0.30 + 0.65 ms for 15,928 packed tokens).  What they read
 // and write, the tiles that they pass on included, is 5.1 + 6.5 + 6.1 GB, 2.7 ms at the
-// copy bandwidth: states is near it (85 %), prepare at 57 % (a block's loads, its
+// copy bandwidth: states is nearest (77 %), prepare at 52 % (a block's loads, its
 // inverse and its stores wait for one another, and two blocks per SM is what shared
 // memory holds), gradients at 37 % (17,000 cycles a v-head, of which the MMAs are
 // 6,000: the element-wise parts between them and two barriers are the rest).  Passing
@@ -551,8 +557,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) prepare_half_kernel(BwdArgs a
 // The state's image has one factor, joined over the block, and so has the image of V'; that of dV' has one a row.  Both
 // are written while the second product runs.
 // A chunk waits for the one before it, and a thread issues an MMA every 90 to 130 cycles: so N is all of Dk, x is
-// two sums over half of Dk from two warps, and z = (diag(qe) dO)^T Q comes from a third (1.15 ms for 2 x 32768 tokens
-// and 32 heads of 128; 1.54 with one warp and N = 64, 1.51 with a ninth warp for all of them; 2.11 with warp MMAs).
+// two sums over half of Dk from two warps, and z = (diag(qe) dO)^T Q comes from a third (2 x 32768 tokens and 32
+// heads of 128, while its operands had fixed factors: 1.15 ms; 1.54 with one warp and N = 64, 1.51 with a ninth warp for all
+// of them; 2.11 with warp MMAs).
 
 constexpr int kStateThreads = 256;
 
@@ -1303,7 +1310,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_half_kernel(BwdArgs a) 
 #pragma unroll
         for (int e = 0; e < 2; ++e) put_row(s_v[e], reda + (4 + (w8 >> 2)) * C + r0 + 8 * e, ln.t);
       }
-      ptx::fence_proxy_async_smem();  // V' was rewritten in place before a copy comes over it
+      ptx::fence_proxy_async_smem();  // the tiles' generic reads come before the copies over them
       __syncthreads();
       if (tid == 0 && (!last || next < items)) fetch_rest(last ? next : item, last ? (int)(next % a.nqk) * group : h + 1);
       // ---- 4.

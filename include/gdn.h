@@ -394,14 +394,21 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
  *   p                as gdn_chunk_fwd
  *
  * Kernels: with bf16 io and qk_l2norm, GDN_KERNEL_AUTO and GDN_KERNEL_TC use fp16
- * operands (each rounded by at most 2^-12 of its value, under powers of two shared by
- * tiles) with fp32 sums and states, and need g <= 0 and 0 <= beta <= 2: a gate outside
- * leaves the results undefined and is reported as GDN_ERR_GATE.  GDN_KERNEL_SIMT, fp32
- * io and calls without qk_l2norm hold each operand as a pair of fp16 numbers under such
- * a power of two: within 2^-22 of its value, or 2^-32 of the largest of its tile (64
- * tokens of one head, 64 columns of a state; one row of q and k), if that is more.  They take any
- * finite g and beta.  GDN_KERNEL_TC is rejected for the latter two kinds of call.  The
+ * operands with fp32 sums and states, and need g <= 0 and 0 <= beta <= 2: a gate outside
+ * leaves the results undefined and is reported as GDN_ERR_GATE (such calls take
+ * GDN_KERNEL_SIMT; AUTO does not look at the gates).  An operand is rounded by at most
+ * 2^-11 of its value, or 2^-32 of the largest of its tile, if that is more; powers of two
+ * that rows or tiles share follow each chunk's own factors.  A gradient meets up to eleven
+ * of them: errors measure 2e-4 to 1.3e-3 of a head's largest element with random keys, up
+ * to 4e-3 (dbeta 9e-3) where keys repeat through a chunk and beta is at most 1, so that the
+ * terms of T and W cancel, and up to 1e-2 (dbeta 2e-2, dg 6e-2) with beta up to 2.
+ * GDN_KERNEL_SIMT, fp32 io and calls without qk_l2norm hold each operand as a pair of fp16
+ * numbers: within 2^-22 of its value, or 2^-32 of the largest of its tile (64 tokens of
+ * one head, 64 columns of a state; one row of q, k and W), if that is more.  They take
+ * any finite g and beta.  GDN_KERNEL_TC is rejected for the latter two kinds of call.  The
  * workspace size depends on that choice.
+ * In all of them a gate below -105 (less the chunk's positive ones), whose decay is 0 in
+ * fp32, counts as that much, also the type's lowest value and -infinity.
  *
  * No output may overlap an input, another output or the workspace.  Tokens that
  * cu_seqlens leaves outside every sequence are not written.  Zero-length
@@ -421,7 +428,7 @@ int gdn_chunk_bwd(const void *q, const void *k, const void *v,
 /*
  * Bytes of workspace that gdn_chunk_bwd needs, or a negative gdn_status_t.  Host only.
  * About (total_tokens / 64 + num_seqs) * Nv records of 157 KB with fp16 operands and
- * 315 KB otherwise at Dk = Dv = 128 (67 and 133 KB at 64): many sequences much shorter
+ * 315 KB otherwise at Dk = Dv = 128 (67 and 134 KB at 64): many sequences much shorter
  * than 64 tokens take a record each.
  */
 int64_t gdn_chunk_bwd_workspace(int32_t num_seqs, int64_t total_tokens, const gdn_params_t *p);
