@@ -407,6 +407,9 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
  * one head, 64 columns of a state; one row of q, k and W), if that is more.  They take
  * any finite g and beta.  GDN_KERNEL_TC is rejected for the latter two kinds of call.  The
  * workspace size depends on that choice.
+ * So what lies far below the largest of its chunk and head (the share of tokens that a
+ * strong gate cuts off from every token with a gradient or a value, or whose beta is near 0
+ * beside others) has fewer digits: full ones down to about 2^-20 of it, none at 2^-32.
  * In all of them a gate below -105 (less the chunk's positive ones), whose decay is 0 in
  * fp32, counts as that much, also the type's lowest value and -infinity.
  *
