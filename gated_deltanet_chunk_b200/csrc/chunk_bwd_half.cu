@@ -18,12 +18,12 @@
 // Bounds that the factors of two use (they hold for 0 <= beta <= 2, g <= 0 and normalised q,
 // k; the prepare kernel reports gates outside, where the results are undefined): decays are
 // at most 1, |T_ri| <= 2 (row r of T is beta_r k_r^T times a product of contractions, times
-// k_i), |W_r| <= beta_r e_r, |q_r . k_i| <= 1.  T and P have a fixed
-// factor, since T's diagonal is 1 and P's products are of unit rows.  Factors that depend on
-// the gates follow them: e takes any number of binades over a chunk and from one to the
-// next, beta any value, so W has a power of two for every row, T diag(b), diag(qe) dO,
-// V' diag(kw) and dV' diag(wr) one of their largest (6 % of prepare's time for diag(qe) dO, 4 to
-// 10 % of states' for its two, against fixed ones, which lost all digits behind strong gates).
+// k_i), |W_r| <= beta_r e_r, |q_r . k_i| <= 1.  T and P have a fixed factor, since T's
+// diagonal is 1 and P's products are of unit rows.  Factors that depend on the gates follow
+// them: e takes any number of binades over a chunk and from one to the next, beta any value,
+// so W has a power of two for every row, T diag(b), diag(qe) dO, V' diag(kw) and dV' diag(wr)
+// one of their largest (6 % of prepare's time for diag(qe) dO, 4 to 10 % of states' for its
+// two, against fixed ones, which lost all digits behind strong gates).
 //
 // Measured for 2 x 32768 tokens, 16 / 32 heads of 128, as prepare + states + gradients:
 // 1.51 + 1.29 + 2.48 ms (0.39 + 0.30 + 0.65 ms for 15,928 packed tokens).  What they read

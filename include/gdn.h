@@ -409,7 +409,7 @@ int gdn_qkv_conv_update(const void *mixed_qkv, const float *weight, const float 
  * workspace size depends on that choice.
  * So what lies far below the largest of its chunk and head (the share of tokens that a
  * strong gate cuts off from every token with a gradient or a value, or whose beta is near 0
- * beside others) has fewer digits: full ones down to about 2^-20 of it, none at 2^-32.
+ * beside others) has fewer digits: 11 bits at 2^-20 of it in either kind, none at 2^-32.
  * In all of them a gate below -105 (less the chunk's positive ones), whose decay is 0 in
  * fp32, counts as that much, also the type's lowest value and -infinity.
  *
